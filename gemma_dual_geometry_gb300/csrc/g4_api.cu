@@ -622,6 +622,349 @@ g4_status g4_attn_out_residual(const void* ao, int32_t M, int32_t K, const void*
   return cuda_status(g4::launch_gemm_tc(a, ao, w_o, static_cast<cudaStream_t>(stream)), "o_proj launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+bool kv4_block_size(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+// check_params, and what the 4-bit cache adds to it.
+g4_status kv4_check_params(const g4_layer_params* p) {
+  const g4_status st = check_params(p);
+  if (st != G4_OK) return st;
+  if (p->dtype != G4_BF16) return fail(G4_ERR_UNSUPPORTED, "the 4-bit cache serves bf16 layers only");
+  return G4_OK;
+}
+
+// Resolves the pool a layer reads and checks that it matches the layer.
+g4_status kv4_resolve_src(const g4_layer_params* p, const g4_kv4_pool* pools, int n_layers, int layer,
+                          const g4_kv4_pool** out) {
+  if (pools == nullptr) return fail(G4_ERR_INVALID_ARG, "pools is NULL");
+  if (layer < 0 || layer >= n_layers) return fail(G4_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, n_layers);
+  const int src = p->kv_share_src < 0 ? layer : p->kv_share_src;
+  if (src >= n_layers) return fail(G4_ERR_INVALID_ARG, "kv_share_src %d outside [0, %d)", src, n_layers);
+  const g4_kv4_pool* c = &pools[src];
+  if (c->data == nullptr) return fail(G4_ERR_INVALID_ARG, "pool of layer %d (read by layer %d) has NULL data", src, layer);
+  if (c->layer_type != p->layer_type || c->head_dim != p->head_dim || c->n_kv_heads != p->n_kv_heads)
+    return fail(G4_ERR_SHARE_MISMATCH,
+                "layer %d (type %d, head_dim %d, n_kv %d) cannot read the pool of layer %d (type %d, head_dim %d, n_kv %d)",
+                layer, p->layer_type, p->head_dim, p->n_kv_heads, src, c->layer_type, c->head_dim, c->n_kv_heads);
+  if (!kv4_block_size(c->block_size))
+    return fail(G4_ERR_UNSUPPORTED, "pool of layer %d: block_size %d not supported (16, 32, 64, 128)", src, c->block_size);
+  if (c->n_blocks < 1 || static_cast<long long>(c->n_blocks) * c->block_size > 0x7fffffffLL)
+    return fail(G4_ERR_INVALID_ARG, "pool of layer %d: %d blocks of %d positions outside [1, 2^31 - 1] positions", src,
+                c->n_blocks, c->block_size);
+  if (c->k_exp < -32 || c->k_exp > 32)
+    return fail(G4_ERR_INVALID_ARG, "pool of layer %d: k_exp %d outside [-32, 32]", src, c->k_exp);
+  if (!aligned16(c->data)) return fail(G4_ERR_INVALID_ARG, "pool of layer %d is not 16-byte aligned", src);
+  *out = c;
+  return G4_OK;
+}
+
+// The table's width against a pool's block size (max_blocks * block_size is a length).
+g4_status kv4_check_table(const void* table, int max_blocks, int block_size) {
+  if (table == nullptr) return fail(G4_ERR_INVALID_ARG, "block_table must be non-NULL");
+  if (max_blocks < 1 || static_cast<long long>(max_blocks) * block_size > 0x7fffffffLL)
+    return fail(G4_ERR_INVALID_ARG, "max_blocks %d outside [1, (2^31 - 1) / %d]", max_blocks, block_size);
+  return G4_OK;
+}
+
+// The bf16 rows that a prefill's keys are laid out in: per sequence, and the bytes of K (as of V).
+int kv4_prefill_rows(const g4_layer_params* p, int T, int max_seq_len) {
+  if (p->layer_type != G4_SLIDING) return max_seq_len;
+  const long long rows = static_cast<long long>(T) + p->window - 1;
+  return rows < max_seq_len ? static_cast<int>(rows) : max_seq_len;
+}
+size_t kv4_prefill_kv_bytes(const g4_layer_params* p, int B, int T, int max_seq_len) {
+  return static_cast<size_t>(B) * p->n_kv_heads * kv4_prefill_rows(p, T, max_seq_len) * p->head_dim * 2;
+}
+size_t kv4_prefill_head_bytes(int B) { return (static_cast<size_t>(B) * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+extern "C" {
+
+g4_status g4_kv4_assign_blocks(int32_t B, int32_t T, int32_t block_size, int32_t n_blocks, int32_t max_blocks,
+                               const int32_t* old_lens, const int32_t* new_lens, int32_t* free_blocks,
+                               const int32_t* free_count, int32_t* block_table, int32_t* lens_out,
+                               int32_t* free_count_out, int32_t* positions, int32_t* slots, void* stream) {
+  if (B < 0 || T < 0) return fail(G4_ERR_INVALID_ARG, "B %d and T %d must be >= 0", B, T);
+  if (!kv4_block_size(block_size))
+    return fail(G4_ERR_UNSUPPORTED, "block_size %d not supported (16, 32, 64, 128)", block_size);
+  if (n_blocks < 1 || static_cast<long long>(n_blocks) * block_size > 0x7fffffffLL)
+    return fail(G4_ERR_INVALID_ARG, "%d blocks of %d positions outside [1, 2^31 - 1] positions", n_blocks, block_size);
+  if (max_blocks < 1) return fail(G4_ERR_INVALID_ARG, "max_blocks %d must be >= 1", max_blocks);
+  if (B > g4::kKv4MaxBatch)
+    return fail(G4_ERR_UNSUPPORTED, "B %d exceeds %d sequences", B, g4::kKv4MaxBatch);
+  if (static_cast<long long>(B) * max_blocks > 0x7fffffffLL || static_cast<long long>(B) * T > 0x7fffffffLL)
+    return fail(G4_ERR_INVALID_ARG, "B * max_blocks and B * T must not exceed 2^31 - 1");
+  if (old_lens == nullptr || new_lens == nullptr || free_blocks == nullptr || free_count == nullptr ||
+      block_table == nullptr || lens_out == nullptr || free_count_out == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "lengths, free list, table and their outputs must be non-NULL");
+  if (T > 0 && (positions == nullptr || slots == nullptr))
+    return fail(G4_ERR_INVALID_ARG, "positions and slots must be non-NULL");
+  // (B = 0 still passes the count on)
+  g4::Kv4AssignArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = B;
+  a.T = T;
+  a.block_shift = log2_of(block_size);
+  a.n_blocks = n_blocks;
+  a.max_blocks = max_blocks;
+  a.old_lens = old_lens;
+  a.new_lens = new_lens;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.table = block_table;
+  a.lens_out = lens_out;
+  a.count_out = free_count_out;
+  a.positions = positions;
+  a.slots = slots;
+  return cuda_status(g4::launch_kv4_assign(a, static_cast<cudaStream_t>(stream)), "block assignment launch");
+}
+
+g4_status g4_kv4_append_normrope(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
+                                 int32_t layer, const void* q_in, const void* k_in, const void* v_in,
+                                 const float* q_norm_w, const float* k_norm_w, const int32_t* positions,
+                                 const int32_t* slots, int32_t B, int32_t T, void* q_out, void* stream) {
+  g4_status st = kv4_check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0 || T < 0) return fail(G4_ERR_INVALID_ARG, "B %d and T %d must be >= 0", B, T);
+  if (q_in == nullptr || q_out == nullptr || q_norm_w == nullptr || positions == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q_in, q_out, q_norm_w and positions must be non-NULL");
+  if (!aligned16(q_in) || !aligned16(q_out) || !aligned16(q_norm_w))
+    return fail(G4_ERR_INVALID_ARG, "q_in, q_out and q_norm_w must be 16-byte aligned");
+  const bool shared = params->kv_share_src >= 0;
+  g4::Kv4AppendArgs a;
+  memset(&a, 0, sizeof(a));
+  if (shared) {
+    if (k_in != nullptr || v_in != nullptr || k_norm_w != nullptr)
+      return fail(G4_ERR_INVALID_ARG, "layer %d shares the pool of layer %d: k_in, v_in and k_norm_w must be NULL",
+                  layer, params->kv_share_src);
+    if (layer < 0 || layer >= n_layers) return fail(G4_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, n_layers);
+  } else {
+    if (k_in == nullptr || v_in == nullptr || k_norm_w == nullptr || slots == nullptr)
+      return fail(G4_ERR_INVALID_ARG, "layer %d owns its pool: k_in, v_in, k_norm_w and slots must be non-NULL", layer);
+    if (!aligned16(k_in) || !aligned16(v_in) || !aligned16(k_norm_w))
+      return fail(G4_ERR_INVALID_ARG, "k_in, v_in and k_norm_w must be 16-byte aligned");
+    const g4_kv4_pool* c = nullptr;
+    st = kv4_resolve_src(params, pools, n_layers, layer, &c);
+    if (st != G4_OK) return st;
+    a.data = static_cast<uint8_t*>(c->data);
+    a.n_slots = c->n_blocks * c->block_size;
+    a.block_shift = log2_of(c->block_size);
+    a.k_mul = static_cast<float>(ldexp(1.0, -c->k_exp));
+    a.k_in = k_in;
+    a.v_in = v_in;
+    a.k_w = k_norm_w;
+    a.slots = slots;
+  }
+  const long long tokens = static_cast<long long>(B) * T;
+  if (tokens > 0x7fffffffLL) return fail(G4_ERR_INVALID_ARG, "B * T exceeds 2^31 - 1");
+  if (tokens == 0) return ok();
+  a.q_in = q_in;
+  a.q_w = q_norm_w;
+  a.positions = positions;
+  a.q_out = q_out;
+  a.tokens = static_cast<int>(tokens);
+  a.H = params->n_heads;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.eps = params->eps;
+  const int nrows = a.H + (shared ? 0 : 2 * a.Hkv);
+  // small launches split a token's rows over CTAs
+  a.rows_per_cta = tokens >= 1024 ? nrows : 4;
+  const int half = a.hd / 2;
+  int n_rot = static_cast<int>(floor(static_cast<double>(a.hd) * static_cast<double>(params->rotary_fraction) / 2.0));
+  if (n_rot > half) n_rot = half;
+  a.n_rot = n_rot;
+  for (int j = 0; j < half; ++j)
+    a.inv_freq[j] = j < n_rot ? static_cast<float>(pow(static_cast<double>(params->theta), -2.0 * j / a.hd)) : 0.0f;
+  return cuda_status(g4::launch_kv4_append(a, static_cast<cudaStream_t>(stream)), "4-bit append launch");
+}
+
+g4_status g4_kv4_gather(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers, int32_t layer,
+                        const int32_t* block_table, int32_t max_blocks, const int32_t* start,
+                        const int32_t* seq_lens, int32_t B, int32_t rows, void* k_out, void* v_out, void* stream) {
+  g4_status st = kv4_check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0 || rows < 0) return fail(G4_ERR_INVALID_ARG, "B %d and rows %d must be >= 0", B, rows);
+  if (start == nullptr || seq_lens == nullptr || k_out == nullptr || v_out == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "start, seq_lens, k_out and v_out must be non-NULL");
+  if (!aligned16(k_out) || !aligned16(v_out))
+    return fail(G4_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  const g4_kv4_pool* c = nullptr;
+  st = kv4_resolve_src(params, pools, n_layers, layer, &c);
+  if (st != G4_OK) return st;
+  st = kv4_check_table(block_table, max_blocks, c->block_size);
+  if (st != G4_OK) return st;
+  if (B == 0 || rows == 0) return ok();
+  g4::Kv4GatherArgs a;
+  memset(&a, 0, sizeof(a));
+  a.data = static_cast<const uint8_t*>(c->data);
+  a.table = block_table;
+  a.start = start;
+  a.lens = seq_lens;
+  a.k = k_out;
+  a.v = v_out;
+  a.B = B;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.rows = rows;
+  a.max_blocks = max_blocks;
+  a.n_blocks = c->n_blocks;
+  a.block_shift = log2_of(c->block_size);
+  a.k_mul = static_cast<float>(ldexp(1.0, c->k_exp));
+  return cuda_status(g4::launch_kv4_gather(a, static_cast<cudaStream_t>(stream)), "4-bit gather launch");
+}
+
+size_t g4_kv4_decode_workspace_size(const g4_layer_params* params, int32_t B, int32_t max_seq_len) {
+  if (kv4_check_params(params) != G4_OK || B < 1 || max_seq_len < 1) return 0;
+  return g4::kv4_decode_plan(params->layer_type == G4_SLIDING ? params->window : 0, params->head_dim, params->n_heads,
+                             params->n_kv_heads, B, max_seq_len)
+      .ws_bytes;
+}
+
+g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
+                             int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,
+                             const int32_t* seq_lens, int32_t B, int32_t max_seq_len, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  g4_status st = kv4_check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0) return fail(G4_ERR_INVALID_ARG, "B %d must be >= 0", B);
+  if (q == nullptr || out == nullptr || seq_lens == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q, out and seq_lens must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(G4_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const g4_kv4_pool* c = nullptr;
+  st = kv4_resolve_src(params, pools, n_layers, layer, &c);
+  if (st != G4_OK) return st;
+  st = kv4_check_table(block_table, max_blocks, c->block_size);
+  if (st != G4_OK) return st;
+  if (max_seq_len < 1 || max_seq_len > max_blocks * c->block_size)
+    return fail(G4_ERR_CAPACITY, "max_seq_len %d outside [1, %d blocks of %d]", max_seq_len, max_blocks, c->block_size);
+  if (B == 0) return ok();
+  const int window = params->layer_type == G4_SLIDING ? params->window : 0;
+  const g4::Kv4DecodePlan plan =
+      g4::kv4_decode_plan(window, params->head_dim, params->n_heads, params->n_kv_heads, B, max_seq_len);
+  if (static_cast<long long>(B) * params->n_kv_heads * plan.nsplit > 0x7fffffffLL)
+    return fail(G4_ERR_INVALID_ARG, "B %d too large", B);
+  if (workspace_bytes < plan.ws_bytes)
+    return fail(G4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
+  if (plan.ws_bytes > 0 && (workspace == nullptr || !aligned16(workspace)))
+    return fail(G4_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
+  int* err = device_error_ptr();
+  if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
+  g4::Kv4DecodeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.data = static_cast<const uint8_t*>(c->data);
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.out = out;
+  a.err = err;
+  a.B = B;
+  a.H = params->n_heads;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.max_blocks = max_blocks;
+  a.n_blocks = c->n_blocks;
+  a.block_shift = log2_of(c->block_size);
+  a.window = window;
+  a.len_cap = max_seq_len;
+  a.chunk = plan.chunk;
+  a.nsplit = plan.nsplit;
+  a.scale_log2 = params->attn_scale * 1.4426950408889634f * static_cast<float>(ldexp(1.0, c->k_exp));
+  if (plan.nsplit > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.ws_o = reinterpret_cast<float*>(ws);
+    a.ws_m = reinterpret_cast<float*>(ws + plan.o_bytes);
+    a.ws_l = reinterpret_cast<float*>(ws + plan.o_bytes + plan.m_bytes);
+    a.tickets = reinterpret_cast<unsigned*>(ws + plan.o_bytes + 2 * plan.m_bytes);
+  }
+  return cuda_status(g4::launch_kv4_decode(a, static_cast<cudaStream_t>(stream)), "4-bit decode launch");
+}
+
+size_t g4_kv4_prefill_workspace_size(const g4_layer_params* params, int32_t B, int32_t T, int32_t max_seq_len) {
+  if (kv4_check_params(params) != G4_OK || B < 1 || T < 1 || max_seq_len < T) return 0;
+  return kv4_prefill_head_bytes(B) + 2 * kv4_prefill_kv_bytes(params, B, T, max_seq_len);
+}
+
+g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
+                              int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,
+                              const int32_t* q_start_pos, const int32_t* seq_lens, int32_t B, int32_t T,
+                              int32_t max_seq_len, void* out, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  g4_status st = kv4_check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0 || T < 0) return fail(G4_ERR_INVALID_ARG, "B %d and T %d must be >= 0", B, T);
+  if (q == nullptr || out == nullptr || q_start_pos == nullptr || seq_lens == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q, out, q_start_pos and seq_lens must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(G4_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const g4_kv4_pool* c = nullptr;
+  st = kv4_resolve_src(params, pools, n_layers, layer, &c);
+  if (st != G4_OK) return st;
+  st = kv4_check_table(block_table, max_blocks, c->block_size);
+  if (st != G4_OK) return st;
+  if (max_seq_len < 1 || max_seq_len > max_blocks * c->block_size)
+    return fail(G4_ERR_CAPACITY, "max_seq_len %d outside [1, %d blocks of %d]", max_seq_len, max_blocks, c->block_size);
+  if (T > max_seq_len) return fail(G4_ERR_CAPACITY, "T %d exceeds max_seq_len %d", T, max_seq_len);
+  if (B == 0 || T == 0) return ok();
+  const size_t head = kv4_prefill_head_bytes(B), kv = kv4_prefill_kv_bytes(params, B, T, max_seq_len);
+  if (workspace_bytes < head + 2 * kv)
+    return fail(G4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, head + 2 * kv);
+  if (workspace == nullptr || !aligned16(workspace))
+    return fail(G4_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
+  int* err = device_error_ptr();
+  if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  g4::Kv4GatherArgs ga;
+  memset(&ga, 0, sizeof(ga));
+  ga.data = static_cast<const uint8_t*>(c->data);
+  ga.table = block_table;
+  ga.lens = seq_lens;
+  ga.q_start = q_start_pos;
+  ga.q_rel = reinterpret_cast<int32_t*>(ws);
+  ga.k = ws + head;
+  ga.v = ws + head + kv;
+  ga.B = B;
+  ga.Hkv = params->n_kv_heads;
+  ga.hd = params->head_dim;
+  ga.rows = kv4_prefill_rows(params, T, max_seq_len);
+  ga.max_blocks = max_blocks;
+  ga.n_blocks = c->n_blocks;
+  ga.block_shift = log2_of(c->block_size);
+  ga.T = T;
+  ga.window = params->layer_type == G4_SLIDING ? params->window : 0;
+  ga.max_seq_len = max_seq_len;
+  ga.k_mul = static_cast<float>(ldexp(1.0, c->k_exp));
+  st = cuda_status(g4::launch_kv4_gather(ga, s), "4-bit prefill's gather launch");
+  if (st != G4_OK) return st;
+  g4::PrefillTcArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.ck = ga.k;
+  a.cv = ga.v;
+  a.out = out;
+  a.q_start = ga.q_rel;
+  a.err = err;
+  a.B = B;
+  a.T = T;
+  a.H = params->n_heads;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.max_len = ga.rows;
+  a.sliding = params->layer_type == G4_SLIDING;
+  a.window = params->window;
+  a.scale_log2 = params->attn_scale * 1.4426950408889634f;
+  return cuda_status(g4::launch_prefill_tc(a, s), "tcgen05 prefill launch");
+}
+
 const char* g4_last_error(void) { return g_last_error.c_str(); }
 
 int32_t g4_take_device_error(void) {

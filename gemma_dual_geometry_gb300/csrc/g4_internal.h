@@ -170,4 +170,87 @@ struct DecodePlan {
 DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len);
 int sm_count();  // SMs of the current device
 
+// ---------------------------------------------------------------- the paged 4-bit cache
+// (its layout: include/g4attn.h and g4_kv4.cuh)
+
+struct Kv4AssignArgs {
+  int B, T, block_shift, n_blocks, max_blocks;
+  const int32_t* old_lens;
+  const int32_t* new_lens;
+  int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* table;
+  int32_t* lens_out;
+  int32_t* count_out;
+  int32_t* positions;
+  int32_t* slots;
+};
+constexpr int kKv4MaxBatch = 8192;  // a CTA keeps 8 bytes per sequence in shared memory
+cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s);
+
+struct Kv4AppendArgs {
+  const void* q_in;
+  const void* k_in;  // null on a shared layer
+  const void* v_in;
+  const float* q_w;
+  const float* k_w;
+  const int32_t* positions;  // [B*T]
+  const int32_t* slots;      // [B*T]
+  void* q_out;
+  uint8_t* data;  // the layer's pool
+  int tokens, H, Hkv, hd;
+  int n_slots;       // n_blocks * block_size
+  int block_shift;   // log2(block_size)
+  int rows_per_cta;  // head rows (of H + 2 Hkv) of a token handled per CTA
+  float k_mul;       // 2^-k_exp
+  int n_rot;
+  float eps;
+  float inv_freq[kMaxHalf];
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
+
+// Positions [first, first + rows) of every sequence as bf16 rows
+// k, v [B][Hkv][rows][hd].  first is start[b], or with q_start set (prefill)
+// the first position that any of T queries from q_start[b] on sees; then only
+// rows up to the last query are written, and q_rel[b] is the first query's row.
+struct Kv4GatherArgs {
+  const uint8_t* data;
+  const int32_t* table;
+  const int32_t* start;
+  const int32_t* lens;
+  const int32_t* q_start;
+  int32_t* q_rel;
+  void* k;
+  void* v;
+  int B, Hkv, hd, rows, max_blocks, n_blocks, block_shift;
+  int T, window, max_seq_len;  // prefill; window 0 on a full layer
+  float k_mul;                 // 2^k_exp
+};
+cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
+
+struct Kv4DecodeArgs {
+  const void* q;  // [B][H][hd] bf16
+  const uint8_t* data;
+  const int32_t* table;
+  const int32_t* lens;
+  void* out;
+  float* ws_o;        // [B][H][nsplit][hd]
+  float* ws_m;        // [B][H][nsplit]
+  float* ws_l;
+  unsigned* tickets;  // [B][Hkv]
+  int* err;
+  int B, H, Hkv, hd, max_blocks, n_blocks, block_shift;
+  int window;  // 0 on a full layer
+  int len_cap;
+  int chunk;  // 16-position groups per split
+  int nsplit;
+  float scale_log2;  // attn_scale * log2(e) * 2^k_exp
+};
+struct Kv4DecodePlan {
+  int chunk, nsplit;
+  size_t o_bytes, m_bytes, t_bytes, ws_bytes;  // as DecodePlan
+};
+Kv4DecodePlan kv4_decode_plan(int window, int hd, int H, int Hkv, int B, int max_seq_len);
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
+
 }  // namespace g4

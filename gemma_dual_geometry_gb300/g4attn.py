@@ -41,6 +41,12 @@ class G4KVCache(ctypes.Structure):
                 ("batch", ctypes.c_int32), ("dtype", ctypes.c_int32), ("ring", ctypes.c_int32)]
 
 
+class G4KV4Pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("layer_type", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("k_exp", ctypes.c_int32)]
+
+
 _P = ctypes.POINTER
 # Every function include/g4attn.h declares, with its ctypes signature.
 SIGNATURES = {
@@ -63,6 +69,18 @@ SIGNATURES = {
                                      _c_void_p, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _c_void_p]),
     "g4_attn_out_residual": (_i32, [_c_void_p, _i32, _i32, _c_void_p, _i32, _c_void_p, ctypes.c_float, _c_void_p,
                                     _c_void_p, _c_void_p]),
+    "g4_kv4_assign_blocks": (_i32, [_i32] * 5 + [_c_void_p] * 10),
+    "g4_kv4_append_normrope": (_i32, [_P(G4LayerParams), _P(G4KV4Pool), _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                      _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _c_void_p]),
+    "g4_kv4_gather": (_i32, [_P(G4LayerParams), _P(G4KV4Pool), _i32, _i32, _c_void_p, _i32, _c_void_p, _c_void_p,
+                             _i32, _i32, _c_void_p, _c_void_p, _c_void_p]),
+    "g4_kv4_decode_workspace_size": (ctypes.c_size_t, [_P(G4LayerParams), _i32, _i32]),
+    "g4_kv4_attn_decode": (_i32, [_P(G4LayerParams), _P(G4KV4Pool), _i32, _i32, _c_void_p, _c_void_p, _i32, _c_void_p,
+                                  _i32, _i32, _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "g4_kv4_prefill_workspace_size": (ctypes.c_size_t, [_P(G4LayerParams), _i32, _i32, _i32]),
+    "g4_kv4_attn_prefill": (_i32, [_P(G4LayerParams), _P(G4KV4Pool), _i32, _i32, _c_void_p, _c_void_p, _i32,
+                                   _c_void_p, _c_void_p, _i32, _i32, _i32, _c_void_p, _c_void_p, ctypes.c_size_t,
+                                   _c_void_p]),
     "g4_last_error": (ctypes.c_char_p, []),
     "g4_take_device_error": (_i32, []),
 }
@@ -191,6 +209,66 @@ def g4_attn_out_residual(ao, M, K, w_o, D, post_norm_w, eps, h, out, stream=None
     """out = h + rmsnorm(ao . w_o^T, post_norm_w, eps)."""
     _check(lib().g4_attn_out_residual(_ptr(ao), int(M), int(K), _ptr(w_o), int(D), _ptr(post_norm_w), float(eps),
                                       _ptr(h), _ptr(out), _stream(stream, ao)))
+
+
+def kv4_pool_table(n_layers):
+    """Zeroed array of n_layers g4_kv4_pool entries."""
+    return (G4KV4Pool * n_layers)()
+
+
+def kv4_pool_bytes(n_blocks, n_kv_heads, block_size, head_dim):
+    """Bytes of one layer's pool."""
+    return n_blocks * n_kv_heads * (block_size // 16) * 18 * head_dim
+
+
+def set_kv4_pool(table, layer, data, layer_type, head_dim, n_kv_heads, n_blocks, block_size, k_exp=0):
+    """Fill entry ``layer`` of a pool table."""
+    table[layer] = G4KV4Pool(_ptr(data), int(layer_type), int(head_dim), int(n_kv_heads), int(n_blocks),
+                             int(block_size), int(k_exp))
+
+
+def g4_kv4_assign_blocks(B, T, block_size, n_blocks, max_blocks, old_lens, new_lens, free_blocks, free_count,
+                         block_table, lens_out, free_count_out, positions, slots, stream=None):
+    _check(lib().g4_kv4_assign_blocks(B, T, block_size, n_blocks, max_blocks, _ptr(old_lens), _ptr(new_lens),
+                                      _ptr(free_blocks), _ptr(free_count), _ptr(block_table), _ptr(lens_out),
+                                      _ptr(free_count_out), _ptr(positions), _ptr(slots), _stream(stream, old_lens)))
+
+
+def g4_kv4_append_normrope(params, pools, layer, q_in, k_in, v_in, q_norm_w, k_norm_w, positions, slots, B, T, q_out,
+                           stream=None):
+    """g4_kv_append_normrope into a 4-bit pool at the tokens' slots."""
+    _check(lib().g4_kv4_append_normrope(ctypes.byref(params), pools, len(pools), layer, _ptr(q_in), _ptr(k_in),
+                                        _ptr(v_in), _ptr(q_norm_w), _ptr(k_norm_w), _ptr(positions), _ptr(slots), B,
+                                        T, _ptr(q_out), _stream(stream, q_in)))
+
+
+def g4_kv4_gather(params, pools, layer, block_table, max_blocks, start, seq_lens, B, rows, k_out, v_out, stream=None):
+    """Positions [start, start + rows) of every sequence as bf16 rows."""
+    _check(lib().g4_kv4_gather(ctypes.byref(params), pools, len(pools), layer, _ptr(block_table), max_blocks,
+                               _ptr(start), _ptr(seq_lens), B, rows, _ptr(k_out), _ptr(v_out),
+                               _stream(stream, k_out)))
+
+
+def g4_kv4_decode_workspace_size(params, B, max_seq_len):
+    return int(lib().g4_kv4_decode_workspace_size(ctypes.byref(params), B, max_seq_len))
+
+
+def g4_kv4_attn_decode(params, pools, layer, q, block_table, max_blocks, seq_lens, B, max_seq_len, out,
+                       workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().g4_kv4_attn_decode(ctypes.byref(params), pools, len(pools), layer, _ptr(q), _ptr(block_table),
+                                    max_blocks, _ptr(seq_lens), B, max_seq_len, _ptr(out), _ptr(workspace),
+                                    int(workspace_bytes), _stream(stream, q)))
+
+
+def g4_kv4_prefill_workspace_size(params, B, T, max_seq_len):
+    return int(lib().g4_kv4_prefill_workspace_size(ctypes.byref(params), B, T, max_seq_len))
+
+
+def g4_kv4_attn_prefill(params, pools, layer, q, block_table, max_blocks, q_start_pos, seq_lens, B, T, max_seq_len,
+                        out, workspace, workspace_bytes, stream=None):
+    _check(lib().g4_kv4_attn_prefill(ctypes.byref(params), pools, len(pools), layer, _ptr(q), _ptr(block_table),
+                                     max_blocks, _ptr(q_start_pos), _ptr(seq_lens), B, T, max_seq_len, _ptr(out),
+                                     _ptr(workspace), int(workspace_bytes), _stream(stream, q)))
 
 
 def g4_last_error():

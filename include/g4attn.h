@@ -351,6 +351,173 @@ g4_status g4_attn_decode_noalloc(const g4_layer_params* params, const g4_kv_cach
                                  int32_t layer, const void* q, const int32_t* seq_lens, int32_t B,
                                  int32_t max_seq_len, void* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged KV cache in 4 bits
+ *
+ * The cache above is one rectangle of bf16 or float32 rows per layer.  A
+ * server that holds many contexts of differing lengths keeps them instead in
+ * blocks of 16 to 128 positions, dealt out of a pool as sequences grow, and
+ * in 4.5 bits per element: decode streams the cache, so 2 / 0.5625 = 3.6
+ * times fewer bytes are 3.6 times more contexts and as much less to stream.
+ * (The pages have no counterpart: this is a cache of this library.)
+ *
+ * What a row holds.  x is the bf16 row that g4_kv_append_normrope would
+ * store.  For every 16 consecutive elements, with e = k_exp for k and 0 for v:
+ *   s      = RN_e4m3(min(max |x| 2^-e / 6, 448))   one byte
+ *   code_d = RN_e2m1(x_d 2^-e / s), 0 where s = 0   four bits
+ * (RN: to nearest, ties to even; e2m1 holds 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives and saturates at 6), and the row stands for code_d s 2^e,
+ * which bf16 holds exactly.  x is itself correctly rounded, so the bytes are
+ * a function of the raw inputs alone, whatever kernel wrote them.  A 16 that
+ * holds a NaN or an infinity gets the scale NaN and stands for NaNs.
+ *
+ * Where it lies.  data[n_blocks][n_kv_heads][block_size / 16] records of
+ * 18 head_dim bytes, one per 16 positions of one kv head: K codes (8
+ * head_dim bytes), K scales (head_dim), V codes (8 head_dim), V scales
+ * (head_dim), each in the order in which the lanes of a warp hold a
+ * 16 x 16 tensor-core operand, so that attention reads a record straight into
+ * its fragments.  With p = d / 64, w = (d / 16) mod 4 of element d:
+ *   K, position m = 8 r + g:
+ *     code  at  512 p + 16 (4 g + (d mod 16) / 4) + 8 r + 2 w + (d mod 4) / 2
+ *     scale at  64 p + 8 g + 2 w + r
+ *   V, position m = 8 ih + 2 t + il, i = 2 ih + il:
+ *     code  at  512 p + 16 (4 ((d mod 16) / 2) + t) + 4 i + w
+ *     scale at  64 p + 16 t + 4 w + i
+ * with the code of an even d in the low half of its byte.
+ *
+ * A block's id is its index in the pool; a sequence's blocks are a row of
+ * block_table[B][max_blocks] (int32): position p of sequence b lies in block
+ * block_table[b][p / block_size], and its slot is that id * block_size + p mod
+ * block_size.  One table serves all layers when their pools have the same
+ * number of blocks.  Entries past a sequence's last block are not read; a
+ * block id outside the pool is never dereferenced (its positions count as
+ * absent in decode and as zeros in gather and prefill; the append does not
+ * write them).  Blocks may be shared by several sequences as long as nobody
+ * appends to them.
+ *
+ * head_dim, GQA groups, layer types, shared layers and errors are as above.
+ * Layers are bf16 (G4_ERR_UNSUPPORTED otherwise).
+ */
+
+/*
+ * One layer's pool, caller-owned device memory, 16-byte aligned:
+ *   data        n_blocks * n_kv_heads * block_size / 16 * 18 * head_dim bytes
+ *   block_size  16, 32, 64 or 128 positions
+ *   k_exp       k is stored divided by 2^k_exp, -32 .. 32.  The e4m3 scales
+ *               reach from 2^-9 to 448: 0 suits k_norm_w around 1; with k
+ *               rows of another size take log2 of that size.
+ * n_blocks * block_size must not exceed 2^31 - 1.  Layers that read another
+ * layer's pool may leave their entry zeroed.
+ */
+typedef struct {
+  void* data;
+  int32_t layer_type;
+  int32_t head_dim;
+  int32_t n_kv_heads;
+  int32_t n_blocks;
+  int32_t block_size;
+  int32_t k_exp;
+} g4_kv4_pool;
+
+/*
+ * Gives the B sequences of a batch blocks of a pool as their lengths change,
+ * and says where their new tokens go; one launch, no host round trip.
+ *   old_lens, new_lens  [B] positions held now and wanted.  Growing takes
+ *                   blocks, shrinking gives them back (new_lens 0: the
+ *                   sequence has ended; old_lens 0: it is admitted).  Both are
+ *                   clamped into [0, max_blocks * block_size], and a sequence
+ *                   grows by T positions per call at most.
+ *   free_blocks     [n_blocks] the pool's free block ids, free_count[0] of
+ *                   them in front: a stack whose top is its last entry.
+ *   block_table     [B][max_blocks]
+ *   lens_out        [B] the lengths granted; may be old_lens itself
+ *   free_count_out  [1]; may be free_count itself
+ *   positions, slots  [B][T]: token t of sequence b is position old_lens[b]
+ *                   + t and its slot, or -1 and -1 past its granted length
+ *                   (g4_kv4_append_normrope's arguments).
+ * Blocks given back are pushed first, in the order of sequences and entries;
+ * then blocks are popped in the same order.  Sequences are served first come,
+ * first served: one that needs blocks is granted its new length if the
+ * blocks of all sequences up to it fit, else it keeps old_lens and gets no
+ * slots.  Writes the table entries of the blocks taken, the free_blocks
+ * entries of those given back, and the outputs; table entries of blocks given
+ * back keep their stale ids.  With lens_out and free_count_out apart from
+ * the inputs, a repeated call (a replayed graph) repeats its results.  B is at
+ * most 8192 and B * max_blocks, B * T at most 2^31 - 1.
+ */
+g4_status g4_kv4_assign_blocks(int32_t B, int32_t T, int32_t block_size, int32_t n_blocks, int32_t max_blocks,
+                               const int32_t* old_lens, const int32_t* new_lens, int32_t* free_blocks,
+                               const int32_t* free_count, int32_t* block_table, int32_t* lens_out,
+                               int32_t* free_count_out, int32_t* positions, int32_t* slots, void* stream);
+
+/*
+ * g4_kv_append_normrope into a pool: q is normed and roped to q_out, k normed
+ * and roped and v normed, and both stored in 4 bits at the tokens' slots.
+ *   positions  [B][T] RoPE positions (any value)
+ *   slots      [B][T] where k and v go; a slot outside the pool is not written
+ * Other arguments as g4_kv_append_normrope; the layer's pool is pools[layer].
+ * Two tokens of one call with the same slot leave a mixture of both rows.
+ */
+g4_status g4_kv4_append_normrope(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
+                                 int32_t layer, const void* q_in, const void* k_in, const void* v_in,
+                                 const float* q_norm_w, const float* k_norm_w, const int32_t* positions,
+                                 const int32_t* slots, int32_t B, int32_t T, void* q_out, void* stream);
+
+/*
+ * Reads positions [start[b], start[b] + rows) of every sequence back into
+ * k_out, v_out [B][n_kv_heads][rows][head_dim] bf16, exactly the values the
+ * pool stands for; zeros at positions from seq_lens[b] on (and below 0).  For
+ * handing a context to the bf16 calls above, to another pool, or to the host.
+ */
+g4_status g4_kv4_gather(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers, int32_t layer,
+                        const int32_t* block_table, int32_t max_blocks, const int32_t* start,
+                        const int32_t* seq_lens, int32_t B, int32_t rows, void* k_out, void* v_out, void* stream);
+
+/* Workspace bytes g4_kv4_attn_decode needs (0: none). */
+size_t g4_kv4_decode_workspace_size(const g4_layer_params* params, int32_t B, int32_t max_seq_len);
+
+/*
+ * g4_attn_decode over a pool: one query token per sequence.
+ *   seq_lens     [B] keys per sequence including the new token (append it
+ *                first), clamped into [0, max_seq_len].  A sequence of no
+ *                keys gets an output of zeros.
+ *   max_seq_len  1 .. max_blocks * block_size
+ * q, out, workspace (zero-filled once, left ready by every call, not shared
+ * by calls that overlap) as g4_attn_decode.  q.k and P.V run on
+ * tensor cores from fp16 operands with float32 sums: keys and values are
+ * exact in fp16, q is scaled by a power of two per head, and a probability
+ * times its value's scale is rounded to 11 bits.
+ */
+g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
+                             int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,
+                             const int32_t* seq_lens, int32_t B, int32_t max_seq_len, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Workspace bytes g4_kv4_attn_prefill needs. */
+size_t g4_kv4_prefill_workspace_size(const g4_layer_params* params, int32_t B, int32_t T, int32_t max_seq_len);
+
+/*
+ * g4_attn_prefill over a pool: T new tokens per sequence, token t of
+ * sequence b at position q_start_pos[b] + t, appended before.
+ *   seq_lens     [B] keys held, usually q_start_pos[b] + T.  Fewer (a padded
+ *                batch) makes the tokens from seq_lens[b] - q_start_pos[b] on
+ *                padding: their rows are computed as if the positions past
+ *                seq_lens[b] held zero keys and values.
+ *   max_seq_len  bound on q_start_pos[b] + T, T .. max_blocks * block_size;
+ *                q_start_pos is clamped into [0, max_seq_len - T]
+ *   workspace    16-byte aligned, no contents needed; not shared by calls
+ *                that overlap
+ * The keys that the T tokens see are laid out in the workspace as bf16 (a
+ * sliding layer's T + window - 1, a full layer's max_seq_len per sequence) and
+ * attention runs on the tensor cores as in g4_attn_prefill, whose limits on
+ * launches in flight hold.
+ */
+g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
+                              int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,
+                              const int32_t* q_start_pos, const int32_t* seq_lens, int32_t B, int32_t T,
+                              int32_t max_seq_len, void* out, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Thread-local message of the last non-OK status ("" if none). */
 const char* g4_last_error(void);
 
