@@ -851,8 +851,6 @@ g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* p
   const int window = params->layer_type == G4_SLIDING ? params->window : 0;
   const g4::Kv4DecodePlan plan =
       g4::kv4_decode_plan(window, params->head_dim, params->n_heads, params->n_kv_heads, B, max_seq_len);
-  if (static_cast<long long>(B) * params->n_kv_heads * plan.nsplit > 0x7fffffffLL)
-    return fail(G4_ERR_INVALID_ARG, "B %d too large", B);
   if (workspace_bytes < plan.ws_bytes)
     return fail(G4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
   if (plan.ws_bytes > 0 && (workspace == nullptr || !aligned16(workspace)))
@@ -876,15 +874,13 @@ g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* p
   a.block_shift = log2_of(c->block_size);
   a.window = window;
   a.len_cap = max_seq_len;
-  a.chunk = plan.chunk;
-  a.nsplit = plan.nsplit;
+  a.nctas = plan.nctas;
   a.scale_log2 = params->attn_scale * 1.4426950408889634f * static_cast<float>(ldexp(1.0, c->k_exp));
-  if (plan.nsplit > 1) {
+  if (plan.ws_bytes > 0) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.ws_o = reinterpret_cast<float*>(ws);
-    a.ws_m = reinterpret_cast<float*>(ws + plan.o_bytes);
-    a.ws_l = reinterpret_cast<float*>(ws + plan.o_bytes + plan.m_bytes);
-    a.tickets = reinterpret_cast<unsigned*>(ws + plan.o_bytes + 2 * plan.m_bytes);
+    a.tickets = reinterpret_cast<unsigned*>(ws);
+    a.ws_ml = reinterpret_cast<float2*>(ws + g4::kKv4TicketBytes);
+    a.ws_o = reinterpret_cast<float*>(ws + g4::kKv4TicketBytes + plan.ml_bytes);
   }
   return cuda_status(g4::launch_kv4_decode(a, static_cast<cudaStream_t>(stream)), "4-bit decode launch");
 }

@@ -234,21 +234,23 @@ struct Kv4DecodeArgs {
   const int32_t* table;
   const int32_t* lens;
   void* out;
-  float* ws_o;        // [B][H][nsplit][hd]
-  float* ws_m;        // [B][H][nsplit]
-  float* ws_l;
-  unsigned* tickets;  // [B][Hkv]
+  float* ws_o;        // [2 nctas][G][hd] partial outputs: two units of a CTA's share may continue in other CTAs'
+  float2* ws_ml;      // [2 nctas][8] their softmax references and denominators
+  unsigned* tickets;  // arrival counters (zero between calls): [kKv4MaxCtas] of units, [2 kKv4MaxCtas] of parts of them
   int* err;
   int B, H, Hkv, hd, max_blocks, n_blocks, block_shift;
   int window;  // 0 on a full layer
   int len_cap;
-  int chunk;  // 16-position groups per split
-  int nsplit;
+  int nctas;
   float scale_log2;  // attn_scale * log2(e) * 2^k_exp
 };
+// Workspace: the tickets, then ws_ml, then ws_o.  The tickets are in front and of
+// a fixed size, so calls of different shapes may take turns on one workspace.
+constexpr int kKv4MaxCtas = 1024;
+constexpr size_t kKv4TicketBytes = 3 * kKv4MaxCtas * 4;
 struct Kv4DecodePlan {
-  int chunk, nsplit;
-  size_t o_bytes, m_bytes, t_bytes, ws_bytes;  // as DecodePlan
+  int nctas;
+  size_t ml_bytes, o_bytes, ws_bytes;
 };
 Kv4DecodePlan kv4_decode_plan(int window, int hd, int H, int Hkv, int B, int max_seq_len);
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);

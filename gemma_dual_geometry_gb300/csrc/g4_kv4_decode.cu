@@ -4,14 +4,12 @@
 // out_h = sum_j p_j v_j / sum_j p_j,  p_j = 2^(c (q_h . k_j) - m),  over the keys
 // [max(0, L - window), L) (all L on full layers), c = attn_scale log2(e).
 //
-// One CTA per (split, kv head, sequence), all G <= 8 query heads of the kv
-// head together, so a record of the cache is read once.  A record (16
-// positions, 18 head_dim bytes) is one bulk copy; every warp owns a ring of
-// stages and takes its CTA's records in turn.  At 4.5 bits per element an SM's
-// share of HBM is ~42 elements per clock, each of which meets 8 (padded)
-// heads twice: more multiply-adds than the CUDA cores have, so both products
-// run on mma.sync m16n8k16 (fp16 operands, float32 sums), whose 16 x 16 operand
-// is a record's scale block and whose 8 columns are the heads:
+// All G <= 8 query heads of a kv head are served together, so a record of the
+// cache (16 positions, 18 head_dim bytes) is read once.  At 4.5 bits per
+// element an SM's share of HBM is ~42 elements per clock, each of which meets
+// 8 (padded) heads twice: more multiply-adds than the CUDA cores have, so both
+// products run on mma.sync m16n8k16 (fp16 operands, float32 sums), whose
+// 16 x 16 operand is a record's scale block and whose 8 columns are the heads:
 //   S^T[16 positions][8 heads] += s . (K[16 x 16] Q^T)    per 16 elements: the
 //     product of the bare codes, scaled by the block's scale in float32;
 //   O^T[16 elements][8 heads]  += V^T[16 x 16] (P s)^T    per 16 elements: the
@@ -21,14 +19,32 @@
 // each lane its fragments in 16-byte loads, free of bank conflicts; codes widen
 // two at a time with one conversion.
 //
-// The online softmax keeps, per lane, a reference m that only moves (rescaling
-// O) when a score exceeds it by 2^kSlack, so most records need no
-// reduction over the warp.  Probabilities are formed as 2^(s - m + kShift):
-// fp16's 11 bits then reach down to 2^-18 of the reference.
+// Work.  The records of all (sequence, kv head) units, laid end to end, are
+// dealt out in equal contiguous shares to as many CTAs as are resident, so
+// ragged lengths leave no SM idle.  A unit inside one share is written
+// directly; the CTAs of a unit that spans shares leave partials in the workspace
+// and the one that takes the last ticket merges them.
 //
-// Splits of a sequence leave their partials in the workspace; the CTA that
-// takes the last ticket of a (sequence, kv head) merges them.  The number of
-// splits that take part is that of the sequence's own length.
+// A CTA (4 warps) takes STEP records per step.  Each warp scores its share of
+// them and forms their probabilities; after a CTA barrier each warp adds all the
+// step's P V for its own slice of head_dim, so O takes few registers and needs no
+// merge between warps (at head_dim 64 and 128, whose 64-element pieces are
+// fewer than the warps, 4 or 2 warps hold a piece and split the records).  K and V
+// parts of a record are separate bulk copies in the order K_0 V_0 K_1 V_1 ...
+// through a ring of SLOTS buffers: a step's K buffer is free at its barrier, its V
+// buffer at the next step's.  The copies run on across the units of a share.
+//
+// With at most 4 heads the other 4 columns serve a second scale block, so that
+// scales are handled once for two blocks.  Scores: the contraction takes 8
+// elements of block 2j and 8 of block 2j + 1, q being zero for the other
+// block's elements in columns 0-3 and 4-7; two products give the two blocks'
+// sums side by side.  P V: the operand's rows are 8 elements of block 2j and 8 of
+// block 2j + 1, columns 0-3 carry P times the scales of 2j and 4-7 of 2j + 1.
+//
+// The online softmax keeps a reference m per head, common to the CTA, that
+// only moves (rescaling O) when a score exceeds it by 2^kSlack, so most steps
+// need no reduction over positions.  Probabilities are formed as
+// 2^(s - m + kShift): fp16's 11 bits then reach down to 2^-18 of the reference.
 #include <math.h>
 
 #include "g4_device.cuh"
@@ -42,24 +58,29 @@ constexpr int kHeads = 8;  // columns of the tensor-core product
 constexpr float kSlack = 8.0f;
 constexpr float kShift = 4.0f;
 constexpr float kNoKey = -1e30f;  // reference of a state that has seen no key
+constexpr int kFan = 16;      // partials that a first merge takes
+constexpr int kMaxLevel = 64;  // partials that a last merge may be left with (CTAs / kFan at most)
 
+// Shape of the kernel at one head_dim (also used by the plan).
 template <int HD>
 struct Kv4Cfg {
-  static constexpr int NW = 4;                                  // warps per CTA
-  static constexpr int GP = HD >= 256 ? 1 : 256 / HD;           // records per stage
-  static constexpr int NST = 2;                                 // stages per warp
-  static constexpr int MINB = HD >= 512 ? 2 : 4;                // CTAs per SM
-  static constexpr int STAGE_B = GP * Kv4Rec<HD>::BYTES;
-  static constexpr int RING_B = NW * NST * STAGE_B;
-  static constexpr int MERGE_B = NW * kHeads * HD * 4;          // the warps' outputs
-  static constexpr int AREA_B = RING_B > MERGE_B ? RING_B : MERGE_B;
-  static constexpr int Q_OFF = AREA_B;                          // q fragments, fp16
-  static constexpr int BAR_OFF = Q_OFF + kHeads * HD * 2;
-  static constexpr int OK_OFF = BAR_OFF + NW * NST * 8;         // record present, per stage and record
-  static constexpr int QF_OFF = OK_OFF + NW * NST * GP * 4;     // score factor of each head
-  static constexpr int ML_OFF = QF_OFF + kHeads * 4;            // the warps' m and l
-  static constexpr int W_OFF = ML_OFF + NW * kHeads * 8;        // merge weights
-  static constexpr int SMEM_B = W_OFF + kHeads * kMaxSplits * 4;
+  static constexpr int W = 4;                                   // warps per CTA
+  static constexpr int NP = HD / 64;                            // pieces of a row
+  static constexpr int RW = HD >= 256 ? 1 : 256 / HD;           // records a warp scores per step
+  static constexpr int STEP = W * RW;                           // records per step
+  static constexpr int PW = NP >= W ? NP / W : 1;               // pieces of O per warp
+  static constexpr int KS = NP >= W ? 1 : W / NP;               // warps that share a piece
+  static constexpr int MINB = HD >= 512 ? 3 : HD == 256 ? 5 : 4;  // CTAs per SM
+  static constexpr int SLOTS = HD >= 512 ? 3 : 4;               // what MINB leaves room for
+  static constexpr int HALF_B = 9 * HD;                         // K (or V) part of a record
+  static constexpr int SLOT_B = STEP * HALF_B;
+  static constexpr int Q_OFF = SLOTS * SLOT_B;                  // q fragments, fp16 (8 columns)
+  static constexpr int P_OFF = Q_OFF + 16 * HD;                 // probabilities of two steps
+  static constexpr int P_B = 2 * STEP * 32 * 8;
+  static constexpr int RED_OFF = P_OFF + P_B;                   // partial O of warps that share a piece
+  static constexpr int SMEM_B = RED_OFF + (KS > 1 ? kHeads * HD * KS * 4 : 0);
+  static_assert(P_B >= kHeads * kMaxLevel * 4, "the merge's weights take the place of the probabilities");
+  static_assert(MINB * (SMEM_B + 1024 + 1024) <= 227 * 1024, "shared memory of the resident CTAs");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -78,373 +99,664 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return as_u32(__floats2half2_rn(lo, hi)); }
 
-template <int HD>
-__global__ void __launch_bounds__(Kv4Cfg<HD>::NW * 32, Kv4Cfg<HD>::MINB)
+// Keys and records of one sequence.
+struct Kv4Seq {
+  int L, kbeg, first, n;  // visible keys [kbeg, L) in records [first, first + n)
+};
+__device__ __forceinline__ Kv4Seq seq_of(const Kv4DecodeArgs& a, int b) {
+  Kv4Seq s;
+  s.L = min(max(a.lens[b], 0), a.len_cap);
+  s.kbeg = a.window > 0 ? max(0, s.L - a.window) : 0;
+  s.first = s.kbeg >> 4;
+  s.n = ((s.L + 15) >> 4) - s.first;
+  return s;
+}
+
+// The slot of a unit's part i, left by CTA c_first + i: the second of its two
+// where the unit begins, else the first.
+__device__ __forceinline__ int part_slot(int c_first, int i) { return 2 * (c_first + i) + (i == 0 ? 1 : 0); }
+
+// Merges n <= kMaxLevel parts first, first + step, ... of a unit into out, or
+// with out null (un-normalised) into the slot of the first.
+template <int HD, int W>
+__device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first, int first, int step, int n, int G,
+                                         __nv_bfloat16* out, float* s_w) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int h = warp; h < G; h += W) {
+    float M = kNoKey;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&a.ws_ml[part_slot(c_first, first + i * step) * kHeads + h]).x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float l = 0.0f;
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = __ldcg(&a.ws_ml[part_slot(c_first, first + i * step) * kHeads + h]);
+      const float w = ex2_approx(ml.x - M);
+      s_w[h * kMaxLevel + i] = w;
+      l += w * ml.y;
+    }
+    l = warp_sum(l);
+    __syncwarp();
+    if (out != nullptr) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      for (int i = lane; i < n; i += 32) s_w[h * kMaxLevel + i] *= inv;
+    } else if (lane == 0) {
+      a.ws_ml[part_slot(c_first, first) * kHeads + h] = make_float2(M, l);
+    }
+  }
+  __syncthreads();
+  constexpr int kBatch = 4;
+  const int row = G * HD / 4;  // float4 of a slot
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < row; idx += W * 32) {
+    const float* sw = s_w + (idx * 4 / HD) * kMaxLevel;
+    const float4* src = reinterpret_cast<const float4*>(a.ws_o) + idx;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float4 v[kBatch];  // loads in flight
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i0 + i < n) v[i] = __ldcg(src + static_cast<size_t>(part_slot(c_first, first + (i0 + i) * step)) * row);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i0 + i < n) {
+          const float w = sw[i0 + i];
+          acc[0] = fmaf(w, v[i].x, acc[0]);
+          acc[1] = fmaf(w, v[i].y, acc[1]);
+          acc[2] = fmaf(w, v[i].z, acc[2]);
+          acc[3] = fmaf(w, v[i].w, acc[3]);
+        }
+    }
+    if (out != nullptr)
+      store_elems<4>(out + idx * 4, acc);
+    else
+      store_elems<4>(a.ws_o + static_cast<size_t>(part_slot(c_first, first)) * G * HD + idx * 4, acc);
+  }
+}
+
+// A place in the units laid end to end: `off` records into (b, kvh), whose
+// sequence has n records from `first` on; `left` records of the share remain.
+struct Kv4Place {
+  int b, kvh, off, left, first, n;
+};
+
+// GM: most heads per kv head, 4 (two scale blocks per product) or 8.
+template <int HD, int GM>
+__global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs a) {
   using C = Kv4Cfg<HD>;
-  using R = Kv4Rec<HD>;
-  constexpr int NW = C::NW, NST = C::NST, GP = C::GP, NB = HD / 16;
+  constexpr int RW = C::RW, STEP = C::STEP, PW = C::PW, KS = C::KS;
+  constexpr int W = C::W, NT = W * 32, SLOTS = C::SLOTS;
+  constexpr bool PAIR = GM == 4;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  int* s_ok = reinterpret_cast<int*>(smem + C::OK_OFF);
-  float* s_qf = reinterpret_cast<float*>(smem + C::QF_OFF);
-  float* s_m = reinterpret_cast<float*>(smem + C::ML_OFF);
-  float* s_l = s_m + NW * kHeads;
-  float* s_w = reinterpret_cast<float*>(smem + C::W_OFF);
+  __shared__ uint64_t s_bar[SLOTS];
+  __shared__ long long s_scan[W];
+  __shared__ long long s_unit0;                      // records before the consumer's unit
+  __shared__ Kv4Place s_ip, s_cp;                    // next step to copy; unit being consumed
+  __shared__ float s_qf[kHeads];                     // score factor of each head
+  __shared__ float s_top[W * kHeads];
+  __shared__ float s_l[W * kHeads];
+  __shared__ uint32_t s_ok[4];                       // records present in a step (step mod 4)
   __shared__ int s_last;
+  __shared__ int s_abort;
 
-  const int split = blockIdx.x % a.nsplit;
-  const int unit = blockIdx.x / a.nsplit;  // b * Hkv + kvh
-  const int kvh = unit % a.Hkv, b = unit / a.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = a.H / a.Hkv;
-  uint64_t* wbar = bars + warp * NST;
-  int* wok = s_ok + warp * NST * GP;
-  if (lane == 0) {
-    for (int i = 0; i < NST; ++i) mbar_init(smem_u32(&wbar[i]), 1);
+  float* s_w = reinterpret_cast<float*>(smem + C::P_OFF);  // merge weights (no probabilities then)
+  const int h0 = PAIR ? 2 * (t & 1) : 2 * t;               // this lane's columns are heads h0 and h0 + 1
+  if (tid == 0) {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(smem_u32(&s_bar[i]), 1);
     fence_mbar_init();
+    s_abort = 0;
   }
-  __syncwarp();
   pdl_wait();
   pdl_trigger();
 
-  const int L = min(max(a.lens[b], 0), a.len_cap);
-  const int kbeg = a.window > 0 ? max(0, L - a.window) : 0;
-  const int gfirst = kbeg >> 4, gend = (L + 15) >> 4;  // records of the visible keys
-  const int nsplit = (gend - gfirst + a.chunk - 1) / a.chunk;  // splits that hold any
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(b) * a.H + kvh * G) * HD;
-  if (split >= nsplit) {
-    if (split == 0) {  // no key at all
-      for (int i = threadIdx.x; i < G * HD / 2; i += NW * 32) reinterpret_cast<uint32_t*>(out)[i] = 0u;
-    }
-    return;
+  // ---- this CTA's share [w0, w1) of the records laid end to end
+  const int per = (a.B + NT - 1) / NT;  // consecutive sequences per thread
+  const int sb0 = min(a.B, tid * per), sb1 = min(a.B, sb0 + per);
+  long long sum = 0;
+  for (int b = sb0; b < sb1; ++b) sum += seq_of(a, b).n;
+  long long upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
   }
-  const int g0 = gfirst + split * a.chunk;
-  const int ng = min(a.chunk, gend - g0);
-  const int nstages = (ng + GP - 1) / GP;
-  const int mine = nstages > warp ? (nstages - warp + NW - 1) / NW : 0;  // stages of this warp
-
-  // Block ids of the warp's stages, 32 stages at a time: lane k % 32 holds
-  // those of stage k and issues its copies.  The next 32 are loaded as soon as
-  // the first of the current ones is used.
-  const int32_t* row = a.table + static_cast<size_t>(b) * a.max_blocks;
-  auto stage_group = [&](int k) { return g0 + (warp + k * NW) * GP; };
-  int ids[GP], ids_next[GP];
-  auto load_ids = [&](int window, int (&to)[GP]) {
-    const int k = window * 32 + lane;
+  if (lane == 31) s_scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
 #pragma unroll
-    for (int i = 0; i < GP; ++i) {
-      const int gi = stage_group(k) + i;
-      to[i] = -1;
-      if (k < mine && gi < g0 + ng) {
-        const int entry = gi >> (a.block_shift - 4);
-        if (entry < a.max_blocks) to[i] = row[entry];
-      }
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) upto += s_scan[w];
+    total += s_scan[w];
+  }
+  total *= a.Hkv;
+  const int nctas = gridDim.x;
+  long long share = (total + nctas - 1) / nctas;
+  share = (share + STEP - 1) / STEP * STEP;
+  const long long w0 = min(total, share * blockIdx.x), w1 = min(total, w0 + share);
+  // sequences without keys, spread over the CTAs
+  for (int b = blockIdx.x; b < a.B; b += nctas) {
+    if (seq_of(a, b).n == 0) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(b) * a.H * HD);
+      for (int i = tid; i < a.H * HD / 2; i += NT) o[i] = 0u;
     }
-  };
-  uint8_t* ring = smem + warp * (NST * C::STAGE_B);
-  auto issue = [&](int k) {  // stage k of this warp into buffer k % NST
-    if ((k & 31) == 0 && k > 0) {
-#pragma unroll
-      for (int i = 0; i < GP; ++i) ids[i] = ids_next[i];
-      load_ids((k >> 5) + 1, ids_next);
-    }
-    if (lane == (k & 31)) {
-      const int buf = k % NST;
-      const uint32_t bar = smem_u32(&wbar[buf]);
-      const uint32_t dst = smem_u32(ring + buf * C::STAGE_B);
-      bool ok[GP];
-      uint32_t bytes = 0;
-#pragma unroll
-      for (int i = 0; i < GP; ++i) {
-        ok[i] = ids[i] >= 0 && ids[i] < a.n_blocks;
-        wok[buf * GP + i] = ok[i];
-        bytes += ok[i] ? R::BYTES : 0;
-      }
-      mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-      for (int i = 0; i < GP; ++i) {
-        if (ok[i]) {
-          const int in_block = (stage_group(k) + i) & ((1 << (a.block_shift - 4)) - 1);
-          bulk_g2s(dst + i * R::BYTES, a.data + kv4_record<HD>(ids[i], kvh, in_block, a.Hkv, a.block_shift), R::BYTES,
-                   bar);
-        }
-      }
-    }
-  };
-  load_ids(0, ids);
-  load_ids(1, ids_next);
-  for (int k = 0; k < NST && k < mine; ++k) issue(k);
-
-  // q fragments: lane (head g, t) holds elements 4t .. 4t+3 of every 16, two
-  // blocks side by side; each head scaled by the power of two that brings its
-  // largest element into [1, 2).
+  }
+  if (w0 >= w1) return;
   {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(b) * a.H + kvh * G) * HD;
-    for (int h = warp; h < kHeads; h += NW) {
-      constexpr int PER = HD / 32;  // elements per lane, consecutive
-      float x[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) x[i] = 0.0f;
-      if (h < G) load_elems<PER>(q + h * HD + lane * PER, x);
-      float top = 0.0f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) top = fmaxf(top, fabsf(x[i]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      e = top > 0.0f ? min(max(e, -120), 120) : 0;
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      if (lane == 0) s_qf[h] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-      for (int i = 0; i < PER; i += 2) {
-        const int d = lane * PER + i;
-        const int blk = d >> 4, tt = (d >> 2) & 3;
-        *reinterpret_cast<uint32_t*>(smem + C::Q_OFF + ((blk >> 1) * 32 + h * 4 + tt) * 16 + (blk & 1) * 8 + (d & 2) * 2) =
-            pack_f16x2(x[i] * down, x[i + 1] * down);
+    long long at = (upto - sum) * a.Hkv;  // records before this thread's sequences
+    if (w0 >= at && w0 < upto * a.Hkv) {
+      for (int b = sb0; b < sb1; ++b) {
+        const Kv4Seq seq = seq_of(a, b);
+        const long long n = seq.n;
+        if (w0 < at + n * a.Hkv) {
+          Kv4Place p;
+          p.b = b;
+          p.kvh = static_cast<int>((w0 - at) / n);
+          p.off = static_cast<int>(w0 - at - p.kvh * n);
+          p.left = static_cast<int>(w1 - w0);
+          p.first = seq.first;
+          p.n = seq.n;
+          s_ip = s_cp = p;
+          s_unit0 = at + p.kvh * n;
+          break;
+        }
+        at += n * a.Hkv;
       }
     }
   }
   __syncthreads();
-  const float qf0 = s_qf[2 * t], qf1 = s_qf[2 * t + 1];
+  // Moves a place n records on within its unit, or to the next unit that has any.
+  auto advance = [&](Kv4Place& p, int n) {
+    p.off += n;
+    p.left -= n;
+    if (p.left <= 0 || p.off < p.n) return;
+    p.off = 0;
+    if (++p.kvh < a.Hkv) return;
+    p.kvh = 0;
+    Kv4Seq seq;
+    do {  // (work is left, so a later sequence has records)
+      seq = seq_of(a, ++p.b);
+    } while (seq.n == 0);
+    p.first = seq.first;
+    p.n = seq.n;
+  };
 
-  float o[NB][4];
-#pragma unroll
-  for (int i = 0; i < NB; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-  float m0 = kNoKey, m1 = kNoKey, l0 = 0.0f, l1 = 0.0f;  // heads 2t and 2t + 1
-
-  int done = 0;
-  bool aborted = false;
-  for (int k = 0; k < mine; ++k) {
-    const int buf = k % NST;
-    if (!warp_wait(smem_u32(&wbar[buf]), (k / NST) & 1, a.err)) {
-      aborted = true;
-      break;
+  // ---- copies (warp 0): lane r < STEP owns record r of a step.  Part n = 2 step +
+  // (V ? 1 : 0) goes to buffer n mod SLOTS once part n - SLOTS has been read.
+  // The block ids of a step are loaded when the step before it has been issued.
+  int nrec_k = 0;               // records of the next K step (0: none is left)
+  int id_k = -1, id_v = -1;     // this lane's block id of the next K part and of the next V part
+  uint32_t rec_k = 0, rec_v = 0;  // and the record's index in its block and head
+  int issued = 0;               // parts
+  const int rec_mask = (1 << (a.block_shift - 4)) - 1;
+  auto load_step = [&]() {      // ids of the step at s_ip; moves it past the step
+    Kv4Place p = s_ip;
+    __syncwarp();
+    id_k = -1;
+    nrec_k = 0;
+    if (p.left <= 0) return;
+    const int n = min(min(STEP, p.n - p.off), p.left);
+    if (lane < n) {
+      const int gi = p.first + p.off + lane;
+      const int entry = gi >> (a.block_shift - 4);
+      if (entry < a.max_blocks) id_k = a.table[static_cast<size_t>(p.b) * a.max_blocks + entry];
+      rec_k = static_cast<uint32_t>(p.kvh) << (a.block_shift - 4) | (gi & rec_mask);
     }
+    nrec_k = n;
+    advance(p, n);
+    if (lane == 0) s_ip = p;
+    __syncwarp();
+  };
+  bool v_pending = false;
+  auto issue = [&]() {  // part `issued`, if there is one
+    const bool is_v = issued & 1;
+    if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort)) || !(is_v ? v_pending : nrec_k > 0)) return;
+    const int id = is_v ? id_v : id_k;
+    const bool there = id >= 0 && id < a.n_blocks;
+    const uint32_t bar = smem_u32(&s_bar[issued % SLOTS]);
+    const uint32_t all = __ballot_sync(0xffffffffu, there);
+    if (lane == 0) {
+      if (!is_v) s_ok[(issued >> 1) & 3] = all;
+      mbar_arrive_expect_tx(bar, __popc(all) * C::HALF_B);
+    }
+    __syncwarp();
+    if (there) {
+      const size_t rec = (static_cast<size_t>(id) * a.Hkv << (a.block_shift - 4)) + (is_v ? rec_v : rec_k);
+      bulk_g2s(smem_u32(smem) + (issued % SLOTS) * C::SLOT_B + lane * C::HALF_B,
+               a.data + rec * Kv4Rec<HD>::BYTES + (is_v ? C::HALF_B : 0), C::HALF_B, bar);
+    }
+    v_pending = !is_v;
+    if (!is_v) {
+      id_v = id_k;
+      rec_v = rec_k;
+      load_step();
+    }
+    ++issued;
+  };
+  if (warp == 0) {
+    load_step();
 #pragma unroll 1
-    for (int i = 0; i < GP; ++i) {
-      const int gi = stage_group(k) + i;
-      if (gi >= g0 + ng || !wok[buf * GP + i]) continue;
-      const uint8_t* rec = ring + buf * C::STAGE_B + i * R::BYTES;
-      const int pos0 = gi * kKv4Group;
+    for (int i = 0; i < SLOTS; ++i) issue();
+  }
 
-      // S^T = K Q^T
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int qrec = warp * RW;                              // first record this warp scores
+  const int vpiece = KS > 1 ? (warp % C::NP) : warp * PW;  // first piece of O of this warp
+  const int vrec0 = KS > 1 ? warp / C::NP : 0;             // its records of a step: vrec0, vrec0 + KS, ...
+
+  // s += the products of 64 elements of a record's keys with q
+  auto score_piece = [&](float (&s)[4], const uint8_t* rec, int p) {
+    const uint4 kc = *reinterpret_cast<const uint4*>(rec + p * 512 + lane * 16);
+    const uint4 qa = *reinterpret_cast<const uint4*>(smem + C::Q_OFF + ((2 * p) * 32 + lane) * 16);
+    const uint4 qb = *reinterpret_cast<const uint4*>(smem + C::Q_OFF + ((2 * p + 1) * 32 + lane) * 16);
+    auto scale_add = [&](uint32_t f16s, const float (&d)[4]) {
+      const float2 sc = __half22float2(as_half2(f16s));
+      s[0] = fmaf(sc.x, d[0], s[0]);
+      s[1] = fmaf(sc.x, d[1], s[1]);
+      s[2] = fmaf(sc.y, d[2], s[2]);
+      s[3] = fmaf(sc.y, d[3], s[3]);
+    };
+    if constexpr (PAIR) {
+      const uint8_t* ks = rec + 8 * HD + p * 64 + g * 8 + (t >> 1) * 2;  // block 2j + (t >> 1): columns 0-3, 4-7
 #pragma unroll
-      for (int p = 0; p < R::NP; ++p) {
-        const uint4 kc = *reinterpret_cast<const uint4*>(rec + R::KC + p * 512 + lane * 16);
-        const uint2 ks = *reinterpret_cast<const uint2*>(rec + R::KS + p * 64 + g * 8);
-        const uint4 qa = *reinterpret_cast<const uint4*>(smem + C::Q_OFF + ((2 * p) * 32 + lane) * 16);
-        const uint4 qb = *reinterpret_cast<const uint4*>(smem + C::Q_OFF + ((2 * p + 1) * 32 + lane) * 16);
-        const uint32_t qw[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t c0 = j ? kc.y : kc.x, c1 = j ? kc.w : kc.z;
+        const uint4 q = j ? qb : qa;
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_f16(d, e2m1x2_f16x2<0>(c0), e2m1x2_f16x2<0>(c1), e2m1x2_f16x2<2>(c0), e2m1x2_f16x2<2>(c1), q.x, q.y);
+        mma_f16(d, e2m1x2_f16x2<1>(c0), e2m1x2_f16x2<1>(c1), e2m1x2_f16x2<3>(c0), e2m1x2_f16x2<3>(c1), q.z, q.w);
+        scale_add(e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(ks + j * 4)), d);
+      }
+    } else {
+      const uint2 ks = *reinterpret_cast<const uint2*>(rec + 8 * HD + p * 64 + g * 8);
+      const uint32_t qw[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t w0 = w < 2 ? kc.x : kc.y, w1 = w < 2 ? kc.z : kc.w;
-          const uint32_t sw = w < 2 ? ks.x : ks.y;
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (w & 1)
-            mma_f16(d, e2m1x2_f16x2<2>(w0), e2m1x2_f16x2<2>(w1), e2m1x2_f16x2<3>(w0), e2m1x2_f16x2<3>(w1), qw[2 * w],
-                    qw[2 * w + 1]);
-          else
-            mma_f16(d, e2m1x2_f16x2<0>(w0), e2m1x2_f16x2<0>(w1), e2m1x2_f16x2<1>(w0), e2m1x2_f16x2<1>(w1), qw[2 * w],
-                    qw[2 * w + 1]);
-          const float2 sc = __half22float2(as_half2(w & 1 ? e4m3x2_hi_f16x2(sw) : e4m3x2_f16x2(sw)));
-          s[0] = fmaf(sc.x, d[0], s[0]);
-          s[1] = fmaf(sc.x, d[1], s[1]);
-          s[2] = fmaf(sc.y, d[2], s[2]);
-          s[3] = fmaf(sc.y, d[3], s[3]);
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t c0 = w < 2 ? kc.x : kc.y, c1 = w < 2 ? kc.z : kc.w;
+        const uint32_t sw = w < 2 ? ks.x : ks.y;
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (w & 1)
+          mma_f16(d, e2m1x2_f16x2<2>(c0), e2m1x2_f16x2<2>(c1), e2m1x2_f16x2<3>(c0), e2m1x2_f16x2<3>(c1), qw[2 * w],
+                  qw[2 * w + 1]);
+        else
+          mma_f16(d, e2m1x2_f16x2<0>(c0), e2m1x2_f16x2<0>(c1), e2m1x2_f16x2<1>(c0), e2m1x2_f16x2<1>(c1), qw[2 * w],
+                  qw[2 * w + 1]);
+        scale_add(w & 1 ? e4m3x2_hi_f16x2(sw) : e4m3x2_f16x2(sw), d);
+      }
+    }
+  };
+  // O^T += V^T (P s)^T for 64 elements of a record's values
+  auto add_piece = [&](float (*o)[4], const uint8_t* rec, int p, uint2 pp, uint32_t vmask) {
+    const uint4 vc = *reinterpret_cast<const uint4*>(rec + p * 512 + lane * 16);
+    const __half2 pa = as_half2(pp.x), pb = as_half2(pp.y);
+    // pairs of positions side by side, for the even and the odd elements
+    const uint32_t lo01 = (vc.x & 0x0f0f0f0fu) | ((vc.y << 4) & 0xf0f0f0f0u);
+    const uint32_t hi01 = ((vc.x >> 4) & 0x0f0f0f0fu) | (vc.y & 0xf0f0f0f0u);
+    const uint32_t lo23 = (vc.z & 0x0f0f0f0fu) | ((vc.w << 4) & 0xf0f0f0f0u);
+    const uint32_t hi23 = ((vc.z >> 4) & 0x0f0f0f0fu) | (vc.w & 0xf0f0f0f0u);
+    const uint8_t* vs = rec + 8 * HD + p * 64 + t * 16;
+    if constexpr (PAIR) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t sw = *reinterpret_cast<const uint32_t*>(vs + (2 * j + (g >> 2)) * 4) & vmask;
+        const uint32_t b0 = as_u32(__hmul2(pa, as_half2(e4m3x2_f16x2(sw))));
+        const uint32_t b1 = as_u32(__hmul2(pb, as_half2(e4m3x2_hi_f16x2(sw))));
+        if (j == 0) {
+          mma_f16(o[0], e2m1x2_f16x2<0>(lo01), e2m1x2_f16x2<1>(lo01), e2m1x2_f16x2<0>(lo23), e2m1x2_f16x2<1>(lo23), b0, b1);
+          mma_f16(o[1], e2m1x2_f16x2<0>(hi01), e2m1x2_f16x2<1>(hi01), e2m1x2_f16x2<0>(hi23), e2m1x2_f16x2<1>(hi23), b0, b1);
+        } else {
+          mma_f16(o[2], e2m1x2_f16x2<2>(lo01), e2m1x2_f16x2<3>(lo01), e2m1x2_f16x2<2>(lo23), e2m1x2_f16x2<3>(lo23), b0, b1);
+          mma_f16(o[3], e2m1x2_f16x2<2>(hi01), e2m1x2_f16x2<3>(hi01), e2m1x2_f16x2<2>(hi23), e2m1x2_f16x2<3>(hi23), b0, b1);
         }
       }
-      s[0] *= qf0;
-      s[1] *= qf1;
-      s[2] *= qf0;
-      s[3] *= qf1;
-
-      // Positions outside [kbeg, L): no weight, and their V scales (any bytes,
-      // even NaN) read as zero.
-      uint32_t vmask = 0xffffffffu;
-      if (pos0 < kbeg || pos0 + kKv4Group > L) {
-        auto seen = [&](int m) { return pos0 + m >= kbeg && pos0 + m < L; };
-        if (!seen(g)) s[0] = s[1] = -INFINITY;
-        if (!seen(g + 8)) s[2] = s[3] = -INFINITY;
-        vmask = (seen(2 * t) ? 0xffu : 0u) | (seen(2 * t + 1) ? 0xff00u : 0u) | (seen(2 * t + 8) ? 0xff0000u : 0u) |
-                (seen(2 * t + 9) ? 0xff000000u : 0u);
+    } else {
+      const uint4 v4 = *reinterpret_cast<const uint4*>(vs);
+      const uint32_t vsw[4] = {v4.x & vmask, v4.y & vmask, v4.z & vmask, v4.w & vmask};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t b0 = as_u32(__hmul2(pa, as_half2(e4m3x2_f16x2(vsw[w]))));
+        const uint32_t b1 = as_u32(__hmul2(pb, as_half2(e4m3x2_hi_f16x2(vsw[w]))));
+        switch (w) {
+          case 0: mma_f16(o[0], e2m1x2_f16x2<0>(lo01), e2m1x2_f16x2<0>(hi01), e2m1x2_f16x2<0>(lo23), e2m1x2_f16x2<0>(hi23), b0, b1); break;
+          case 1: mma_f16(o[1], e2m1x2_f16x2<1>(lo01), e2m1x2_f16x2<1>(hi01), e2m1x2_f16x2<1>(lo23), e2m1x2_f16x2<1>(hi23), b0, b1); break;
+          case 2: mma_f16(o[2], e2m1x2_f16x2<2>(lo01), e2m1x2_f16x2<2>(hi01), e2m1x2_f16x2<2>(lo23), e2m1x2_f16x2<2>(hi23), b0, b1); break;
+          default: mma_f16(o[3], e2m1x2_f16x2<3>(lo01), e2m1x2_f16x2<3>(hi01), e2m1x2_f16x2<3>(lo23), e2m1x2_f16x2<3>(hi23), b0, b1); break;
+        }
       }
+    }
+  };
+  // The output of this lane's x-th of 2 PW element pairs: elements d, d + 1 (of
+  // the head) of heads h0 and h0 + 1.
+  auto out_pairs = [&](float (*o)[4], auto&& put) {
+#pragma unroll
+    for (int x = 0; x < PW * 4; ++x) {
+      if constexpr (PAIR) {  // products 2j and 2j + 1: even and odd elements of block 2j (t < 2) or 2j + 1
+        if (x & 1) continue;
+        const int d = vpiece * 64 + (x + (t >> 1)) * 16 + 2 * g;
+        const bool up = t >= 2;
+        put(d, make_float2(up ? o[x][2] : o[x][0], up ? o[x + 1][2] : o[x + 1][0]),
+            make_float2(up ? o[x][3] : o[x][1], up ? o[x + 1][3] : o[x + 1][1]));
+      } else {
+        const int d = vpiece * 64 + x * 16 + 2 * g;
+        put(d, make_float2(o[x][0], o[x][2]), make_float2(o[x][1], o[x][3]));
+      }
+    }
+  };
+  auto part_at = [&](int n) { return smem + (n % SLOTS) * C::SLOT_B; };
+  auto wait_part = [&](int n) { return warp_wait(smem_u32(&s_bar[n % SLOTS]), (n / SLOTS) & 1, a.err, &s_abort); };
 
-      float top0 = fmaxf(s[0], s[2]), top1 = fmaxf(s[1], s[3]);
-      if (__any_sync(0xffffffffu, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
+  int k = 0;  // step of the share
+  while (true) {
+    // ---- a unit (or the part of one in this share) begins
+    const int r0 = s_cp.first + s_cp.off;                  // first record
+    const int nrec = min(s_cp.n - s_cp.off, s_cp.left);
+    int L, kbeg;
+    {
+      const Kv4Seq seq = seq_of(a, s_cp.b);
+      L = seq.L;
+      kbeg = seq.kbeg;
+    }
+    // q fragments: lane (column g, t) holds elements 4t .. 4t+3 of every 16, two
+    // blocks side by side, zeros in columns without a head (and, two blocks to a
+    // product, where the other block's elements stand); each head scaled by the
+    // power of two that brings its largest element into [1, 2).
+    {
+      const __nv_bfloat16* q =
+          static_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(s_cp.b) * a.H + s_cp.kvh * G) * HD;
+#pragma unroll 1
+      for (int h = warp; h < GM; h += W) {
+        constexpr int PER = HD / 32;  // elements per lane, consecutive
+        float x[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = 0.0f;
+        if (h < G) load_elems<PER>(q + h * HD + lane * PER, x);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+        for (int x2 = 16; x2 > 0; x2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x2));
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        e = top > 0.0f ? min(max(e, -120), 120) : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if (lane == 0) s_qf[h] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+          const int d = lane * PER + i;
+          const int blk = d >> 4, tt = (d >> 2) & 3, odd = (d >> 1) & 1;  // odd: elements 4t+2, 4t+3
+          const uint32_t v = pack_f16x2(x[i] * down, x[i + 1] * down);
+          uint32_t* at = reinterpret_cast<uint32_t*>(smem + C::Q_OFF + (blk >> 1) * 512);
+          if constexpr (PAIR) {  // column h + 4 (block 2j + 1), words {product 1: b0, b1; product 2: b0, b1}
+            const int up = blk & 1;
+            *reinterpret_cast<uint2*>(at + ((h + 4 * up) * 4 + tt) * 4 + odd * 2) = up ? make_uint2(0u, v) : make_uint2(v, 0u);
+          } else {
+            at[(h * 4 + tt) * 4 + (blk & 1) * 2 + odd] = v;
+          }
+        }
+      }
+    }
+    float o[PW * 4][4];
+#pragma unroll
+    for (int i = 0; i < PW * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m0 = kNoKey, m1 = kNoKey, l0 = 0.0f, l1 = 0.0f;  // heads h0 and h0 + 1
+    __syncthreads();
+    const float qf0 = s_qf[h0], qf1 = s_qf[h0 + 1];
+
+#pragma unroll 1
+    for (int done = 0; done < nrec; done += STEP, ++k) {
+      const int base = r0 + done, nhere = min(STEP, nrec - done);
+      // a step that lies wholly inside [kbeg, L) and the share needs no masks
+      const bool edge = base * kKv4Group < kbeg || (base + STEP) * kKv4Group > L || nhere < STEP;
+      // ---- scores of this warp's records
+      float s[RW][4];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+      if (wait_part(2 * k)) {
+        const uint8_t* kpart = part_at(2 * k) + qrec * C::HALF_B;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+#pragma unroll
+          for (int p = 0; p < C::NP; ++p) score_piece(s[i], kpart + i * C::HALF_B, p);
+          if constexpr (PAIR) {  // the two blocks' columns
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[i][x] += __shfl_xor_sync(0xffffffffu, s[i][x], 2);
+          }
+        }
+      }
+      // ---- their probabilities
+      float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        s[i][0] *= qf0;
+        s[i][1] *= qf1;
+        s[i][2] *= qf0;
+        s[i][3] *= qf1;
+        if (edge) {  // positions outside [kbeg, L), and records past the share: no weight
+          const int pos = (base + qrec + i) * kKv4Group + g;
+          const bool in = qrec + i < nhere;
+          if (!in || pos < kbeg || pos >= L) s[i][0] = s[i][1] = -INFINITY;
+          if (!in || pos + 8 < kbeg || pos + 8 >= L) s[i][2] = s[i][3] = -INFINITY;
+        }
+        top0 = fmaxf(top0, fmaxf(s[i][0], s[i][2]));
+        top1 = fmaxf(top1, fmaxf(s[i][1], s[i][3]));
+      }
+      uint2* pbuf = reinterpret_cast<uint2*>(smem + C::P_OFF) + (k & 1) * STEP * 32;
+      float ps0, ps1;
+      auto probabilities = [&]() {
+        const float ref0 = m0 - kShift, ref1 = m1 - kShift;
+        ps0 = ps1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const float p0 = ex2_approx(s[i][0] - ref0), p1 = ex2_approx(s[i][1] - ref1);
+          const float p2 = ex2_approx(s[i][2] - ref0), p3 = ex2_approx(s[i][3] - ref1);
+          ps0 += p0 + p2;
+          ps1 += p1 + p3;
+          // head g; positions 2t, 2t+1 and 2t+8, 2t+9
+          pbuf[(qrec + i) * 32 + lane] =
+              make_uint2(transpose8x8(pack_f16x2(p0, p1)), transpose8x8(pack_f16x2(p2, p3)));
+        }
+      };
+      probabilities();
+      const bool any_over = __syncthreads_or(top0 > m0 + kSlack || top1 > m1 + kSlack);
+      // A step with absent blocks (scored from whatever their buffers hold) or
+      // with scores far above the reference is weighed again.
+      const uint32_t ok = s_ok[k & 3];
+      const bool gaps = ok != (1u << nhere) - 1u;
+      if (any_over || gaps) {
+        top0 = top1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          if (!((ok >> (qrec + i)) & 1u)) s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
+          top0 = fmaxf(top0, fmaxf(s[i][0], s[i][2]));
+          top1 = fmaxf(top1, fmaxf(s[i][1], s[i][3]));
+        }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
           top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, x));
           top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, x));
         }
-        const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+        if (g == 0) {
+          s_top[warp * kHeads + 2 * t] = top0;
+          s_top[warp * kHeads + 2 * t + 1] = top1;
+        }
+        __syncthreads();
+        float n0 = m0, n1 = m1;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          n0 = fmaxf(n0, s_top[w * kHeads + 2 * t]);
+          n1 = fmaxf(n1, s_top[w * kHeads + 2 * t + 1]);
+        }
         const float f0 = ex2_approx(m0 - n0), f1 = ex2_approx(m1 - n1);
         m0 = n0;
         m1 = n1;
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
+        for (int x = 0; x < PW * 4; ++x) {
           o[x][0] *= f0;
           o[x][1] *= f1;
           o[x][2] *= f0;
           o[x][3] *= f1;
         }
+        probabilities();
+        __syncthreads();
       }
-      const float r0 = m0 - kShift, r1 = m1 - kShift;
-      const float p0 = ex2_approx(s[0] - r0), p1 = ex2_approx(s[1] - r1);
-      const float p2 = ex2_approx(s[2] - r0), p3 = ex2_approx(s[3] - r1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      const __half2 pa = as_half2(transpose8x8(pack_f16x2(p0, p1)));  // head g, positions 2t, 2t+1
-      const __half2 pb = as_half2(transpose8x8(pack_f16x2(p2, p3)));  // 2t+8, 2t+9
+      l0 += ps0;
+      l1 += ps1;
 
-      // O^T += V^T (P s)^T
+      // ---- refill the buffers of the last step's V and of this step's K
+      if (warp == 0) {
+        if (k > 0) issue();
+        issue();
+      }
+
+      // ---- P V of the step for this warp's pieces
+      // V scales of positions outside [kbeg, L) and of absent records may be any
+      // bytes, even NaN: they read as zero
+      const bool masked = edge || gaps;
+      auto vmask_of = [&](int i) -> uint32_t {
+        if (!masked) return 0xffffffffu;
+        if (!((ok >> i) & 1u)) return 0u;
+        const int pos0 = (base + i) * kKv4Group;
+        auto seen = [&](int m) { return pos0 + m >= kbeg && pos0 + m < L; };
+        return (seen(2 * t) ? 0xffu : 0u) | (seen(2 * t + 1) ? 0xff00u : 0u) | (seen(2 * t + 8) ? 0xff0000u : 0u) |
+               (seen(2 * t + 9) ? 0xff000000u : 0u);
+      };
+      if (wait_part(2 * k + 1)) {
+        const uint8_t* vpart = part_at(2 * k + 1);
 #pragma unroll
-      for (int p = 0; p < R::NP; ++p) {
-        const uint4 vc = *reinterpret_cast<const uint4*>(rec + R::VC + p * 512 + lane * 16);
-        const uint4 vs = *reinterpret_cast<const uint4*>(rec + R::VS + p * 64 + t * 16);
-        // pairs of positions side by side, for the even and the odd elements
-        const uint32_t lo01 = (vc.x & 0x0f0f0f0fu) | ((vc.y << 4) & 0xf0f0f0f0u);
-        const uint32_t hi01 = ((vc.x >> 4) & 0x0f0f0f0fu) | (vc.y & 0xf0f0f0f0u);
-        const uint32_t lo23 = (vc.z & 0x0f0f0f0fu) | ((vc.w << 4) & 0xf0f0f0f0u);
-        const uint32_t hi23 = ((vc.z >> 4) & 0x0f0f0f0fu) | (vc.w & 0xf0f0f0f0u);
-        const uint32_t vsw[4] = {vs.x & vmask, vs.y & vmask, vs.z & vmask, vs.w & vmask};
+        for (int ii = 0; ii < STEP / KS; ++ii) {
+          const int i = vrec0 + ii * KS;
+          const uint2 pp = pbuf[i * 32 + lane];
+          const uint32_t vmask = vmask_of(i);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t b0 = as_u32(__hmul2(pa, as_half2(e4m3x2_f16x2(vsw[w]))));
-          const uint32_t b1 = as_u32(__hmul2(pb, as_half2(e4m3x2_hi_f16x2(vsw[w]))));
-          float(&d)[4] = o[4 * p + w];
-          switch (w) {
-            case 0: mma_f16(d, e2m1x2_f16x2<0>(lo01), e2m1x2_f16x2<0>(hi01), e2m1x2_f16x2<0>(lo23), e2m1x2_f16x2<0>(hi23), b0, b1); break;
-            case 1: mma_f16(d, e2m1x2_f16x2<1>(lo01), e2m1x2_f16x2<1>(hi01), e2m1x2_f16x2<1>(lo23), e2m1x2_f16x2<1>(hi23), b0, b1); break;
-            case 2: mma_f16(d, e2m1x2_f16x2<2>(lo01), e2m1x2_f16x2<2>(hi01), e2m1x2_f16x2<2>(lo23), e2m1x2_f16x2<2>(hi23), b0, b1); break;
-            default: mma_f16(d, e2m1x2_f16x2<3>(lo01), e2m1x2_f16x2<3>(hi01), e2m1x2_f16x2<3>(lo23), e2m1x2_f16x2<3>(hi23), b0, b1); break;
-          }
+          for (int pi = 0; pi < PW; ++pi) add_piece(o + pi * 4, vpart + i * C::HALF_B, vpiece + pi, pp, vmask);
         }
       }
     }
-    __syncwarp();  // every lane is done with the stage
-    done = k + 1;
-    if (k + NST < mine) issue(k + NST);
-  }
-  if (aborted) {  // copies of this warp still in flight
-    for (int k = done; k < mine && k < done + NST; ++k) warp_wait(smem_u32(&wbar[k % NST]), (k / NST) & 1, nullptr);
-  }
 
-  // The warps' states through shared memory (the rings are free now).
+    // ---- the unit's part in this share ends
 #pragma unroll
-  for (int x = 4; x < 32; x <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-  }
-  if (g == 0) {
-    s_m[warp * kHeads + 2 * t] = m0;
-    s_m[warp * kHeads + 2 * t + 1] = m1;
-    s_l[warp * kHeads + 2 * t] = l0;
-    s_l[warp * kHeads + 2 * t + 1] = l1;
-  }
-  __syncthreads();
-  float M0 = s_m[2 * t], M1 = s_m[2 * t + 1];
-#pragma unroll
-  for (int w = 1; w < NW; ++w) {
-    M0 = fmaxf(M0, s_m[w * kHeads + 2 * t]);
-    M1 = fmaxf(M1, s_m[w * kHeads + 2 * t + 1]);
-  }
-  const float f0 = ex2_approx(m0 - M0), f1 = ex2_approx(m1 - M1);
-  float* os = reinterpret_cast<float*>(smem) + warp * kHeads * HD;
-#pragma unroll
-  for (int x = 0; x < NB; ++x) {
-    const int d = x * 16 + 2 * g;
-    if (2 * t < G) *reinterpret_cast<float2*>(os + (2 * t) * HD + d) = make_float2(o[x][0] * f0, o[x][2] * f0);
-    if (2 * t + 1 < G) *reinterpret_cast<float2*>(os + (2 * t + 1) * HD + d) = make_float2(o[x][1] * f1, o[x][3] * f1);
-  }
-  __syncthreads();
-  const size_t pbase = (static_cast<size_t>(b) * a.H + kvh * G) * a.nsplit;
-  for (int idx = threadIdx.x; idx < G * HD / 4; idx += NW * 32) {
-    const int h = idx * 4 / HD, d = idx * 4 % HD;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float M = kNoKey, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * kHeads + h) * HD + d);
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-      M = fmaxf(M, s_m[w * kHeads + h]);
+    for (int x = 4; x < 32; x <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
     }
+    if (g == 0) {
+      s_l[warp * kHeads + 2 * t] = l0;
+      s_l[warp * kHeads + 2 * t + 1] = l1;
+    }
+    float* red = reinterpret_cast<float*>(smem + C::RED_OFF);  // [KS][head][HD]
+    if constexpr (KS > 1) {
+      if (vrec0 > 0)
+        out_pairs(o, [&](int d, float2 u, float2 v) {
+          float* r = red + vrec0 * kHeads * HD + d;
+          *reinterpret_cast<float2*>(r + h0 * HD) = u;
+          *reinterpret_cast<float2*>(r + (h0 + 1) * HD) = v;
+        });
+    }
+    __syncthreads();
+    l0 = l1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) l += s_l[w * kHeads + h] * ex2_approx(s_m[w * kHeads + h] - M);
-    if (nsplit == 1) {
+    for (int w = 0; w < W; ++w) {
+      l0 += s_l[w * kHeads + h0];
+      l1 += s_l[w * kHeads + h0 + 1];
+    }
+    const Kv4Place cp = s_cp;
+    const long long unit0 = s_unit0;
+    const int c_first = static_cast<int>(unit0 / share), c_last = static_cast<int>((unit0 + cp.n - 1) / share);
+    const bool whole = c_first == c_last;
+    const int slot = part_slot(c_first, static_cast<int>(blockIdx.x) - c_first);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(cp.b) * a.H + cp.kvh * G) * HD;
+    if (vrec0 == 0) {
       // (l is zero only where no key was present; a NaN stays one)
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const float f[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      store_elems<4>(out + h * HD + d, f);
-    } else {
-      const size_t pr = pbase + static_cast<size_t>(h) * a.nsplit + split;
-      *reinterpret_cast<float4*>(a.ws_o + pr * HD + d) = acc;
-      if (d == 0) {
-        a.ws_m[pr] = M;
-        a.ws_l[pr] = l;
+      const float i0 = l0 == 0.0f ? 0.0f : 1.0f / l0, i1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
+      out_pairs(o, [&](int d, float2 u, float2 v) {
+        if constexpr (KS > 1) {
+#pragma unroll
+          for (int y = 1; y < KS; ++y) {
+            const float* r = red + y * kHeads * HD + d;
+            const float2 ru = *reinterpret_cast<const float2*>(r + h0 * HD);
+            const float2 rv = *reinterpret_cast<const float2*>(r + (h0 + 1) * HD);
+            u.x += ru.x;
+            u.y += ru.y;
+            v.x += rv.x;
+            v.y += rv.y;
+          }
+        }
+        if (whole) {
+          if (h0 < G) *reinterpret_cast<uint32_t*>(out + h0 * HD + d) = pack_bf16x2(u.x * i0, u.y * i0);
+          if (h0 + 1 < G) *reinterpret_cast<uint32_t*>(out + (h0 + 1) * HD + d) = pack_bf16x2(v.x * i1, v.y * i1);
+        } else {
+          float* w = a.ws_o + static_cast<size_t>(slot) * G * HD + d;
+          if (h0 < G) *reinterpret_cast<float2*>(w + h0 * HD) = u;
+          if (h0 + 1 < G) *reinterpret_cast<float2*>(w + (h0 + 1) * HD) = v;
+        }
+      });
+    }
+    if (!whole) {
+      if (warp == 0 && g == 0) {
+        if (h0 < G) a.ws_ml[slot * kHeads + h0] = make_float2(m0, l0);
+        if (h0 + 1 < G) a.ws_ml[slot * kHeads + h0 + 1] = make_float2(m1, l1);
+      }
+      // Up to kFan parts are merged at once by the CTA that completes them; more
+      // go through one level of merges of kFan neighbours, each left in the
+      // slot of its first part.
+      const int nparts = c_last - c_first + 1;
+      unsigned* ticket = a.tickets + c_first;  // (a CTA's share has one unit that begins in it and goes on)
+      int first = 0, step = 1, n = nparts;
+      bool final = true;
+      if (nparts > kFan) {
+        first = (static_cast<int>(blockIdx.x) - c_first) / kFan * kFan;
+        n = min(kFan, nparts - first);
+        ticket = a.tickets + kKv4MaxCtas + part_slot(c_first, first);
+        final = false;
+      }
+#pragma unroll 1
+      while (true) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          s_last = atomicAdd(ticket, 1u) == static_cast<unsigned>(n - 1);
+          if (s_last) *ticket = 0u;  // ready for the next call
+        }
+        __syncthreads();
+        if (!s_last) break;
+        __threadfence();
+        merge_parts<HD, W>(a, c_first, first, step, n, G, final ? out : nullptr, s_w);
+        if (final) break;
+        ticket = a.tickets + c_first;
+        first = 0;
+        step = kFan;
+        n = (nparts + kFan - 1) / kFan;
+        final = true;
       }
     }
-  }
-  if (nsplit == 1) return;
-
-  __threadfence();
-  __syncthreads();
-  unsigned* ticket = a.tickets + unit;
-  if (threadIdx.x == 0) s_last = atomicAdd(ticket, 1u) == static_cast<unsigned>(nsplit - 1);
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  for (int h = warp; h < G; h += NW) {
-    const size_t p0 = pbase + static_cast<size_t>(h) * a.nsplit;
-    float M = kNoKey;
-    for (int i = lane; i < nsplit; i += 32) M = fmaxf(M, __ldcg(a.ws_m + p0 + i));
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    float l = 0.0f;
-    for (int i = lane; i < nsplit; i += 32) {
-      const float w = ex2_approx(__ldcg(a.ws_m + p0 + i) - M);
-      s_w[h * kMaxSplits + i] = w;
-      l += w * __ldcg(a.ws_l + p0 + i);
+    if (cp.left <= nrec) break;
+    __syncthreads();  // (every thread has read the place)
+    if (tid == 0) {
+      Kv4Place p = cp;
+      advance(p, nrec);
+      s_unit0 = unit0 + cp.n;
+      s_cp = p;
     }
-    l = warp_sum(l);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    __syncwarp();
-    for (int i = lane; i < nsplit; i += 32) s_w[h * kMaxSplits + i] *= inv;
+    __syncthreads();
   }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < G * HD / 4; idx += NW * 32) {
-    const int h = idx * 4 / HD, d = idx * 4 % HD;
-    const float* src = a.ws_o + (pbase + static_cast<size_t>(h) * a.nsplit) * HD + d;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-    for (int i = 0; i < nsplit; ++i) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(i) * HD));
-      const float w = s_w[h * kMaxSplits + i];
-      acc[0] = fmaf(w, v.x, acc[0]);
-      acc[1] = fmaf(w, v.y, acc[1]);
-      acc[2] = fmaf(w, v.z, acc[2]);
-      acc[3] = fmaf(w, v.w, acc[3]);
-    }
-    store_elems<4>(out + h * HD + d, acc);
+  // After an abandoned wait: the copies still in flight.
+  if (s_abort && warp == 0) {
+    for (int n = max(0, issued - SLOTS); n < issued; ++n)
+      warp_wait(smem_u32(&s_bar[n % SLOTS]), (n / SLOTS) & 1, nullptr);
   }
-  if (threadIdx.x == 0) *ticket = 0u;  // ready for the next call
 }
 
-template <int HD>
-cudaError_t launch_h(const Kv4DecodeArgs& a, cudaStream_t s) {
+template <int HD, int GM>
+cudaError_t launch_hg(const Kv4DecodeArgs& a, cudaStream_t s) {
   using C = Kv4Cfg<HD>;
-  const cudaError_t e = set_smem_limit_once<kv4_decode_kernel<HD>>(C::SMEM_B);
+  const cudaError_t e = set_smem_limit_once<kv4_decode_kernel<HD, GM>>(C::SMEM_B);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hkv * a.nsplit));
-  cfg.blockDim = dim3(C::NW * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.nctas));
+  cfg.blockDim = dim3(C::W * 32);
   cfg.dynamicSmemBytes = C::SMEM_B;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -452,7 +764,36 @@ cudaError_t launch_h(const Kv4DecodeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<HD>, a);
+  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<HD, GM>, a);
+}
+
+template <int HD>
+cudaError_t launch_h(const Kv4DecodeArgs& a, cudaStream_t s) {
+  if (a.H <= 4 * a.Hkv) return launch_hg<HD, 4>(a, s);
+  if constexpr (HD <= 256) return launch_hg<HD, 8>(a, s);
+  return cudaErrorInvalidValue;
+}
+
+template <int HD>
+Kv4DecodePlan plan_h(int window, int H, int Hkv, int B, int max_seq_len) {
+  using C = Kv4Cfg<HD>;
+  const int span = window > 0 && window < max_seq_len ? window : max_seq_len;
+  // a window that starts inside a record touches one more
+  const long long groups = (static_cast<long long>(span) + 15) / 16 + (span < max_seq_len ? 1 : 0);
+  const long long units = static_cast<long long>(B) * Hkv;
+  // as many CTAs as are resident, each with a step or more
+  long long n = (units * groups + C::STEP - 1) / C::STEP;
+  const long long slots = static_cast<long long>(sm_count()) * C::MINB;
+  if (n > slots) n = slots;
+  static_assert(kKv4MaxCtas <= kFan * kMaxLevel, "two levels of merges");
+  if (n > kKv4MaxCtas) n = kKv4MaxCtas;
+  Kv4DecodePlan p;
+  p.nctas = static_cast<int>(n);
+  const size_t G = static_cast<size_t>(H / Hkv);
+  p.o_bytes = (2 * static_cast<size_t>(n) * G * HD * 4 + 255) / 256 * 256;
+  p.ml_bytes = (2 * static_cast<size_t>(n) * kHeads * 8 + 255) / 256 * 256;
+  p.ws_bytes = n > 1 ? kKv4TicketBytes + p.ml_bytes + p.o_bytes : 0;
+  return p;
 }
 
 }  // namespace
@@ -468,31 +809,12 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s) {
 }
 
 Kv4DecodePlan kv4_decode_plan(int window, int hd, int H, int Hkv, int B, int max_seq_len) {
-  Kv4DecodePlan p;
-  const int span = window > 0 && window < max_seq_len ? window : max_seq_len;
-  // a window that starts inside a record touches one more
-  const int groups = static_cast<int>((static_cast<long long>(span) + 15) / 16) + (span < max_seq_len ? 1 : 0);
-  const long long units = static_cast<long long>(B) * Hkv;
-  const int slots = sm_count() * (hd >= 512 ? 2 : 4);
-  // Two waves of CTAs even out ragged lengths; a split has at least two
-  // records per warp.
-  long long want = (2LL * slots + units - 1) / units;
-  const int most = (groups + 7) / 8;
-  if (want > most) want = most;
-  if (want > kMaxSplits) want = kMaxSplits;
-  if (want < 1) want = 1;
-  p.chunk = static_cast<int>((groups + want - 1) / want);
-  p.nsplit = (groups + p.chunk - 1) / p.chunk;
-  if (p.nsplit <= 1) {
-    p.o_bytes = p.m_bytes = p.t_bytes = p.ws_bytes = 0;
-  } else {
-    const size_t np = static_cast<size_t>(B) * H * p.nsplit;
-    p.o_bytes = (np * hd * 4 + 255) / 256 * 256;
-    p.m_bytes = (np * 4 + 255) / 256 * 256;
-    p.t_bytes = (static_cast<size_t>(units) * 4 + 255) / 256 * 256;
-    p.ws_bytes = p.o_bytes + 2 * p.m_bytes + p.t_bytes;
+  switch (hd) {
+    case 64: return plan_h<64>(window, H, Hkv, B, max_seq_len);
+    case 128: return plan_h<128>(window, H, Hkv, B, max_seq_len);
+    case 256: return plan_h<256>(window, H, Hkv, B, max_seq_len);
+    default: return plan_h<512>(window, H, Hkv, B, max_seq_len);
   }
-  return p;
 }
 
 }  // namespace g4

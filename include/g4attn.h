@@ -482,8 +482,10 @@ size_t g4_kv4_decode_workspace_size(const g4_layer_params* params, int32_t B, in
  *                first), clamped into [0, max_seq_len].  A sequence of no
  *                keys gets an output of zeros.
  *   max_seq_len  1 .. max_blocks * block_size
- * q, out, workspace (zero-filled once, left ready by every call, not shared
- * by calls that overlap) as g4_attn_decode.  q.k and P.V run on
+ * q and out as g4_attn_decode.  The workspace is zero-filled once before its
+ * first use; every call leaves it ready for the next, whatever that call's
+ * layer, batch and lengths (size it for the largest).  Calls that overlap on
+ * the GPU need a workspace each.  q.k and P.V run on
  * tensor cores from fp16 operands with float32 sums: keys and values are
  * exact in fp16, q is scaled by a power of two per head, and a probability
  * times its value's scale is rounded to 11 bits.
