@@ -115,6 +115,38 @@ g4_status resolve_src(const g4_layer_params* p, const g4_kv_cache* caches, int n
   return G4_OK;
 }
 
+// inv_freq[j] = theta^(-2j / hd) in float64, stored as float32, for the rotated
+// pairs j < n_rot, zero past them.  The powers of a layer's constants take
+// longer on the host than its launch, so a thread keeps the tables of the last
+// few constants it has met (a stack alternates between two).
+void rope_table(const g4_layer_params* p, int* n_rot_out, float* inv_freq) {
+  struct Table {
+    float theta;
+    int hd, n_rot;
+    float f[g4::kMaxHalf];
+  };
+  static thread_local Table kept[4] = {};
+  static thread_local int oldest = 0;
+  const int hd = p->head_dim, half = hd / 2;
+  int n_rot = static_cast<int>(floor(static_cast<double>(hd) * static_cast<double>(p->rotary_fraction) / 2.0));
+  if (n_rot > half) n_rot = half;
+  *n_rot_out = n_rot;
+  const Table* t = nullptr;
+  for (const Table& k : kept)
+    if (k.hd == hd && k.n_rot == n_rot && k.theta == p->theta) t = &k;
+  if (t == nullptr) {
+    Table* k = &kept[oldest];
+    oldest = (oldest + 1) % 4;
+    k->theta = p->theta;
+    k->hd = hd;
+    k->n_rot = n_rot;
+    for (int j = 0; j < half; ++j)
+      k->f[j] = j < n_rot ? static_cast<float>(pow(static_cast<double>(p->theta), -2.0 * j / hd)) : 0.0f;
+    t = k;
+  }
+  memcpy(inv_freq, t->f, static_cast<size_t>(half) * sizeof(float));
+}
+
 g4_status cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return ok();
   return fail(G4_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -215,13 +247,7 @@ g4_status g4_kv_append_normrope(const g4_layer_params* params, const g4_kv_cache
   a.tok_per_cta = T >= 16 ? (B < 8 ? B : 8) : 1;
   const long long ctas = static_cast<long long>(T) * ((B + a.tok_per_cta - 1) / a.tok_per_cta);
   a.rows_per_cta = ctas >= 1024 ? nrows : 4;
-  // inv_freq[j] = theta^(-2j/hd) in float64, stored as float32; zero past the rotated pairs.
-  const int half = a.hd / 2;
-  int n_rot = static_cast<int>(floor(static_cast<double>(a.hd) * static_cast<double>(params->rotary_fraction) / 2.0));
-  if (n_rot > half) n_rot = half;
-  a.n_rot = n_rot;
-  for (int j = 0; j < half; ++j)
-    a.inv_freq[j] = j < n_rot ? static_cast<float>(pow(static_cast<double>(params->theta), -2.0 * j / a.hd)) : 0.0f;
+  rope_table(params, &a.n_rot, a.inv_freq);
   return cuda_status(g4::launch_append(a, params->dtype, static_cast<cudaStream_t>(stream)), "append launch");
 }
 
@@ -469,14 +495,7 @@ g4_status decode_common(const g4_layer_params* params, const g4_kv_cache* caches
       a.cache_k = caches[layer].k;
       a.cache_v = caches[layer].v;
     }
-    const int half = a.hd / 2;
-    int n_rot =
-        static_cast<int>(floor(static_cast<double>(a.hd) * static_cast<double>(params->rotary_fraction) / 2.0));
-    if (n_rot > half) n_rot = half;
-    a.n_rot = n_rot;
-    for (int j = 0; j < half; ++j)
-      a.inv_freq[j] =
-          j < n_rot ? static_cast<float>(pow(static_cast<double>(params->theta), -2.0 * j / a.hd)) : 0.0f;
+    rope_table(params, &a.n_rot, a.inv_freq);
   }
   if (plan.win)
     return cuda_status(g4::launch_decode_win(a, static_cast<cudaStream_t>(stream)), "windowed decode launch");
@@ -581,12 +600,7 @@ g4_status g4_qkv_project_append(const g4_layer_params* params, const g4_kv_cache
   a.q_w = q_norm_w;
   a.positions = positions;
   a.q_out = q_out;
-  const int half = hd / 2;
-  int n_rot = static_cast<int>(floor(static_cast<double>(hd) * static_cast<double>(params->rotary_fraction) / 2.0));
-  if (n_rot > half) n_rot = half;
-  a.n_rot = n_rot;
-  for (int j = 0; j < half; ++j)
-    a.inv_freq[j] = j < n_rot ? static_cast<float>(pow(static_cast<double>(params->theta), -2.0 * j / hd)) : 0.0f;
+  rope_table(params, &a.n_rot, a.inv_freq);
   int* err = device_error_ptr();
   if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
   a.err = err;
@@ -740,7 +754,7 @@ g4_status g4_kv4_append_normrope(const g4_layer_params* params, const g4_kv4_poo
   if (!aligned16(q_in) || !aligned16(q_out) || !aligned16(q_norm_w))
     return fail(G4_ERR_INVALID_ARG, "q_in, q_out and q_norm_w must be 16-byte aligned");
   const bool shared = params->kv_share_src >= 0;
-  g4::Kv4AppendArgs a;
+  g4::AppendArgs a;
   memset(&a, 0, sizeof(a));
   if (shared) {
     if (k_in != nullptr || v_in != nullptr || k_norm_w != nullptr)
@@ -755,7 +769,7 @@ g4_status g4_kv4_append_normrope(const g4_layer_params* params, const g4_kv4_poo
     const g4_kv4_pool* c = nullptr;
     st = kv4_resolve_src(params, pools, n_layers, layer, &c);
     if (st != G4_OK) return st;
-    a.data = static_cast<uint8_t*>(c->data);
+    a.cache_k = c->data;
     a.n_slots = c->n_blocks * c->block_size;
     a.block_shift = log2_of(c->block_size);
     a.k_mul = static_cast<float>(ldexp(1.0, -c->k_exp));
@@ -771,20 +785,21 @@ g4_status g4_kv4_append_normrope(const g4_layer_params* params, const g4_kv4_poo
   a.q_w = q_norm_w;
   a.positions = positions;
   a.q_out = q_out;
-  a.tokens = static_cast<int>(tokens);
+  a.B = B;
+  a.T = T;
   a.H = params->n_heads;
   a.Hkv = params->n_kv_heads;
   a.hd = params->head_dim;
   a.eps = params->eps;
+  // Tokens at the same t of a few sequences share a CTA (and, where their
+  // positions agree, a cos/sin table); small launches split the rows.  4 tokens
+  // measured 1-4 % faster than 8 (whose CTAs are fewer than three waves at
+  // 8 x 2048 tokens) and 10 % faster than 1 (no rows to load ahead).
   const int nrows = a.H + (shared ? 0 : 2 * a.Hkv);
-  // small launches split a token's rows over CTAs
-  a.rows_per_cta = tokens >= 1024 ? nrows : 4;
-  const int half = a.hd / 2;
-  int n_rot = static_cast<int>(floor(static_cast<double>(a.hd) * static_cast<double>(params->rotary_fraction) / 2.0));
-  if (n_rot > half) n_rot = half;
-  a.n_rot = n_rot;
-  for (int j = 0; j < half; ++j)
-    a.inv_freq[j] = j < n_rot ? static_cast<float>(pow(static_cast<double>(params->theta), -2.0 * j / a.hd)) : 0.0f;
+  a.tok_per_cta = T >= 16 ? (B < g4::kAppendMaxTokens ? B : g4::kAppendMaxTokens) : 1;
+  const long long ctas = static_cast<long long>(T) * ((B + a.tok_per_cta - 1) / a.tok_per_cta);
+  a.rows_per_cta = ctas >= 1024 ? nrows : 4;
+  rope_table(params, &a.n_rot, a.inv_freq);
   return cuda_status(g4::launch_kv4_append(a, static_cast<cudaStream_t>(stream)), "4-bit append launch");
 }
 

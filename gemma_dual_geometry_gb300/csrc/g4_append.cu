@@ -26,6 +26,10 @@
 //   3. the row's sum of squares in double-float (error-free splitting) and a
 //      double-float inverse rms, which decide the rest.
 //
+// The 4-bit cache's append (KV4) differs in where rows go: a row is finished in
+// shared memory, then a q row is copied out and a k or v row quantised by
+// kv4_store_row.
+//
 // Lane l of a warp owns elements [l*E, l*E + E) of the lower half and the
 // same offsets of the upper half (E = head_dim / 64), so each rotate_half
 // pair (j, j + head_dim/2) sits in one lane.  Each warp loads its next row
@@ -34,6 +38,7 @@
 
 #include "g4_device.cuh"
 #include "g4_internal.h"
+#include "g4_kv4.cuh"
 #include "g4_normrope.cuh"
 
 namespace g4 {
@@ -135,8 +140,120 @@ __device__ __forceinline__ void rotate_elems(float* oa, float* ob, const float* 
 // rounding is that of every value within e of it).
 __device__ __forceinline__ bool bf16_decided(float v, float e) { return fabsf(v - bf16_midpoint(v)) > e; }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ AppendArgs a) {
+// Where element d of a row that waits to be quantised lies: 64-element pieces
+// are 32 bytes apart, so that lanes of different pieces meet other banks.
+__host__ __device__ constexpr int kv4_row_at(int d) { return d + (d >> 6) * 16; }
+
+// Quantises a finished row (bf16 values in shared memory, by kv4_row_at) and
+// stores codes and scales of position m into its record.  Lane l takes the
+// HD / 32 elements from l HD / 32 on: a whole block of 16, or a part of one whose
+// other lanes it asks for the largest magnitude.  The code bytes of the 4
+// blocks that the record keeps side by side are then exchanged between their
+// lanes, so that each lane has bytes that lie together.
+//   The divisions x / s and max / 6 are products with a rounded reciprocal,
+// brought back by a rounding to 2^-12 (x / s, which is at most 12) or to 16
+// significant bits (max / 6).  That is as good as the exact quotient: x and max
+// have 8 significant bits, the numbers between which codes and scales change, times s
+// or 6, at most 7 (3 of a code times 4 of a scale; 5 of a scale times 2 of a 6), so
+// a quotient is one of those numbers or at least 2^-8 (relative) away, where the
+// products are off by 2^-22.
+template <int HD>
+__device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t* rec, int m, bool is_k, float mul,
+                                              int lane) {
+  constexpr int N = HD / 32;       // elements of this lane
+  constexpr int LPB = 16 / N;      // lanes per block
+  constexpr unsigned kAll = 0xffffffffu;
+  const int d0 = lane * N;
+  uint32_t w[N / 2];               // bf16 pairs
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(row + kv4_row_at(d0));
+  if constexpr (N >= 8) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = src[i];
+  }
+  // largest magnitude, as bits (NaN > infinity > the rest): 16-bit halves compare as integers
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+  for (int o = 1; o < LPB; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+  const bool finite = top < 0x7f80u;
+  const float q6 = __uint_as_float(top << 16) * mul * (1.0f / 6.0f);
+  const uint32_t byte = finite ? e4m3_byte(__uint_as_float((__float_as_uint(q6) + 0x80u) & ~0xffu)) : 0x7fu;
+  const float s = e4m3_value(byte);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv = s > 0.0f ? inv * mul : 0.0f;  // an all-zero block, or a NaN one: codes 0
+  const uint32_t sign = s > 0.0f ? 0x80000000u : 0u;
+  uint32_t code[(N + 7) / 8] = {};    // code bytes, in order
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    constexpr float kSnap = 0x1.8p11f;  // adding it rounds to a multiple of 2^-12
+    const float2 x = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+    float2 q = __fmul2_rn(x, make_float2(inv, inv));
+    q = __fadd2_rn(__fadd2_rn(q, make_float2(kSnap, kSnap)), make_float2(-kSnap, -kSnap));
+    // (a quotient that rounds to zero keeps its sign, except in a block without a scale)
+    code[i / 4] |= e2m1x2_byte(__uint_as_float(__float_as_uint(q.x) | (__float_as_uint(x.x) & sign)),
+                               __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(x.y) & sign)))
+                   << (8 * (i % 4));
+  }
+  if (lane % LPB == 0)
+    rec[is_k ? kv4_k_scale_at<HD>(m, d0) : kv4_v_scale_at<HD>(m, d0)] = static_cast<uint8_t>(byte);
+
+  const int blk = lane / LPB, p0 = blk / 4 * 64;  // its piece begins at element p0
+  if constexpr (HD >= 256) {
+    // the four blocks of a piece are lanes blk % 4 apart by LPB
+    const int b4 = blk & 3, h = lane % LPB;
+    if (is_k) {
+      if constexpr (HD == 512) {  // units of 2 bytes (t): 4 blocks x 4 units, transposed
+        const uint32_t got = __shfl_xor_sync(kAll, b4 < 2 ? code[1] : code[0], 2);
+        const uint32_t a0 = b4 < 2 ? code[0] : got, a1 = b4 < 2 ? got : code[1];  // units 0-1 or 2-3 of blocks b4 & 1, + 2
+        const uint32_t swap = __shfl_xor_sync(kAll, __byte_perm(a0, a1, b4 & 1 ? 0x5410 : 0x7632), 1);
+        const uint32_t mine = __byte_perm(a0, a1, b4 & 1 ? 0x7632 : 0x5410);
+        const uint2 out = b4 & 1 ? make_uint2(__byte_perm(swap, mine, 0x5410), __byte_perm(swap, mine, 0x7632))
+                                 : make_uint2(__byte_perm(mine, swap, 0x5410), __byte_perm(mine, swap, 0x7632));
+        *reinterpret_cast<uint2*>(rec + kv4_k_code_at<HD>(m, p0 + 4 * b4)) = out;  // unit t = b4 of blocks 0 .. 3
+      } else {  // the lane has units 2h, 2h + 1: pairs of blocks change one
+        const uint32_t got = __shfl_xor_sync(kAll, code[0], LPB);
+        const uint32_t out = b4 & 1 ? __byte_perm(got, code[0], 0x7632) : __byte_perm(code[0], got, 0x5410);
+        *reinterpret_cast<uint32_t*>(rec + kv4_k_code_at<HD>(m, p0 + (b4 & 2) * 16 + 4 * (2 * h + (b4 & 1)))) = out;
+      }
+    } else {
+      // 4 blocks x 4 bytes (of g), transposed: byte b4 of blocks 0 .. 3
+#pragma unroll
+      for (int i = 0; i < (HD == 512 ? 2 : 1); ++i) {
+        uint32_t c = code[i];
+        uint32_t got = __shfl_xor_sync(kAll, c, 2 * LPB);
+        c = b4 & 2 ? __byte_perm(got, c, 0x7632) : __byte_perm(c, got, 0x5410);  // bytes 0-1 or 2-3 of b4 & 1, + 2
+        got = __shfl_xor_sync(kAll, c, LPB);
+        c = b4 & 1 ? __byte_perm(got, c, 0x7351) : __byte_perm(c, got, 0x6240);
+        const int g = HD == 512 ? 4 * i + b4 : 4 * h + b4;
+        *reinterpret_cast<uint32_t*>(rec + kv4_v_code_at<HD>(m, p0 + 2 * g)) = c;
+      }
+    }
+  } else if constexpr (HD == 128) {
+    if (is_k) {
+      *reinterpret_cast<uint16_t*>(rec + kv4_k_code_at<HD>(m, d0)) = static_cast<uint16_t>(code[0]);
+    } else {
+      rec[kv4_v_code_at<HD>(m, d0)] = static_cast<uint8_t>(code[0]);
+      rec[kv4_v_code_at<HD>(m, d0 + 2)] = static_cast<uint8_t>(code[0] >> 8);
+    }
+  } else {
+    rec[is_k ? kv4_k_code_at<HD>(m, d0) : kv4_v_code_at<HD>(m, d0)] = static_cast<uint8_t>(code[0]);
+  }
+}
+
+template <typename T, int HD, bool KV4>
+__global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && KV4 ? 6 : 8) append_normrope_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int HALF = HD / 2;
   constexpr int E = HD / 64;
   constexpr bool kBF16 = sizeof(T) == 2;
@@ -144,8 +261,14 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
   constexpr float kErrAB = normrope_err_pair(kDFTrigErrUnits);
   constexpr float kErrO = normrope_err_out<2 * E>();
   constexpr float kErrR = normrope_err_r<2 * E>();
-  __shared__ DF s_cos[HALF];
-  __shared__ DF s_sin[HALF];
+  constexpr int kTabs = KV4 ? kAppendMaxTokens : 1;  // tables held at once
+  __shared__ DF s_cos_all[kTabs * HALF];
+  __shared__ DF s_sin_all[kTabs * HALF];
+  __shared__ int s_tab[KV4 ? 2 * kAppendMaxTokens : 1];  // KV4: each token's table; each table's position
+  int tab = 0;  // where the current token's table begins
+  auto cos_of = [&](int j) -> DF { return s_cos_all[(KV4 ? tab : 0) + j]; };
+  auto sin_of = [&](int j) -> DF { return s_sin_all[(KV4 ? tab : 0) + j]; };
+  __shared__ __align__(16) T s_row[KV4 ? 4 * kv4_row_at(HD) : 1];  // KV4: a finished row per warp
 
   pdl_wait();
   pdl_trigger();
@@ -177,14 +300,23 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     for (int j = threadIdx.x; j < HALF; j += blockDim.x) {
       DF c = {1.0f, 0.0f}, s = {0.0f, 0.0f};
       if (j < a.n_rot) sincos_df(pos, a.inv_freq[j], c, s);
-      s_cos[j] = c;
-      s_sin[j] = s;
+      s_cos_all[j] = c;
+      s_sin_all[j] = s;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      cr[i] = s_cos[lane * E + i].h;
-      sr[i] = s_sin[lane * E + i].h;
+      cr[i] = s_cos_all[lane * E + i].h;
+      sr[i] = s_sin_all[lane * E + i].h;
+    }
+  };
+  // KV4: token b's table becomes the current one.
+  auto use_table = [&](int b) {
+    tab = s_tab[b - b0] * HALF;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      cr[i] = cos_of(lane * E + i).h;
+      sr[i] = sin_of(lane * E + i).h;
     }
   };
 
@@ -195,10 +327,22 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     const float* w;
     bool rope;
     bool valid;
+    uint8_t* rec;  // KV4: the record of a k or v row (null: a q row, whose place is dst) and its position there
+    int m;
+  };
+  // Where element d of a row goes: its place, or (KV4) the warp's row in shared memory.
+  T* const row_buf = s_row + (KV4 ? warp * kv4_row_at(HD) : 0);
+  auto at = [&](const RowRef& rr, int d) -> T* {
+    if constexpr (KV4)
+      return row_buf + kv4_row_at(d);
+    else
+      return rr.dst + d;
   };
   auto row_ref = [&](int b, int row, int pos) -> RowRef {
     const int tok = b * a.T + t;
     RowRef rr;
+    rr.rec = nullptr;
+    rr.m = 0;
     if (row < a.H) {  // q head
       const size_t off = (static_cast<size_t>(tok) * a.H + row) * HD;
       rr.src = static_cast<const T*>(a.q_in) + off;
@@ -209,13 +353,23 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     } else {
       const bool is_k = row < a.H + a.Hkv;
       const int kvh = is_k ? row - a.H : row - a.H - a.Hkv;
-      // k / v need a cache row: the position itself, or on a sliding-window
-      // ring the position modulo its capacity.
-      rr.valid = pos >= 0 && (a.ring || pos < a.max_len);
-      const int crow = !rr.valid ? 0 : (a.ring ? pos % a.max_len : pos);
       rr.src = static_cast<const T*>(is_k ? a.k_in : a.v_in) + (static_cast<size_t>(tok) * a.Hkv + kvh) * HD;
-      rr.dst = static_cast<T*>(is_k ? a.cache_k : a.cache_v) +
-               ((static_cast<size_t>(b) * a.Hkv + kvh) * a.max_len + crow) * HD;
+      if constexpr (KV4) {
+        const int slot = a.slots[tok];
+        rr.valid = slot >= 0 && slot < a.n_slots;
+        const int in_block = slot & ((1 << a.block_shift) - 1);
+        rr.dst = nullptr;
+        rr.rec = static_cast<uint8_t*>(a.cache_k) +
+                 kv4_record<HD>(rr.valid ? slot >> a.block_shift : 0, kvh, in_block >> 4, a.Hkv, a.block_shift);
+        rr.m = in_block & 15;
+      } else {
+        // k / v need a cache row: the position itself, or on a sliding-window
+        // ring the position modulo its capacity.
+        rr.valid = pos >= 0 && (a.ring || pos < a.max_len);
+        const int crow = !rr.valid ? 0 : (a.ring ? pos % a.max_len : pos);
+        rr.dst = static_cast<T*>(is_k ? a.cache_k : a.cache_v) +
+                 ((static_cast<size_t>(b) * a.Hkv + kvh) * a.max_len + crow) * HD;
+      }
       rr.w = is_k ? a.k_w : nullptr;
       rr.rope = is_k;
     }
@@ -244,11 +398,11 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       if (rr.rope) {
         const float xo = static_cast<float>(rr.src[other]);
         const float ws = rr.w != nullptr ? rr.w[self] : 1.0f, wo = rr.w != nullptr ? rr.w[other] : 1.0f;
-        v = normrope_exact_bf16_inl(xs, ws, xo, wo, rd, j < a.n_rot, lower, s_cos[j], s_sin[j]);
+        v = normrope_exact_bf16_inl(xs, ws, xo, wo, rd, j < a.n_rot, lower, cos_of(j), sin_of(j));
       } else {
         v = df_round_bf16(df_mul_f(rd, xs));
       }
-      rr.dst[self] = static_cast<T>(v);
+      *at(rr, self) = static_cast<T>(v);
     }
   };
 
@@ -278,13 +432,13 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
           const float wo = rr.w != nullptr ? rr.w[other] : 1.0f;
           const DF po = two_prod(xo, wo);
           mag += fabsf(po.h);
-          inner = df_add(df_mul(inner, s_cos[j]), df_mul(po, lower ? df_neg(s_sin[j]) : s_sin[j]));
+          inner = df_add(df_mul(inner, cos_of(j)), df_mul(po, lower ? df_neg(sin_of(j)) : sin_of(j)));
         }
       }
       const DF v = df_mul_f(inner, r);
       const float e = fmaf(kErrR, fabsf(v.h), 0x1.0p-40f * r * mag);
       if (fabsf((v.h - bf16_midpoint(v.h)) + v.l) > e)
-        rr.dst[self] = static_cast<T>(df_round_bf16(v));
+        *at(rr, self) = static_cast<T>(df_round_bf16(v));
       else
         open |= 1u << k;
     }
@@ -341,14 +495,27 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
         for (int k = 0; k < 2 * E; ++k) need |= (bf16_decided(o[k], kErrY * fabsf(o[k])) ? 0u : 1u) << k;
       }
     }
-    store_elems<E>(rr.dst + lane * E, o);
-    store_elems<E>(rr.dst + HALF + lane * E, o + E);
+    store_elems<E>(at(rr, lane * E), o);
+    store_elems<E>(at(rr, HALF + lane * E), o + E);
     if constexpr (kBF16) {
       if (__any_sync(0xffffffffu, need != 0)) {
         need = refine(rr, need, r);
         if (__any_sync(0xffffffffu, need != 0))
           fix_elems(rr, need, inv_rms_df(row_sumsq_split<2 * E, HD>(x, sf), HD, a.eps));
       }
+    }
+    if constexpr (KV4) {
+      __syncwarp();
+      if (rr.rec != nullptr) {
+        kv4_store_row<HD>(row_buf, rr.rec, rr.m, rr.rope, rr.rope ? a.k_mul : 1.0f, lane);
+      } else {
+        constexpr int C = HD >= 256 ? 8 : HD / 32;  // elements per copy
+        using V = std::conditional_t<C == 8, uint4, std::conditional_t<C == 4, uint2, uint32_t>>;
+#pragma unroll
+        for (int d = lane * C; d < HD; d += 32 * C)
+          *reinterpret_cast<V*>(rr.dst + d) = *reinterpret_cast<const V*>(row_buf + kv4_row_at(d));
+      }
+      __syncwarp();
     }
   };
 
@@ -360,6 +527,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     while (row >= row1 && b < bB) { row -= nr; ++b; }
     RowRef rr = {};
     HalfBits<T, E> lo, hi;
+    [[maybe_unused]] int b_tab = -1;
     if (b < bB) {
       rr = row_ref(b, row, pos);
       load_row(rr, lo, hi);
@@ -373,6 +541,9 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
         rrn = row_ref(bn, rn, pos);
         load_row(rrn, lon, hin);
       }
+      if constexpr (KV4) {
+        if (b != b_tab) use_table(b_tab = b);
+      }
       if (all_rot)
         do_row(rr, lo, hi, std::true_type());
       else
@@ -385,6 +556,35 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     }
   };
 
+  if constexpr (KV4) {
+    // A table per distinct position (neighbours that agree share one), all of
+    // them built at once, so that rows of all tokens follow each other.
+    if (threadIdx.x == 0) {
+      int n = -1, last = 0;
+      for (int b = b0; b < b1; ++b) {
+        const int pos = a.positions[b * a.T + t];
+        if (n < 0 || pos != last) s_tab[kAppendMaxTokens + ++n] = last = pos;
+        s_tab[b - b0] = n;
+      }
+    }
+    __syncthreads();
+    const int ntab = s_tab[b1 - 1 - b0] + 1;
+    for (int idx = threadIdx.x; idx < ntab * HD; idx += blockDim.x) {
+      const int j = (idx >> 1) % HALF, part = idx & 1, at = (idx >> 1) / HALF * HALF + j;
+      if (j < a.n_rot) {
+        bool to_cos;
+        const DF v = sincos_df_part(s_tab[kAppendMaxTokens + idx / HD], a.inv_freq[j], part, to_cos);
+        (to_cos ? s_cos_all : s_sin_all)[at] = v;
+      } else if (part == 0) {
+        s_cos_all[at] = DF{1.0f, 0.0f};
+      } else {
+        s_sin_all[at] = DF{0.0f, 0.0f};
+      }
+    }
+    __syncthreads();
+    run(b0, b1, 0);
+    return;
+  }
   // One cos/sin table serves every token of the CTA when their positions
   // agree (the usual prefill case); otherwise tokens go one at a time.
   const int p0 = a.positions[b0 * a.T + t];
@@ -417,15 +617,15 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, cudaStream_t s, const AppendArgs& a
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename T>
+template <typename T, bool KV4>
 cudaError_t launch_t(const AppendArgs& a, cudaStream_t s) {
   const int nrows = a.H + (a.k_in ? 2 * a.Hkv : 0);
   dim3 grid(a.T * ((a.B + a.tok_per_cta - 1) / a.tok_per_cta), (nrows + a.rows_per_cta - 1) / a.rows_per_cta);
   switch (a.hd) {
-    case 64: return launch_pdl(append_normrope_kernel<T, 64>, grid, s, a);
-    case 128: return launch_pdl(append_normrope_kernel<T, 128>, grid, s, a);
-    case 256: return launch_pdl(append_normrope_kernel<T, 256>, grid, s, a);
-    case 512: return launch_pdl(append_normrope_kernel<T, 512>, grid, s, a);
+    case 64: return launch_pdl(append_normrope_kernel<T, 64, KV4>, grid, s, a);
+    case 128: return launch_pdl(append_normrope_kernel<T, 128, KV4>, grid, s, a);
+    case 256: return launch_pdl(append_normrope_kernel<T, 256, KV4>, grid, s, a);
+    case 512: return launch_pdl(append_normrope_kernel<T, 512, KV4>, grid, s, a);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -433,7 +633,9 @@ cudaError_t launch_t(const AppendArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-  return dtype == 1 ? launch_t<__nv_bfloat16>(a, s) : launch_t<float>(a, s);
+  return dtype == 1 ? launch_t<__nv_bfloat16, false>(a, s) : launch_t<float, false>(a, s);
 }
+
+cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t s) { return launch_t<__nv_bfloat16, true>(a, s); }
 
 }  // namespace g4

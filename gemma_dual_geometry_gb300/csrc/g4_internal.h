@@ -33,6 +33,7 @@ cudaError_t set_smem_limit_once(int bytes) {
 constexpr int kMaxHalf = 256;  // head_dim / 2 for the widest supported head (512)
 
 // Step a4: norm -> RoPE -> cache append.
+constexpr int kAppendMaxTokens = 4;  // tok_per_cta at most of the 4-bit append
 struct AppendArgs {
   const void* q_in;
   const void* k_in;  // null on a shared layer
@@ -49,6 +50,11 @@ struct AppendArgs {
   int tok_per_cta;   // tokens (same t, consecutive b) handled per CTA
   int n_rot;         // rotated pairs; inv_freq[j] == 0 for j >= n_rot
   float eps;
+  // the 4-bit cache: k and v of a token go to its slot of the pool
+  const int32_t* slots;  // [B*T]
+  int n_slots;           // n_blocks * block_size
+  int block_shift;       // log2(block_size)
+  float k_mul;           // 2^-k_exp
   float inv_freq[kMaxHalf];
 };
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s);
@@ -188,26 +194,8 @@ struct Kv4AssignArgs {
 constexpr int kKv4MaxBatch = 8192;  // a CTA keeps 8 bytes per sequence in shared memory
 cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s);
 
-struct Kv4AppendArgs {
-  const void* q_in;
-  const void* k_in;  // null on a shared layer
-  const void* v_in;
-  const float* q_w;
-  const float* k_w;
-  const int32_t* positions;  // [B*T]
-  const int32_t* slots;      // [B*T]
-  void* q_out;
-  uint8_t* data;  // the layer's pool
-  int tokens, H, Hkv, hd;
-  int n_slots;       // n_blocks * block_size
-  int block_shift;   // log2(block_size)
-  int rows_per_cta;  // head rows (of H + 2 Hkv) of a token handled per CTA
-  float k_mul;       // 2^-k_exp
-  int n_rot;
-  float eps;
-  float inv_freq[kMaxHalf];
-};
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
+// AppendArgs with the 4-bit fields set; cache_k is the layer's pool.
+cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t s);
 
 // Positions [first, first + rows) of every sequence as bf16 rows
 // k, v [B][Hkv][rows][hd].  first is start[b], or with q_start set (prefill)

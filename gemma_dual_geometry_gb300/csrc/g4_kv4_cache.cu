@@ -1,12 +1,11 @@
-// The paged 4-bit KV cache: block tables and slots from request lengths, the
-// norm -> RoPE -> 4-bit append, and the read-back to bf16.
+// The paged 4-bit KV cache: block tables and slots from request lengths, and
+// the read-back to bf16.  (The append: g4_append.cu.)
 // Formats and byte order: include/g4attn.h, g4_kv4.cuh.
 #include <cooperative_groups.h>
 
 #include "g4_device.cuh"
 #include "g4_internal.h"
 #include "g4_kv4.cuh"
-#include "g4_normrope.cuh"
 
 namespace g4 {
 namespace {
@@ -179,117 +178,6 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
   }
 }
 
-// ---------------------------------------------------------------- append
-//
-// A warp norms and ropes a head row (g4_normrope.cuh: the correctly rounded
-// bf16 values) and stores q rows as they are and k / v rows in 4 bits.
-
-// Quantises the lane's elements of a row (pieces l + 32c of PE elements, as
-// norm_rope_row leaves them; f already divided by 2^k_exp) and stores codes
-// and scales of position m into the record.
-template <int HD, int NPC, int PE>
-__device__ __forceinline__ void kv4_store_row(uint8_t* rec, int m, bool is_k, const float* f, int lane) {
-#pragma unroll
-  for (int c = 0; c < NPC; ++c) {
-    const int d0 = (lane + 32 * c) * PE;
-    // max |x| over the 16 elements of the scale block, as bits: NaN > infinity > the rest
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < PE; ++e) top = max(top, __float_as_uint(f[c * PE + e]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 1; o < 16 / PE; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t sb = top >= 0x7f800000u ? 0x7fu : e4m3_byte(__fdiv_rn(__uint_as_float(top), 6.0f));
-    const float s = e4m3_value(sb);
-    if (d0 % 16 == 0) rec[is_k ? kv4_k_scale_at<HD>(m, d0) : kv4_v_scale_at<HD>(m, d0)] = static_cast<uint8_t>(sb);
-#pragma unroll
-    for (int e = 0; e < PE; e += 2) {
-      const float lo = s > 0.0f ? __fdiv_rn(f[c * PE + e], s) : 0.0f;
-      const float hi = s > 0.0f ? __fdiv_rn(f[c * PE + e + 1], s) : 0.0f;
-      rec[is_k ? kv4_k_code_at<HD>(m, d0 + e) : kv4_v_code_at<HD>(m, d0 + e)] =
-          static_cast<uint8_t>(e2m1x2_byte(lo, hi));
-    }
-  }
-}
-
-template <int HD>
-__global__ void __launch_bounds__(128) kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
-  using T = __nv_bfloat16;
-  constexpr int EL = HD / 32;
-  constexpr int PE = EL < 8 ? EL : 8;
-  constexpr int NPC = EL / PE;
-  constexpr int NW = 4;
-  __shared__ DF s_cos[HD / 2];
-  __shared__ DF s_sin[HD / 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok = blockIdx.x;
-  const bool owns = a.k_in != nullptr;
-  const int nrows = a.H + (owns ? 2 * a.Hkv : 0);
-  const int row0 = blockIdx.y * a.rows_per_cta;
-  const int row1 = min(nrows, row0 + a.rows_per_cta);
-
-  pdl_wait();
-  pdl_trigger();
-  const int pos = a.positions[tok];
-  const int slot = owns ? a.slots[tok] : -1;
-  const bool kept = slot >= 0 && slot < a.n_slots;
-
-  auto load = [&](int row, float* f, float* wf) {
-    const T* src;
-    const float* w = nullptr;
-    if (row < a.H) {
-      src = static_cast<const T*>(a.q_in) + (static_cast<size_t>(tok) * a.H + row) * HD;
-      w = a.q_w;
-    } else if (row < a.H + a.Hkv) {
-      src = static_cast<const T*>(a.k_in) + (static_cast<size_t>(tok) * a.Hkv + row - a.H) * HD;
-      w = a.k_w;
-    } else {
-      src = static_cast<const T*>(a.v_in) + (static_cast<size_t>(tok) * a.Hkv + row - a.H - a.Hkv) * HD;
-    }
-    load_row<T, NPC, PE>(src, lane, f);
-    if (w != nullptr) {
-      load_row<float, NPC, PE>(w, lane, wf);
-    } else {
-#pragma unroll
-      for (int i = 0; i < EL; ++i) wf[i] = 1.0f;
-    }
-  };
-
-  float f[EL], wf[EL];
-  const int first = row0 + warp;
-  if (first < row1) load(first, f, wf);
-  for (int idx = threadIdx.x; idx < HD; idx += NW * 32) {
-    const int j = idx >> 1, part = idx & 1;
-    if (j < a.n_rot) {
-      bool to_cos;
-      const DF v = sincos_df_part(pos, a.inv_freq[j], part, to_cos);
-      (to_cos ? s_cos : s_sin)[j] = v;
-    } else if (part == 0) {
-      s_cos[j] = DF{1.0f, 0.0f};
-    } else {
-      s_sin[j] = DF{0.0f, 0.0f};
-    }
-  }
-  __syncthreads();
-  for (int row = first; row < row1; row += NW) {
-    if (row != first) load(row, f, wf);
-    const bool is_q = row < a.H, is_k = !is_q && row < a.H + a.Hkv;
-    if (!is_q && !kept) break;  // k and v rows come last
-    norm_rope_row<T, HD, NPC, PE>(f, wf, is_q || is_k, s_cos, s_sin, a.n_rot, a.eps, lane);
-    if (is_q) {
-      store_row<T, NPC, PE>(static_cast<T*>(a.q_out) + (static_cast<size_t>(tok) * a.H + row) * HD, lane, f);
-    } else {
-      if (is_k) {
-#pragma unroll
-        for (int i = 0; i < EL; ++i) f[i] *= a.k_mul;
-      }
-      const int kvh = row - a.H - (is_k ? 0 : a.Hkv);
-      const int in_block = slot & ((1 << a.block_shift) - 1);
-      uint8_t* rec = a.data + kv4_record<HD>(slot >> a.block_shift, kvh, in_block >> 4, a.Hkv, a.block_shift);
-      kv4_store_row<HD, NPC, PE>(rec, in_block & 15, is_k, f, lane);
-    }
-  }
-}
-
 // ---------------------------------------------------------------- gather
 //
 // A warp per record: 16-byte loads in fragment order, values as fp16 code
@@ -405,18 +293,6 @@ cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
   unsigned n = 1;
   while (n < 8 && n < static_cast<unsigned>(a.B) && work > 4096LL * n) n *= 2;
   return launch_pdl(kv4_assign_kernel, dim3(n), kAssignThreads, smem, n, s, a);
-}
-
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
-  const int nrows = a.H + (a.k_in ? 2 * a.Hkv : 0);
-  const dim3 grid(a.tokens, (nrows + a.rows_per_cta - 1) / a.rows_per_cta);
-  switch (a.hd) {
-    case 64: return launch_pdl(kv4_append_kernel<64>, grid, 128, 0, 1, s, a);
-    case 128: return launch_pdl(kv4_append_kernel<128>, grid, 128, 0, 1, s, a);
-    case 256: return launch_pdl(kv4_append_kernel<256>, grid, 128, 0, 1, s, a);
-    case 512: return launch_pdl(kv4_append_kernel<512>, grid, 128, 0, 1, s, a);
-    default: return cudaErrorInvalidValue;
-  }
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s) {

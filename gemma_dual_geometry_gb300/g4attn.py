@@ -117,13 +117,25 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = None  # device index -> the address of its current stream
+
+
+def _find_raw_stream():
+    import torch
+    # (building a torch.cuda.Stream object takes as long as a launch)
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get if get is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream(stream, *tensors):
+    global _raw_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     for t in tensors:
         if t is not None and not isinstance(t, int) and t.is_cuda:
-            import torch
-            return torch.cuda.current_stream(t.device).cuda_stream
+            if _raw_stream is None:
+                _raw_stream = _find_raw_stream()
+            return _raw_stream(t.get_device())
     return None
 
 
