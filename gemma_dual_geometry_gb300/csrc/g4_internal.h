@@ -191,7 +191,7 @@ struct Kv4AssignArgs {
   int32_t* positions;
   int32_t* slots;
 };
-constexpr int kKv4MaxBatch = 8192;  // a CTA keeps 8 bytes per sequence in shared memory
+constexpr int kKv4MaxBatch = 8192;  // a CTA keeps 8 to 16 bytes per sequence in shared memory
 cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s);
 
 // AppendArgs with the 4-bit fields set; cache_k is the layer's pool.

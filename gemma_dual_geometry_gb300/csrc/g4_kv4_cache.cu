@@ -40,44 +40,45 @@ cudaError_t launch_pdl(void (*kern)(Args), dim3 grid, unsigned block, size_t sme
 // so the result does not depend on the order in which threads run.
 //
 // One cluster.  Every CTA scans all B lengths (both sums packed in one 64-bit
-// word; a few KB from L2, cheaper than exchanging partial sums), then serves
-// its own share of the sequences: it pushes their returned blocks, waits for
-// the cluster (blocks given back may be taken in the same call), pops, and
-// writes the positions and slots.  Bound by latency: three dependent global
-// reads (lengths, free list, table) and one cluster barrier.
+// word; a few KB from L2, cheaper than exchanging partial sums) and keeps the sums
+// in shared memory, then serves its own share of the sequences: it pushes their
+// returned blocks, waits for the cluster (blocks given back may be taken in the
+// same call), pops, and writes lengths, positions and slots.  Pushes and pops are
+// dealt out one block per thread, its sequence found in the sums by bisection.
+//   Bound by latency: lengths, free list and table are dependent reads, with
+// one cluster barrier between them.
 
-constexpr int kAssignThreads = 512;
+constexpr int kAssignThreads = 1024;
 
-// Block lengths of one sequence, clamped to the contract.
-struct Span {
-  int old_len, new_len, have, want;
-};
-__device__ __forceinline__ Span span_of(const Kv4AssignArgs& a, int b) {
-  const long long most = static_cast<long long>(a.max_blocks) << a.block_shift;
-  const int cap = static_cast<int>(most > 0x7fffffffLL ? 0x7fffffffLL : most);
-  Span s;
-  s.old_len = min(max(__ldcg(a.old_lens + b), 0), cap);
-  const long long grown = static_cast<long long>(s.old_len) + a.T;
-  s.new_len = min(max(__ldcg(a.new_lens + b), 0), cap);
-  if (s.new_len > grown) s.new_len = static_cast<int>(grown);
-  // (the sum in 64 bits: a length may be within a block of 2^31)
-  const long long up = (1 << a.block_shift) - 1;
-  s.have = static_cast<int>((s.old_len + up) >> a.block_shift);
-  s.want = static_cast<int>((s.new_len + up) >> a.block_shift);
-  return s;
+// The first i in [lo, hi) with v[i] > x (hi if there is none); v ascends.
+__device__ __forceinline__ int first_above(const int* v, int lo, int hi, int x) {
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] > x)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
 }
 
 __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid_constant__ Kv4AssignArgs a) {
-  extern __shared__ int s_sums[];  // [B] blocks taken up to and including b; [B] given back before b
+  extern __shared__ int s_mem[];
   __shared__ unsigned long long s_warp[kAssignThreads / 32];
-  __shared__ unsigned long long s_carry;
-  __shared__ int s_taken;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = kAssignThreads / 32;
   const int nctas = gridDim.x, rank = blockIdx.x;
-  int* upto = s_sums;
-  int* before = s_sums + a.B;
+  const int per = (a.B + nctas - 1) / nctas;
+  const int b0 = min(a.B, rank * per), b1 = min(a.B, b0 + per);  // this CTA's sequences
+  int* taken = s_mem;           // [B] blocks taken up to and including b
+  int* given = taken + a.B;     // [B] blocks given back up to and including b
+  int* s_old = given + a.B;     // [per] lengths of its sequences, clamped to the contract
+  int* s_new = s_old + per;
+  const long long most = static_cast<long long>(a.max_blocks) << a.block_shift;
+  const int cap = static_cast<int>(most > 0x7fffffffLL ? 0x7fffffffLL : most);
+  const int mask = (1 << a.block_shift) - 1;
+  auto blocks_of = [&](int len) { return (len >> a.block_shift) + ((len & mask) != 0); };
 
   pdl_wait();
   pdl_trigger();
@@ -87,9 +88,15 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
     const int b = base + tid;
     unsigned long long v = 0;
     if (b < a.B) {
-      const Span s = span_of(a, b);
-      v = static_cast<unsigned long long>(static_cast<unsigned>(max(s.have - s.want, 0))) << 32 |
-          static_cast<unsigned>(max(s.want - s.have, 0));
+      const int was = min(max(__ldcg(a.old_lens + b), 0), cap);
+      int len = min(max(__ldcg(a.new_lens + b), 0), cap);
+      if (len - was > a.T) len = was + a.T;  // (both in [0, 2^31): no overflow)
+      if (b >= b0 && b < b1) {
+        s_old[b - b0] = was;
+        s_new[b - b0] = len;
+      }
+      const int d = blocks_of(len) - blocks_of(was);
+      v = d >= 0 ? static_cast<unsigned>(d) : static_cast<unsigned long long>(static_cast<unsigned>(-d)) << 32;
     }
     unsigned long long sum = v;  // inclusive over the warp; neither half can carry (B * max_blocks < 2^31)
 #pragma unroll
@@ -99,82 +106,106 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
     }
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    unsigned long long pre = carry;
-    for (int w = 0; w < warp; ++w) pre += s_warp[w];
-    sum += pre;
+    unsigned long long all = lane < NW ? s_warp[lane] : 0;  // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += u;
+    }
+    const unsigned long long before = __shfl_sync(0xffffffffu, all, warp == 0 ? 0 : warp - 1);
+    sum += carry + (warp == 0 ? 0 : before);
     if (b < a.B) {
-      upto[b] = static_cast<int>(sum & 0xffffffffu);
-      before[b] = static_cast<int>((sum - v) >> 32);
+      taken[b] = static_cast<int>(sum & 0xffffffffu);
+      given[b] = static_cast<int>(sum >> 32);
     }
-    if (tid == kAssignThreads - 1) s_carry = sum;
+    carry += __shfl_sync(0xffffffffu, all, 31);
     __syncthreads();
-    carry = s_carry;
   }
-  if (tid == 0) s_taken = 0;
-  const int there = static_cast<int>(min(static_cast<long long>(count) + static_cast<long long>(carry >> 32),
-                                         static_cast<long long>(a.n_blocks)));
+  const int back = static_cast<int>(carry >> 32);
+  const int there = static_cast<int>(min(static_cast<long long>(count) + back, static_cast<long long>(a.n_blocks)));
 
-  // this CTA's sequences
-  const int per = (a.B + nctas - 1) / nctas;
-  const int b0 = min(a.B, rank * per), b1 = min(a.B, b0 + per);
-  for (int b = b0 + warp; b < b1; b += NW) {
-    const Span s = span_of(a, b);
-    for (int e = s.want + lane; e < s.have; e += 32) {
-      const long long at = static_cast<long long>(count) + before[b] + (e - s.want);
-      if (at < a.n_blocks) a.free_blocks[at] = __ldcg(a.table + static_cast<size_t>(b) * a.max_blocks + e);
-    }
+  // Blocks given back by this CTA's sequences: the x-th of the call goes behind
+  // the free list's first `count`.
+  const int g0 = b0 > 0 ? given[b0 - 1] : 0, g1 = b1 > b0 ? given[b1 - 1] : g0;
+  for (int x = g0 + tid; x < g1; x += kAssignThreads) {
+    const int b = first_above(given, b0, b1, x);
+    const int e = blocks_of(s_new[b - b0]) + x - (b > 0 ? given[b - 1] : 0);
+    const long long at = static_cast<long long>(count) + x;
+    if (at < a.n_blocks) a.free_blocks[at] = __ldcg(a.table + static_cast<size_t>(b) * a.max_blocks + e);
   }
-  // Blocks given back are in place (and every CTA has read the lengths and the
-  // count, which the outputs may overwrite).
+  // Blocks given back are in place, and every CTA has read the lengths and the
+  // count, which the outputs may overwrite.
   if (nctas > 1) {
     cluster.sync();
   } else {
     __syncthreads();
   }
-  for (int b = b0 + warp; b < b1; b += NW) {
-    const Span s = span_of(a, b);
-    const int need = s.want - s.have;
-    if (need > 0 && upto[b] <= there) {
-      const int top = there - 1 - (upto[b] - need);
-      for (int j = lane; j < need; j += 32)
-        a.table[static_cast<size_t>(b) * a.max_blocks + s.have + j] = __ldcg(a.free_blocks + top - j);
-    }
+  // Blocks taken: the x-th of the call is the free list's x-th from its top.  A
+  // sequence is served if the blocks of all up to it are there.
+  const int t0 = b0 > 0 ? taken[b0 - 1] : 0, t1 = b1 > b0 ? min(taken[b1 - 1], there) : t0;
+  for (int x = t0 + tid; x < t1; x += kAssignThreads) {
+    const int b = first_above(taken, b0, b1, x);
+    if (taken[b] <= there)
+      a.table[static_cast<size_t>(b) * a.max_blocks + blocks_of(s_old[b - b0]) + x - (b > 0 ? taken[b - 1] : 0)] =
+          __ldcg(a.free_blocks + (there - 1 - x));
   }
-  // Sequences that need blocks are granted in order, so the largest granted
-  // prefix is what was taken; the first CTA forms it over all of them.
+  __syncthreads();
+  // granted lengths (a sequence that needs no blocks is always served)
+  for (int i = tid; i < b1 - b0; i += kAssignThreads) {
+    const int b = b0 + i;
+    const bool needs = taken[b] > (b > 0 ? taken[b - 1] : 0);
+    const int len = needs && taken[b] > there ? s_old[i] : s_new[i];
+    s_new[i] = len;
+    a.lens_out[b] = len;
+  }
+  // The served ones are those up to some sequence, whose sum is what was taken.
   if (rank == 0) {
-    int taken = 0;
-    for (int b = tid; b < a.B; b += kAssignThreads) {
-      if (upto[b] <= there) taken = max(taken, upto[b]);
-    }
-    atomicMax(&s_taken, taken);
+    if (tid == 0 && (a.B == 0 || taken[0] > there)) *a.count_out = there;
+    for (int b = tid; b < a.B; b += kAssignThreads)
+      if (taken[b] <= there && (b + 1 == a.B || taken[b + 1] > there)) *a.count_out = there - taken[b];
   }
   __syncthreads();
-  if (rank == 0 && tid == 0) *a.count_out = there - s_taken;
 
-  // positions and slots of its sequences, then their lengths
-  const int block_mask = (1 << a.block_shift) - 1;
-  const long long n = static_cast<long long>(b1 - b0) * a.T;
-  for (long long i = tid; i < n; i += kAssignThreads) {
-    const int q = static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(a.T));
-    const int b = b0 + q, t = static_cast<int>(i - static_cast<long long>(q) * a.T);
-    const Span s = span_of(a, b);
-    const bool granted = s.want <= s.have || upto[b] <= there;
-    const long long at = static_cast<long long>(s.old_len) + t;
-    int pos = -1, slot = -1;
-    if (granted && at < s.new_len) {
-      pos = static_cast<int>(at);
-      const int id = a.table[static_cast<size_t>(b) * a.max_blocks + (pos >> a.block_shift)];
-      if (id >= 0 && id < a.n_blocks) slot = (id << a.block_shift) + (pos & block_mask);
+  // positions and slots, four neighbours of a row per thread where rows allow it
+  const int nb = b1 - b0;
+  auto slot_at = [&](const int32_t* row, int pos, int& entry, int& id) {
+    if ((pos >> a.block_shift) != entry) {
+      entry = pos >> a.block_shift;
+      id = row[entry];
     }
-    const size_t o = static_cast<size_t>(b) * a.T + t;
-    a.positions[o] = pos;
-    a.slots[o] = slot;
-  }
-  __syncthreads();
-  for (int b = b0 + tid; b < b1; b += kAssignThreads) {
-    const Span s = span_of(a, b);
-    a.lens_out[b] = s.want <= s.have || upto[b] <= there ? s.new_len : s.old_len;
+    return id >= 0 && id < a.n_blocks ? (id << a.block_shift) + (pos & mask) : -1;
+  };
+  if ((a.T & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0) {
+    const unsigned quads = static_cast<unsigned>(a.T) / 4, n = static_cast<unsigned>(nb) * quads;
+#pragma unroll 2
+    for (unsigned i = tid; i < n; i += kAssignThreads) {
+      const unsigned r = i / quads, t = (i - r * quads) * 4;
+      const int b = b0 + static_cast<int>(r), end = s_new[r];
+      const long long at = static_cast<long long>(s_old[r]) + t;
+      const int32_t* row = a.table + static_cast<size_t>(b) * a.max_blocks;
+      int p[4], q[4], entry = -1, id = -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = at + k < end;
+        p[k] = in ? static_cast<int>(at) + k : -1;
+        q[k] = in ? slot_at(row, p[k], entry, id) : -1;
+      }
+      const size_t o = (static_cast<size_t>(b) * a.T + t) / 4;
+      reinterpret_cast<int4*>(a.positions)[o] = make_int4(p[0], p[1], p[2], p[3]);
+      reinterpret_cast<int4*>(a.slots)[o] = make_int4(q[0], q[1], q[2], q[3]);
+    }
+  } else if (a.T > 0) {
+    const unsigned T = static_cast<unsigned>(a.T), n = static_cast<unsigned>(nb) * T;
+    for (unsigned i = tid; i < n; i += kAssignThreads) {
+      const unsigned r = i / T, t = i - r * T;
+      const int b = b0 + static_cast<int>(r);
+      const long long at = static_cast<long long>(s_old[r]) + t;
+      int entry = -1, id = -1;
+      const bool in = at < s_new[r];
+      const size_t o = static_cast<size_t>(b) * a.T + t;
+      a.positions[o] = in ? static_cast<int>(at) : -1;
+      a.slots[o] = in ? slot_at(a.table + static_cast<size_t>(b) * a.max_blocks, static_cast<int>(at), entry, id) : -1;
+    }
   }
 }
 
@@ -283,15 +314,14 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(a.B) * 8;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 8);
-    if (e != cudaSuccess) return e;
-  }
   // Positions and slots are what grows: a CTA per 4096 of them, up to the portable cluster size.
   const long long work = static_cast<long long>(a.B) * a.T;
   unsigned n = 1;
   while (n < 8 && n < static_cast<unsigned>(a.B) && work > 4096LL * n) n *= 2;
+  const size_t per = (static_cast<size_t>(a.B) + n - 1) / n;
+  const size_t smem = (2 * static_cast<size_t>(a.B) + 2 * per) * 4;
+  const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 16);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kv4_assign_kernel, dim3(n), kAssignThreads, smem, n, s, a);
 }
 

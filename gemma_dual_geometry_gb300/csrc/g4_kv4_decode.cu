@@ -21,11 +21,14 @@
 //
 // Work.  The records of all (sequence, kv head) units, laid end to end, are
 // dealt out in equal contiguous shares to as many CTAs as are resident, so
-// ragged lengths leave no SM idle.  A unit inside one share is written
-// directly; the CTAs of a unit that spans shares leave partials in the workspace
-// and the one that takes the last ticket merges them.
+// ragged lengths leave no SM idle.  Where shares are short (a few steps: windows,
+// short sequences) they are cut anew at every unit instead, so that no CTA pays
+// for the start of a second one.  A unit inside one share is written directly;
+// the CTAs of a unit that spans shares leave partials in the workspace and the one
+// that takes the last ticket merges them.
 //
-// A CTA (4 warps) takes STEP records per step.  Each warp scores its share of
+// A CTA takes STEP records per step.  A fifth warp issues the copies; each of the
+// other four scores its share of
 // them and forms their probabilities; after a CTA barrier each warp adds all the
 // step's P V for its own slice of head_dim, so O takes few registers and needs no
 // merge between warps (at head_dim 64 and 128, whose 64-element pieces are
@@ -59,18 +62,20 @@ constexpr float kSlack = 8.0f;
 constexpr float kShift = 4.0f;
 constexpr float kNoKey = -1e30f;  // reference of a state that has seen no key
 constexpr int kFan = 16;      // partials that a first merge takes
+constexpr int kCutSteps = 4;   // longest shares, in steps, that are cut at units
 constexpr int kMaxLevel = 64;  // partials that a last merge may be left with (CTAs / kFan at most)
 
 // Shape of the kernel at one head_dim (also used by the plan).
 template <int HD>
 struct Kv4Cfg {
-  static constexpr int W = 4;                                   // warps per CTA
+  static constexpr int W = 4;                                   // warps that compute
+  static constexpr int NT = (W + 1) * 32;                       // and one that copies
   static constexpr int NP = HD / 64;                            // pieces of a row
   static constexpr int RW = HD >= 256 ? 1 : 256 / HD;           // records a warp scores per step
   static constexpr int STEP = W * RW;                           // records per step
   static constexpr int PW = NP >= W ? NP / W : 1;               // pieces of O per warp
   static constexpr int KS = NP >= W ? 1 : W / NP;               // warps that share a piece
-  static constexpr int MINB = HD >= 512 ? 3 : HD == 256 ? 5 : 4;  // CTAs per SM
+  static constexpr int MINB = HD >= 512 ? 3 : 4;                // CTAs per SM
   static constexpr int SLOTS = HD >= 512 ? 3 : 4;               // what MINB leaves room for
   static constexpr int HALF_B = 9 * HD;                         // K (or V) part of a record
   static constexpr int SLOT_B = STEP * HALF_B;
@@ -120,7 +125,7 @@ __device__ __forceinline__ int part_slot(int c_first, int i) { return 2 * (c_fir
 // with out null (un-normalised) into the slot of the first.
 template <int HD, int W>
 __device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first, int first, int step, int n, int G,
-                                         __nv_bfloat16* out, float* s_w) {
+                                         __nv_bfloat16* out, float* s_w) {  // (W warps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int h = warp; h < G; h += W) {
     float M = kNoKey;
@@ -143,7 +148,7 @@ __device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first,
       a.ws_ml[part_slot(c_first, first) * kHeads + h] = make_float2(M, l);
     }
   }
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
   constexpr int kBatch = 4;
   const int row = G * HD / 4;  // float4 of a slot
 #pragma unroll 1
@@ -182,21 +187,22 @@ struct Kv4Place {
 
 // GM: most heads per kv head, 4 (two scale blocks per product) or 8.
 template <int HD, int GM>
-__global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
+__global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs a) {
   using C = Kv4Cfg<HD>;
   constexpr int RW = C::RW, STEP = C::STEP, PW = C::PW, KS = C::KS;
-  constexpr int W = C::W, NT = W * 32, SLOTS = C::SLOTS;
+  constexpr int W = C::W, NT = C::NT, SLOTS = C::SLOTS;
   constexpr bool PAIR = GM == 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_bar[SLOTS];
-  __shared__ long long s_scan[W];
+  __shared__ long long s_scan[W + 1];
   __shared__ long long s_unit0;                      // records before the consumer's unit
   __shared__ Kv4Place s_ip, s_cp;                    // next step to copy; unit being consumed
   __shared__ float s_qf[kHeads];                     // score factor of each head
   __shared__ float s_top[W * kHeads];
   __shared__ float s_l[W * kHeads];
   __shared__ uint32_t s_ok[4];                       // records present in a step (step mod 4)
+  __shared__ int s_c_first, s_nparts;                // cut at units: the unit's first CTA and parts
   __shared__ int s_last;
   __shared__ int s_abort;
 
@@ -213,30 +219,41 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
   pdl_wait();
   pdl_trigger();
 
-  // ---- this CTA's share [w0, w1) of the records laid end to end
+  // ---- this CTA's share
   const int per = (a.B + NT - 1) / NT;  // consecutive sequences per thread
   const int sb0 = min(a.B, tid * per), sb1 = min(a.B, sb0 + per);
-  long long sum = 0;
-  for (int b = sb0; b < sb1; ++b) sum += seq_of(a, b).n;
-  long long upto = sum;
+  // exclusive sum of x over the threads, and its total
+  auto scan = [&](long long x, long long& total) {
+    long long upto = x;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += u;
-  }
-  if (lane == 31) s_scan[warp] = upto;
-  __syncthreads();
-  long long total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) upto += s_scan[w];
-    total += s_scan[w];
-  }
-  total *= a.Hkv;
+    for (int w = 0; w <= W; ++w) {
+      if (w < warp) upto += s_scan[w];
+      total += s_scan[w];
+    }
+    __syncthreads();
+    return upto - x;
+  };
   const int nctas = gridDim.x;
-  long long share = (total + nctas - 1) / nctas;
-  share = (share + STEP - 1) / STEP * STEP;
-  const long long w0 = min(total, share * blockIdx.x), w1 = min(total, w0 + share);
+  const long long cta = blockIdx.x;
+  long long sum = 0, total, at;
+  for (int b = sb0; b < sb1; ++b) sum += seq_of(a, b).n;
+  at = scan(sum, total) * a.Hkv;  // records before this thread's sequences
+  total *= a.Hkv;
+  auto steps_up = [](long long n) { return (n + STEP - 1) / STEP * STEP; };
+  long long share = steps_up((total + nctas - 1) / nctas);
+  // Cut at every unit: parts of `cut` records (the last of a unit fewer), which
+  // are at most total / cut + units.
+  const long long units = static_cast<long long>(a.B) * a.Hkv;
+  const long long cut = nctas > units ? steps_up((total + nctas - units - 1) / (nctas - units)) : 0;
+  const bool cut_units = cut > 0 && cut <= kCutSteps * STEP;
   // sequences without keys, spread over the CTAs
   for (int b = blockIdx.x; b < a.B; b += nctas) {
     if (seq_of(a, b).n == 0) {
@@ -244,29 +261,54 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
       for (int i = tid; i < a.H * HD / 2; i += NT) o[i] = 0u;
     }
   }
-  if (w0 >= w1) return;
-  {
-    long long at = (upto - sum) * a.Hkv;  // records before this thread's sequences
-    if (w0 >= at && w0 < upto * a.Hkv) {
+  Kv4Place mine;  // where the share begins, set by the thread that finds it there
+  mine.left = 0;
+  if (cut_units) {
+    long long parts = 0, nparts;
+    for (int b = sb0; b < sb1; ++b) parts += (seq_of(a, b).n + cut - 1) / cut;
+    long long before = scan(parts, nparts) * a.Hkv;
+    if (cta >= nparts * a.Hkv) return;
+    if (cta >= before && cta < before + parts * a.Hkv) {
+      for (int b = sb0; b < sb1; ++b) {
+        const Kv4Seq seq = seq_of(a, b);
+        const int np = static_cast<int>((seq.n + cut - 1) / cut);
+        if (cta < before + static_cast<long long>(np) * a.Hkv) {
+          mine.b = b;
+          mine.kvh = static_cast<int>(cta - before) / np;
+          const int part = static_cast<int>(cta - before) % np;
+          mine.off = part * static_cast<int>(cut);
+          mine.left = min(static_cast<int>(cut), seq.n - mine.off);
+          mine.first = seq.first;
+          mine.n = seq.n;
+          s_c_first = static_cast<int>(cta) - part;
+          s_nparts = np;
+          break;
+        }
+        before += static_cast<long long>(np) * a.Hkv;
+      }
+    }
+  } else {
+    const long long w0 = min(total, share * cta), w1 = min(total, w0 + share);
+    if (w0 >= w1) return;
+    if (w0 >= at && w0 < at + sum * a.Hkv) {
       for (int b = sb0; b < sb1; ++b) {
         const Kv4Seq seq = seq_of(a, b);
         const long long n = seq.n;
         if (w0 < at + n * a.Hkv) {
-          Kv4Place p;
-          p.b = b;
-          p.kvh = static_cast<int>((w0 - at) / n);
-          p.off = static_cast<int>(w0 - at - p.kvh * n);
-          p.left = static_cast<int>(w1 - w0);
-          p.first = seq.first;
-          p.n = seq.n;
-          s_ip = s_cp = p;
-          s_unit0 = at + p.kvh * n;
+          mine.b = b;
+          mine.kvh = static_cast<int>((w0 - at) / n);
+          mine.off = static_cast<int>(w0 - at - mine.kvh * n);
+          mine.left = static_cast<int>(w1 - w0);
+          mine.first = seq.first;
+          mine.n = seq.n;
+          s_unit0 = at + mine.kvh * n;
           break;
         }
         at += n * a.Hkv;
       }
     }
   }
+  if (mine.left > 0) s_ip = s_cp = mine;
   __syncthreads();
   // Moves a place n records on within its unit, or to the next unit that has any.
   auto advance = [&](Kv4Place& p, int n) {
@@ -284,62 +326,91 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
     p.n = seq.n;
   };
 
-  // ---- copies (warp 0): lane r < STEP owns record r of a step.  Part n = 2 step +
-  // (V ? 1 : 0) goes to buffer n mod SLOTS once part n - SLOTS has been read.
-  // The block ids of a step are loaded when the step before it has been issued.
-  int nrec_k = 0;               // records of the next K step (0: none is left)
-  int id_k = -1, id_v = -1;     // this lane's block id of the next K part and of the next V part
-  uint32_t rec_k = 0, rec_v = 0;  // and the record's index in its block and head
-  int issued = 0;               // parts
-  const int rec_mask = (1 << (a.block_shift - 4)) - 1;
-  auto load_step = [&]() {      // ids of the step at s_ip; moves it past the step
-    Kv4Place p = s_ip;
-    __syncwarp();
-    id_k = -1;
-    nrec_k = 0;
-    if (p.left <= 0) return;
-    const int n = min(min(STEP, p.n - p.off), p.left);
-    if (lane < n) {
-      const int gi = p.first + p.off + lane;
-      const int entry = gi >> (a.block_shift - 4);
-      if (entry < a.max_blocks) id_k = a.table[static_cast<size_t>(p.b) * a.max_blocks + entry];
-      rec_k = static_cast<uint32_t>(p.kvh) << (a.block_shift - 4) | (gi & rec_mask);
-    }
-    nrec_k = n;
-    advance(p, n);
-    if (lane == 0) s_ip = p;
-    __syncwarp();
-  };
-  bool v_pending = false;
-  auto issue = [&]() {  // part `issued`, if there is one
-    const bool is_v = issued & 1;
-    if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort)) || !(is_v ? v_pending : nrec_k > 0)) return;
-    const int id = is_v ? id_v : id_k;
-    const bool there = id >= 0 && id < a.n_blocks;
-    const uint32_t bar = smem_u32(&s_bar[issued % SLOTS]);
-    const uint32_t all = __ballot_sync(0xffffffffu, there);
-    if (lane == 0) {
-      if (!is_v) s_ok[(issued >> 1) & 3] = all;
-      mbar_arrive_expect_tx(bar, __popc(all) * C::HALF_B);
-    }
-    __syncwarp();
-    if (there) {
-      const size_t rec = (static_cast<size_t>(id) * a.Hkv << (a.block_shift - 4)) + (is_v ? rec_v : rec_k);
-      bulk_g2s(smem_u32(smem) + (issued % SLOTS) * C::SLOT_B + lane * C::HALF_B,
-               a.data + rec * Kv4Rec<HD>::BYTES + (is_v ? C::HALF_B : 0), C::HALF_B, bar);
-    }
-    v_pending = !is_v;
-    if (!is_v) {
-      id_v = id_k;
-      rec_v = rec_k;
-      load_step();
-    }
-    ++issued;
-  };
-  if (warp == 0) {
-    load_step();
+  // The computing warps' barrier.
+  auto sync_compute = [] { asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory"); };
+
+  if (warp == W) {
+    // ---- copies (warp W): part n = 2 step + (V ? 1 : 0) goes to buffer n mod SLOTS
+    // once part n - SLOTS has been read; lane r < STEP copies record r of a step.
+    // Block ids are loaded 32 records (of one unit) at a time, a batch ahead.
+    int id = -1, id_next = -1;      // of the batch's record `lane`
+    int n_batch = 0, n_next = 0, at_batch = 0;
+    uint32_t rec = 0, rec_next = 0;  // its record's index among its head's in the block, kvh above
+    const int rec_bits = a.block_shift - 4;
+    auto load_batch = [&]() {  // the batch at s_ip; moves it past the batch
+      Kv4Place p = s_ip;
+      __syncwarp();
+      id_next = -1;
+      n_next = 0;
+      if (p.left <= 0) return;
+      const int n = min(min(32, p.n - p.off), p.left);
+      if (lane < n) {
+        const int gi = p.first + p.off + lane;
+        const int entry = gi >> rec_bits;
+        if (entry < a.max_blocks) id_next = a.table[static_cast<size_t>(p.b) * a.max_blocks + entry];
+        rec_next = static_cast<uint32_t>(p.kvh) << rec_bits | (gi & ((1 << rec_bits) - 1));
+      }
+      n_next = n;
+      advance(p, n);
+      if (lane == 0) s_ip = p;
+      __syncwarp();
+    };
+    int issued = 0, copied = 0;  // parts
+    int id_k = -1;   // of the step being issued
+    uint32_t rec_k = 0;
+    auto issue = [&]() -> bool {  // part `issued`, if there is one
+      const bool is_v = issued & 1;
+      if (!is_v) {
+        if (at_batch >= n_batch) {
+          id = id_next;
+          rec = rec_next;
+          n_batch = n_next;
+          at_batch = 0;
+          load_batch();
+        }
+        if (n_batch == 0) return false;
+        id_k = __shfl_sync(0xffffffffu, id, at_batch + lane);
+        rec_k = __shfl_sync(0xffffffffu, rec, at_batch + lane);
+        if (lane >= STEP || at_batch + lane >= n_batch || id_k >= a.n_blocks) id_k = -1;
+        at_batch += STEP;
+      }
+      // (after an abandoned wait the steps are only counted)
+      if (!__any_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort))) {
+        const uint32_t bar = smem_u32(&s_bar[issued % SLOTS]);
+        const uint32_t all = __ballot_sync(0xffffffffu, id_k >= 0);
+        if (lane == 0) {
+          if (!is_v) s_ok[(issued >> 1) & 3] = all;
+          mbar_arrive_expect_tx(bar, __popc(all) * C::HALF_B);
+        }
+        __syncwarp();
+        if (id_k >= 0) {
+          const size_t r = (static_cast<size_t>(id_k) * a.Hkv << rec_bits) + rec_k;
+          bulk_g2s(smem_u32(smem) + (issued % SLOTS) * C::SLOT_B + lane * C::HALF_B,
+                   a.data + r * Kv4Rec<HD>::BYTES + (is_v ? C::HALF_B : 0), C::HALF_B, bar);
+        }
+        copied = issued + 1;
+      }
+      ++issued;
+      return true;
+    };
+    load_batch();
+    int ready = 0;  // parts issued so far
 #pragma unroll 1
-    for (int i = 0; i < SLOTS; ++i) issue();
+    for (int i = 0; i < SLOTS && issue(); ++i) ++ready;
+    // One CTA barrier per step: then the step's K buffer and the last step's V
+    // buffer are free.
+#pragma unroll 1
+    for (int k = 0; 2 * k < ready; ++k) {
+      __syncthreads_or(0);
+      if (k > 0 && issue()) ++ready;
+      if (issue()) ++ready;
+    }
+    // After an abandoned wait: the copies still in flight.
+    if (*static_cast<volatile int*>(&s_abort)) {
+      for (int n = max(0, copied - SLOTS); n < copied; ++n)
+        warp_wait(smem_u32(&s_bar[n % SLOTS]), (n / SLOTS) & 1, nullptr);
+    }
+    return;
   }
 
   const int qrec = warp * RW;                              // first record this warp scores
@@ -500,7 +571,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
 #pragma unroll
     for (int i = 0; i < PW * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m0 = kNoKey, m1 = kNoKey, l0 = 0.0f, l1 = 0.0f;  // heads h0 and h0 + 1
-    __syncthreads();
+    sync_compute();
     const float qf0 = s_qf[h0], qf1 = s_qf[h0 + 1];
 
 #pragma unroll 1
@@ -580,7 +651,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
           s_top[warp * kHeads + 2 * t] = top0;
           s_top[warp * kHeads + 2 * t + 1] = top1;
         }
-        __syncthreads();
+        sync_compute();
         float n0 = m0, n1 = m1;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -600,16 +671,10 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
           o[x][3] *= f1;
         }
         probabilities();
-        __syncthreads();
+        sync_compute();
       }
       l0 += ps0;
       l1 += ps1;
-
-      // ---- refill the buffers of the last step's V and of this step's K
-      if (warp == 0) {
-        if (k > 0) issue();
-        issue();
-      }
 
       // ---- P V of the step for this warp's pieces
       // V scales of positions outside [kbeg, L) and of absent records may be any
@@ -655,7 +720,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
           *reinterpret_cast<float2*>(r + (h0 + 1) * HD) = v;
         });
     }
-    __syncthreads();
+    sync_compute();
     l0 = l1 = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -664,8 +729,9 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
     }
     const Kv4Place cp = s_cp;
     const long long unit0 = s_unit0;
-    const int c_first = static_cast<int>(unit0 / share), c_last = static_cast<int>((unit0 + cp.n - 1) / share);
-    const bool whole = c_first == c_last;
+    const int c_first = cut_units ? s_c_first : static_cast<int>(unit0 / share);
+    const int nparts = cut_units ? s_nparts : static_cast<int>((unit0 + cp.n - 1) / share) - c_first + 1;
+    const bool whole = nparts == 1;
     const int slot = part_slot(c_first, static_cast<int>(blockIdx.x) - c_first);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(cp.b) * a.H + cp.kvh * G) * HD;
     if (vrec0 == 0) {
@@ -702,7 +768,6 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
       // Up to kFan parts are merged at once by the CTA that completes them; more
       // go through one level of merges of kFan neighbours, each left in the
       // slot of its first part.
-      const int nparts = c_last - c_first + 1;
       unsigned* ticket = a.tickets + c_first;  // (a CTA's share has one unit that begins in it and goes on)
       int first = 0, step = 1, n = nparts;
       bool final = true;
@@ -715,12 +780,12 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
 #pragma unroll 1
       while (true) {
         __threadfence();
-        __syncthreads();
+        sync_compute();
         if (tid == 0) {
           s_last = atomicAdd(ticket, 1u) == static_cast<unsigned>(n - 1);
           if (s_last) *ticket = 0u;  // ready for the next call
         }
-        __syncthreads();
+        sync_compute();
         if (!s_last) break;
         __threadfence();
         merge_parts<HD, W>(a, c_first, first, step, n, G, final ? out : nullptr, s_w);
@@ -733,19 +798,14 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::W * 32, Kv4Cfg<HD>::MINB)
       }
     }
     if (cp.left <= nrec) break;
-    __syncthreads();  // (every thread has read the place)
+    sync_compute();  // (every thread has read the place)
     if (tid == 0) {
       Kv4Place p = cp;
       advance(p, nrec);
       s_unit0 = unit0 + cp.n;
       s_cp = p;
     }
-    __syncthreads();
-  }
-  // After an abandoned wait: the copies still in flight.
-  if (s_abort && warp == 0) {
-    for (int n = max(0, issued - SLOTS); n < issued; ++n)
-      warp_wait(smem_u32(&s_bar[n % SLOTS]), (n / SLOTS) & 1, nullptr);
+    sync_compute();
   }
 }
 
@@ -756,7 +816,7 @@ cudaError_t launch_hg(const Kv4DecodeArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.nctas));
-  cfg.blockDim = dim3(C::W * 32);
+  cfg.blockDim = dim3(C::NT);
   cfg.dynamicSmemBytes = C::SMEM_B;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -782,7 +842,7 @@ Kv4DecodePlan plan_h(int window, int H, int Hkv, int B, int max_seq_len) {
   const long long groups = (static_cast<long long>(span) + 15) / 16 + (span < max_seq_len ? 1 : 0);
   const long long units = static_cast<long long>(B) * Hkv;
   // as many CTAs as are resident, each with a step or more
-  long long n = (units * groups + C::STEP - 1) / C::STEP;
+  long long n = units * ((groups + C::STEP - 1) / C::STEP + 1);
   const long long slots = static_cast<long long>(sm_count()) * C::MINB;
   if (n > slots) n = slots;
   static_assert(kKv4MaxCtas <= kFan * kMaxLevel, "two levels of merges");
