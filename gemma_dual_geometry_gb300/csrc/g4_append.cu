@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
   constexpr int kTabs = KV4 ? kAppendMaxTokens : 1;  // tables held at once
   __shared__ DF s_cos_all[kTabs * HALF];
   __shared__ DF s_sin_all[kTabs * HALF];
-  __shared__ int s_tab[KV4 ? 2 * kAppendMaxTokens : 1];  // KV4: each token's table; each table's position
+  [[maybe_unused]] int tok_pos[kAppendMaxTokens], tok_tab[kAppendMaxTokens];  // KV4: position and table of each token
   int tab = 0;  // where the current token's table begins
   auto cos_of = [&](int j) -> DF { return s_cos_all[(KV4 ? tab : 0) + j]; };
   auto sin_of = [&](int j) -> DF { return s_sin_all[(KV4 ? tab : 0) + j]; };
@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
   };
   // KV4: token b's table becomes the current one.
   auto use_table = [&](int b) {
-    tab = s_tab[b - b0] * HALF;
+    tab = 0;
+#pragma unroll
+    for (int i = 1; i < kAppendMaxTokens; ++i)
+      if (i == b - b0) tab = tok_tab[i] * HALF;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       cr[i] = cos_of(lane * E + i).h;
@@ -522,7 +525,8 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
   // Rows of tokens [bA, bB) (all at position pos), flattened in (b, row)
   // order; warp w takes items w, w + 4, ...  The next item's loads are issued
   // before the current one is computed.
-  auto run = [&](int bA, int bB, int pos) {
+  // `then` runs after the first item's loads have been issued.
+  auto run = [&](int bA, int bB, int pos, auto then) {
     int b = bA, row = row0 + warp;
     while (row >= row1 && b < bB) { row -= nr; ++b; }
     RowRef rr = {};
@@ -532,6 +536,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
       rr = row_ref(b, row, pos);
       load_row(rr, lo, hi);
     }
+    then();
     while (b < bB) {
       int bn = b, rn = row + 4;
       while (rn >= row1 && bn < bB) { rn -= nr; ++bn; }
@@ -558,31 +563,33 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
 
   if constexpr (KV4) {
     // A table per distinct position (neighbours that agree share one), all of
-    // them built at once, so that rows of all tokens follow each other.
-    if (threadIdx.x == 0) {
-      int n = -1, last = 0;
-      for (int b = b0; b < b1; ++b) {
-        const int pos = a.positions[b * a.T + t];
-        if (n < 0 || pos != last) s_tab[kAppendMaxTokens + ++n] = last = pos;
-        s_tab[b - b0] = n;
-      }
+    // them built at once while the first rows are on their way, so that rows of
+    // all tokens follow each other.
+#pragma unroll
+    for (int i = 0; i < kAppendMaxTokens; ++i) {
+      tok_pos[i] = a.positions[min(b0 + i, b1 - 1) * a.T + t];
+      tok_tab[i] = i == 0 ? 0 : tok_tab[i - 1] + (tok_pos[i] != tok_pos[i - 1]);
     }
-    __syncthreads();
-    const int ntab = s_tab[b1 - 1 - b0] + 1;
-    for (int idx = threadIdx.x; idx < ntab * HD; idx += blockDim.x) {
-      const int j = (idx >> 1) % HALF, part = idx & 1, at = (idx >> 1) / HALF * HALF + j;
-      if (j < a.n_rot) {
-        bool to_cos;
-        const DF v = sincos_df_part(s_tab[kAppendMaxTokens + idx / HD], a.inv_freq[j], part, to_cos);
-        (to_cos ? s_cos_all : s_sin_all)[at] = v;
-      } else if (part == 0) {
-        s_cos_all[at] = DF{1.0f, 0.0f};
-      } else {
-        s_sin_all[at] = DF{0.0f, 0.0f};
+    run(b0, b1, 0, [&] {
+      const int ntab = tok_tab[kAppendMaxTokens - 1] + 1;
+      for (int idx = threadIdx.x; idx < ntab * HD; idx += blockDim.x) {
+        const int j = (idx >> 1) % HALF, part = idx & 1, tb = idx / HD, at = tb * HALF + j;
+        int pos = tok_pos[0];
+#pragma unroll
+        for (int i = 1; i < kAppendMaxTokens; ++i)
+          if (tok_tab[i] == tb) pos = tok_pos[i];
+        if (j < a.n_rot) {
+          bool to_cos;
+          const DF v = sincos_df_part(pos, a.inv_freq[j], part, to_cos);
+          (to_cos ? s_cos_all : s_sin_all)[at] = v;
+        } else if (part == 0) {
+          s_cos_all[at] = DF{1.0f, 0.0f};
+        } else {
+          s_sin_all[at] = DF{0.0f, 0.0f};
+        }
       }
-    }
-    __syncthreads();
-    run(b0, b1, 0);
+      __syncthreads();
+    });
     return;
   }
   // One cos/sin table serves every token of the CTA when their positions
@@ -592,13 +599,13 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
   for (int b = b0 + 1; b < b1; ++b) same = same && a.positions[b * a.T + t] == p0;
   if (same) {
     build_table(p0);
-    run(b0, b1, p0);
+    run(b0, b1, p0, [] {});
   } else {
     for (int b = b0; b < b1; ++b) {
       if (b > b0) __syncthreads();  // every warp is done with the previous table
       const int pos = a.positions[b * a.T + t];
       build_table(pos);
-      run(b, b + 1, pos);
+      run(b, b + 1, pos, [] {});
     }
   }
 }

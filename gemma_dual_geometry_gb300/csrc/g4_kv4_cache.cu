@@ -211,16 +211,18 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
 
 // ---------------------------------------------------------------- gather
 //
-// A warp per record: 16-byte loads in fragment order, values as fp16 code
-// times scale (exact), written as bf16; a K store writes 8 bytes per lane (32
-// contiguous per row), a V store 4.
+// A warp per 64-element piece of a record: 16-byte loads in fragment order,
+// values as fp16 code times scale (exact), written as bf16; a K store writes 8
+// bytes per lane (32 contiguous per row), a V store 4.  One piece per warp keeps
+// a small gather (a step's new rows) to one round of loads.
 
 template <int HD>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__ Kv4GatherArgs a) {
   using R = Kv4Rec<HD>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int ngroups = a.rows / kKv4Group + 2;  // that rows positions can touch
-  const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int p = (threadIdx.x >> 5) % R::NP;
+  const long long item = static_cast<long long>(blockIdx.x) * (8 / R::NP) + (threadIdx.x >> 5) / R::NP;
   const long long unit = item / ngroups;
   pdl_wait();
   pdl_trigger();
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
   if (a.q_start != nullptr) {
     const int q0 = min(max(a.q_start[b], 0), a.max_seq_len - a.T);
     const int low = a.window > 0 ? max(0, q0 - a.window + 1) : 0;
-    if (gi == 0 && kvh == 0 && lane == 0) a.q_rel[b] = q0 - low;
+    if (gi == 0 && kvh == 0 && p == 0 && lane == 0) a.q_rel[b] = q0 - low;
     first = low;
     rows = min(rows, q0 - low + a.T);
   } else {
@@ -252,60 +254,59 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
   __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(a.k) + static_cast<size_t>(unit) * a.rows * HD;
   __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(a.v) + static_cast<size_t>(unit) * a.rows * HD;
 
+  // Of the record's 16 positions: the row of the first, and how many are held.
+  const int row0 = static_cast<int>(pos0 - first);
+  const int nheld = there ? static_cast<int>(min(16LL, len - pos0)) : 0;
+
   // fp16x2 code times scale, then the exponent, as bf16x2
   auto value = [](uint32_t codes, __half2 s, float mul) -> uint32_t {
     const float2 v = __half22float2(__hmul2(as_half2(codes), s));
     return pack_bf16x2(v.x * mul, v.y * mul);
   };
+  uint4 kc = make_uint4(0, 0, 0, 0), vc = kc, vs = kc;
+  uint2 ks = make_uint2(0, 0);
+  if (there) {
+    kc = *reinterpret_cast<const uint4*>(rec + R::KC + p * 512 + lane * 16);
+    ks = *reinterpret_cast<const uint2*>(rec + R::KS + p * 64 + g * 8);
+    vc = *reinterpret_cast<const uint4*>(rec + R::VC + p * 512 + lane * 16);
+    vs = *reinterpret_cast<const uint4*>(rec + R::VS + p * 64 + t * 16);
+  }
+  const uint32_t kw[2][2] = {{kc.x, kc.y}, {kc.z, kc.w}};
+  const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
+  const uint32_t vsw[4] = {vs.x, vs.y, vs.z, vs.w};
 #pragma unroll
-  for (int p = 0; p < R::NP; ++p) {
-    uint4 kc = make_uint4(0, 0, 0, 0), vc = kc, vs = kc;
-    uint2 ks = make_uint2(0, 0);
-    if (there) {
-      kc = *reinterpret_cast<const uint4*>(rec + R::KC + p * 512 + lane * 16);
-      ks = *reinterpret_cast<const uint2*>(rec + R::KS + p * 64 + g * 8);
-      vc = *reinterpret_cast<const uint4*>(rec + R::VC + p * 512 + lane * 16);
-      vs = *reinterpret_cast<const uint4*>(rec + R::VS + p * 64 + t * 16);
-    }
-    const uint32_t kw[2][2] = {{kc.x, kc.y}, {kc.z, kc.w}};
-    const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
-    const uint32_t vsw[4] = {vs.x, vs.y, vs.z, vs.w};
+  for (int w = 0; w < 4; ++w) {
+    const __half2 s = as_half2(w & 1 ? e4m3x2_hi_f16x2(w < 2 ? ks.x : ks.y) : e4m3x2_f16x2(w < 2 ? ks.x : ks.y));
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const __half2 s = as_half2(w & 1 ? e4m3x2_hi_f16x2(w < 2 ? ks.x : ks.y) : e4m3x2_f16x2(w < 2 ? ks.x : ks.y));
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const long long pos = pos0 + 8 * r + g;
-        if (pos >= first && pos < first + rows) {
-          const bool held = there && pos < len;
-          const __half2 sr = r == 0 ? __low2half2(s) : __high2half2(s);
-          uint2 o = make_uint2(0, 0);
-          if (held) {
-            const uint32_t word = kw[r][w >> 1];
-            o.x = value(w & 1 ? e2m1x2_f16x2<2>(word) : e2m1x2_f16x2<0>(word), sr, a.k_mul);
-            o.y = value(w & 1 ? e2m1x2_f16x2<3>(word) : e2m1x2_f16x2<1>(word), sr, a.k_mul);
-          }
-          *reinterpret_cast<uint2*>(ko + static_cast<size_t>(pos - first) * HD + p * 64 + w * 16 + t * 4) = o;
+    for (int r = 0; r < 2; ++r) {
+      const int m = 8 * r + g;
+      if (static_cast<unsigned>(row0 + m) < static_cast<unsigned>(rows)) {
+        const __half2 sr = r == 0 ? __low2half2(s) : __high2half2(s);
+        uint2 o = make_uint2(0, 0);
+        if (m < nheld) {
+          const uint32_t word = kw[r][w >> 1];
+          o.x = value(w & 1 ? e2m1x2_f16x2<2>(word) : e2m1x2_f16x2<0>(word), sr, a.k_mul);
+          o.y = value(w & 1 ? e2m1x2_f16x2<3>(word) : e2m1x2_f16x2<1>(word), sr, a.k_mul);
         }
+        *reinterpret_cast<uint2*>(ko + static_cast<size_t>(row0 + m) * HD + p * 64 + w * 16 + t * 4) = o;
       }
-      const __half2 s01 = as_half2(e4m3x2_f16x2(vsw[w])), s23 = as_half2(e4m3x2_hi_f16x2(vsw[w]));
+    }
+    const __half2 s01 = as_half2(e4m3x2_f16x2(vsw[w])), s23 = as_half2(e4m3x2_hi_f16x2(vsw[w]));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long pos = pos0 + 8 * (i >> 1) + 2 * t + (i & 1);
-        if (pos >= first && pos < first + rows) {
-          const bool held = there && pos < len;
-          const __half2 sp = i < 2 ? s01 : s23;
-          const __half2 si = i & 1 ? __high2half2(sp) : __low2half2(sp);
-          uint32_t codes;
-          switch (w) {
-            case 0: codes = e2m1x2_f16x2<0>(vw[i]); break;
-            case 1: codes = e2m1x2_f16x2<1>(vw[i]); break;
-            case 2: codes = e2m1x2_f16x2<2>(vw[i]); break;
-            default: codes = e2m1x2_f16x2<3>(vw[i]); break;
-          }
-          *reinterpret_cast<uint32_t*>(vo + static_cast<size_t>(pos - first) * HD + p * 64 + w * 16 + g * 2) =
-              held ? value(codes, si, 1.0f) : 0u;
+    for (int i = 0; i < 4; ++i) {
+      const int m = 8 * (i >> 1) + 2 * t + (i & 1);
+      if (static_cast<unsigned>(row0 + m) < static_cast<unsigned>(rows)) {
+        const __half2 sp = i < 2 ? s01 : s23;
+        const __half2 si = i & 1 ? __high2half2(sp) : __low2half2(sp);
+        uint32_t codes;
+        switch (w) {
+          case 0: codes = e2m1x2_f16x2<0>(vw[i]); break;
+          case 1: codes = e2m1x2_f16x2<1>(vw[i]); break;
+          case 2: codes = e2m1x2_f16x2<2>(vw[i]); break;
+          default: codes = e2m1x2_f16x2<3>(vw[i]); break;
         }
+        *reinterpret_cast<uint32_t*>(vo + static_cast<size_t>(row0 + m) * HD + p * 64 + w * 16 + g * 2) =
+            m < nheld ? value(codes, si, 1.0f) : 0u;
       }
     }
   }
@@ -327,7 +328,8 @@ cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s) {
   const long long items = static_cast<long long>(a.B) * a.Hkv * (a.rows / kKv4Group + 2);
-  const long long ctas = (items + 7) / 8;
+  const int per = 8 * 64 / a.hd;  // records per CTA of 8 warps
+  const long long ctas = (items + per - 1) / per;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ctas));
   switch (a.hd) {
