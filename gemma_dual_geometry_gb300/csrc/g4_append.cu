@@ -253,7 +253,7 @@ __device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t*
 }
 
 template <typename T, int HD, bool KV4>
-__global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && KV4 ? 6 : 8) append_normrope_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int HALF = HD / 2;
   constexpr int E = HD / 64;
   constexpr bool kBF16 = sizeof(T) == 2;
@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
     else
       return rr.dst + d;
   };
+  // (KV4: pos is the token's slot)
   auto row_ref = [&](int b, int row, int pos) -> RowRef {
     const int tok = b * a.T + t;
     RowRef rr;
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
       const int kvh = is_k ? row - a.H : row - a.H - a.Hkv;
       rr.src = static_cast<const T*>(is_k ? a.k_in : a.v_in) + (static_cast<size_t>(tok) * a.Hkv + kvh) * HD;
       if constexpr (KV4) {
-        const int slot = a.slots[tok];
+        const int slot = pos;
         rr.valid = slot >= 0 && slot < a.n_slots;
         const int in_block = slot & ((1 << a.block_shift) - 1);
         rr.dst = nullptr;
@@ -532,6 +533,9 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
     RowRef rr = {};
     HalfBits<T, E> lo, hi;
     [[maybe_unused]] int b_tab = -1;
+    if constexpr (KV4) {
+      if (b < bB && owns) pos = a.slots[b * a.T + t];
+    }
     if (b < bB) {
       rr = row_ref(b, row, pos);
       load_row(rr, lo, hi);
@@ -542,12 +546,17 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
       while (rn >= row1 && bn < bB) { rn -= nr; ++bn; }
       RowRef rrn = {};
       HalfBits<T, E> lon, hin;
+      [[maybe_unused]] int pos_n = pos;
       if (bn < bB) {
-        rrn = row_ref(bn, rn, pos);
+        if constexpr (KV4) {
+          if (bn != b && owns) pos_n = a.slots[bn * a.T + t];
+        }
+        rrn = row_ref(bn, rn, pos_n);
         load_row(rrn, lon, hin);
       }
       if constexpr (KV4) {
         if (b != b_tab) use_table(b_tab = b);
+        rr = row_ref(b, row, pos);  // (again, rather than kept from the load: its registers)
       }
       if (all_rot)
         do_row(rr, lo, hi, std::true_type());
@@ -555,7 +564,10 @@ __global__ void __launch_bounds__(128, HD >= 512 ? (KV4 ? 4 : 5) : HD == 256 && 
         do_row(rr, lo, hi, std::false_type());
       b = bn;
       row = rn;
-      rr = rrn;
+      if constexpr (KV4)
+        pos = pos_n;
+      else
+        rr = rrn;
       lo = lon;
       hi = hin;
     }
