@@ -640,6 +640,9 @@ g4_status g4_attn_out_residual(const void* ao, int32_t M, int32_t K, const void*
 
 namespace {
 
+// Positions of a table's row at most: sums of a length and a few blocks stay in 32 bits.
+constexpr long long kKv4MaxLen = 1LL << 30;
+
 bool kv4_block_size(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 int log2_of(int x) {
   int n = 0;
@@ -683,8 +686,8 @@ g4_status kv4_resolve_src(const g4_layer_params* p, const g4_kv4_pool* pools, in
 // The table's width against a pool's block size (max_blocks * block_size is a length).
 g4_status kv4_check_table(const void* table, int max_blocks, int block_size) {
   if (table == nullptr) return fail(G4_ERR_INVALID_ARG, "block_table must be non-NULL");
-  if (max_blocks < 1 || static_cast<long long>(max_blocks) * block_size > 0x7fffffffLL)
-    return fail(G4_ERR_INVALID_ARG, "max_blocks %d outside [1, (2^31 - 1) / %d]", max_blocks, block_size);
+  if (max_blocks < 1 || static_cast<long long>(max_blocks) * block_size > kKv4MaxLen)
+    return fail(G4_ERR_INVALID_ARG, "max_blocks %d outside [1, 2^30 / %d]", max_blocks, block_size);
   return G4_OK;
 }
 
@@ -712,7 +715,8 @@ g4_status g4_kv4_assign_blocks(int32_t B, int32_t T, int32_t block_size, int32_t
     return fail(G4_ERR_UNSUPPORTED, "block_size %d not supported (16, 32, 64, 128)", block_size);
   if (n_blocks < 1 || static_cast<long long>(n_blocks) * block_size > 0x7fffffffLL)
     return fail(G4_ERR_INVALID_ARG, "%d blocks of %d positions outside [1, 2^31 - 1] positions", n_blocks, block_size);
-  if (max_blocks < 1) return fail(G4_ERR_INVALID_ARG, "max_blocks %d must be >= 1", max_blocks);
+  if (max_blocks < 1 || static_cast<long long>(max_blocks) * block_size > kKv4MaxLen)
+    return fail(G4_ERR_INVALID_ARG, "max_blocks %d outside [1, 2^30 / %d]", max_blocks, block_size);
   if (B > g4::kKv4MaxBatch)
     return fail(G4_ERR_UNSUPPORTED, "B %d exceeds %d sequences", B, g4::kKv4MaxBatch);
   if (static_cast<long long>(B) * max_blocks > 0x7fffffffLL || static_cast<long long>(B) * T > 0x7fffffffLL)

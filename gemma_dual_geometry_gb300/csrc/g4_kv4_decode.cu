@@ -58,11 +58,12 @@ namespace g4 {
 namespace {
 
 constexpr int kHeads = 8;  // columns of the tensor-core product
-constexpr float kSlack = 8.0f;
-constexpr float kShift = 4.0f;
+constexpr float kSlack = 3.0f;
+constexpr float kShift = 4.0f;  // (2^(kSlack + kShift) times the largest scale, 448, stays within fp16)
 constexpr float kNoKey = -1e30f;  // reference of a state that has seen no key
 constexpr int kFan = 16;      // partials that a first merge takes
 constexpr int kCutSteps = 4;   // longest shares, in steps, that are cut at units
+constexpr int kFew = 6;        // partials that one round of loads takes
 constexpr int kMaxLevel = 64;  // partials that a last merge may be left with (CTAs / kFan at most)
 
 // Shape of the kernel at one head_dim (also used by the plan).
@@ -113,7 +114,7 @@ __device__ __forceinline__ Kv4Seq seq_of(const Kv4DecodeArgs& a, int b) {
   s.L = min(max(a.lens[b], 0), a.len_cap);
   s.kbeg = a.window > 0 ? max(0, s.L - a.window) : 0;
   s.first = s.kbeg >> 4;
-  s.n = ((s.L + 15) >> 4) - s.first;
+  s.n = ((s.L - 1) >> 4) + 1 - s.first;  // (none if L is 0)
   return s;
 }
 
@@ -127,6 +128,52 @@ template <int HD, int W>
 __device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first, int first, int step, int n, int G,
                                          __nv_bfloat16* out, float* s_w) {  // (W warps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = G * HD / 4;  // float4 of a slot
+  if (n <= kFew) {
+    // Few parts: every thread forms the weights itself, so that all its loads
+    // are in flight at once.
+#pragma unroll 1
+    for (int idx = threadIdx.x; idx < row; idx += W * 32) {
+      const int h = idx * 4 / HD;
+      const float4* src = reinterpret_cast<const float4*>(a.ws_o) + idx;
+      float2 ml[kFew];
+      float4 v[kFew];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        const int slot = part_slot(c_first, first + min(i, n - 1) * step);
+        ml[i] = __ldcg(&a.ws_ml[slot * kHeads + h]);
+        v[i] = __ldcg(src + static_cast<size_t>(slot) * row);
+      }
+      float M = kNoKey, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        const float w = i < n ? ex2_approx(ml[i].x - M) : 0.0f;
+        if (i < n) {
+          l = fmaf(w, ml[i].y, l);
+          acc[0] = fmaf(w, v[i].x, acc[0]);
+          acc[1] = fmaf(w, v[i].y, acc[1]);
+          acc[2] = fmaf(w, v[i].z, acc[2]);
+          acc[3] = fmaf(w, v[i].w, acc[3]);
+        }
+      }
+      if (out != nullptr) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float f[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+        store_elems<4>(out + idx * 4, f);
+      } else {
+        store_elems<4>(a.ws_o + static_cast<size_t>(part_slot(c_first, first)) * G * HD + idx * 4, acc);
+        if (idx * 4 % HD == 0) s_w[h] = M, s_w[kHeads + h] = l;
+      }
+    }
+    if (out == nullptr) {
+      asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+      if (static_cast<int>(threadIdx.x) < G)
+        a.ws_ml[part_slot(c_first, first) * kHeads + threadIdx.x] = make_float2(s_w[threadIdx.x], s_w[kHeads + threadIdx.x]);
+    }
+    return;
+  }
   for (int h = warp; h < G; h += W) {
     float M = kNoKey;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&a.ws_ml[part_slot(c_first, first + i * step) * kHeads + h]).x);
@@ -150,7 +197,6 @@ __device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first,
   }
   asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
   constexpr int kBatch = 4;
-  const int row = G * HD / 4;  // float4 of a slot
 #pragma unroll 1
   for (int idx = threadIdx.x; idx < row; idx += W * 32) {
     const float* sw = s_w + (idx * 4 / HD) * kMaxLevel;

@@ -6,6 +6,9 @@ calls: g4_kv_append_normrope then g4_attn_prefill / g4_attn_decode (or
 g4_attn_encoder).  Sliding caches may be rings of one window.  Shared-KV
 tail layers get no cache and read their source layer's
 (cortiq-engine g4e.rs `g4e_forward`: `src = kv_share_src.unwrap_or(li)`).
+``PagedAttnStack`` is the same over the paged 4-bit cache: g4_kv4_assign_blocks
+once per step for all layers, then per layer g4_kv4_append_normrope and
+g4_kv4_attn_prefill / g4_kv4_attn_decode.
 Every step runs in the CUDA kernels; this module only allocates and calls.
 """
 
@@ -17,6 +20,20 @@ from . import g4attn as G
 from . import workloads as W
 
 
+def _layers(cfg):
+    """Source layer, geometry and parameters of every layer."""
+    n = len(cfg["types"])
+    is_s = [t == W.SLIDING for t in cfg["types"]]
+    src = [G.g4_kv_share_src(n, cfg["n_shared"], is_s, l) for l in range(n)]
+    if any(s == -2 for s in src):
+        raise ValueError("invalid shared-KV routing for this stack")
+    geo = [W.layer_geometry(cfg, l) for l in range(n)]
+    params = [G.layer_params(g["layer_type"], g["head_dim"], g["n_heads"], g["n_kv_heads"], g["window"],
+                             g["theta"], g["rotary_fraction"], g["eps"], g["attn_scale"], src[l],
+                             g["dtype"]) for l, g in enumerate(geo)]
+    return src, geo, params
+
+
 class AttnStack:
     def __init__(self, cfg, Lmax, device="cuda", B=None):
         self.cfg = cfg
@@ -24,14 +41,7 @@ class AttnStack:
         self.Lmax = Lmax
         self.device = torch.device(device)
         self.n = len(cfg["types"])
-        is_s = [t == W.SLIDING for t in cfg["types"]]
-        self.src = [G.g4_kv_share_src(self.n, cfg["n_shared"], is_s, l) for l in range(self.n)]
-        if any(s == -2 for s in self.src):
-            raise ValueError("invalid shared-KV routing for this stack")
-        self.geo = [W.layer_geometry(cfg, l) for l in range(self.n)]
-        self.params = [G.layer_params(g["layer_type"], g["head_dim"], g["n_heads"], g["n_kv_heads"], g["window"],
-                                      g["theta"], g["rotary_fraction"], g["eps"], g["attn_scale"], self.src[l],
-                                      g["dtype"]) for l, g in enumerate(self.geo)]
+        self.src, self.geo, self.params = _layers(cfg)
         self.table = G.cache_table(self.n)
         self.caches = {}
         tdt = W.torch_dtype(cfg["dtype"])
@@ -81,3 +91,82 @@ class AttnStack:
     def decode_launches(self, l):
         """Kernels one g4_attn_decode or g4_decode_step call launches."""
         return 1
+
+
+class PagedAttnStack:
+    """A stack over the paged 4-bit cache: B sequence slots of at most max_len positions, whose layers share
+    one block table and n_blocks blocks of block_size positions.  ``k_exp`` as in g4_kv4_pool."""
+
+    def __init__(self, cfg, max_len, n_blocks, block_size=64, device="cuda", B=None, k_exp=0):
+        self.cfg = cfg
+        self.B = cfg["B"] if B is None else B
+        self.device = torch.device(device)
+        self.n = len(cfg["types"])
+        self.n_blocks, self.block_size = n_blocks, block_size
+        self.max_blocks = -(-max_len // block_size)
+        self.max_len = self.max_blocks * block_size
+        self.src, self.geo, self.params = _layers(cfg)
+        self.table = G.kv4_pool_table(self.n)
+        self.pools = {}
+        for l, g in enumerate(self.geo):
+            if self.src[l] < 0:
+                size = G.kv4_pool_bytes(n_blocks, cfg["Hkv"], block_size, g["head_dim"])
+                self.pools[l] = torch.zeros(size, dtype=torch.uint8, device=self.device)
+                G.set_kv4_pool(self.table, l, self.pools[l], g["layer_type"], g["head_dim"], cfg["Hkv"], n_blocks,
+                               block_size, k_exp)
+
+        def i32(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=self.device)
+
+        self.block_table = i32(self.B, self.max_blocks)
+        self.free_blocks = torch.arange(n_blocks, dtype=torch.int32, device=self.device)
+        self.free_count = torch.full((1,), n_blocks, dtype=torch.int32, device=self.device)
+        self.lens = i32(self.B)    # positions held
+        self.start = i32(self.B)   # and held before the last assign()
+        # one decode workspace serves all layers in turn
+        self.ws_bytes = max(G.g4_kv4_decode_workspace_size(p, self.B, self.max_len) for p in self.params)
+        self.ws = torch.zeros(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
+        self._i32 = i32
+        self._steps = {}           # T -> (positions, slots, prefill workspace)
+
+    def _step(self, T):
+        if T not in self._steps:
+            size = max(G.g4_kv4_prefill_workspace_size(p, self.B, T, self.max_len) for p in self.params) if T > 1 else 0
+            self._steps[T] = (self._i32(self.B, T), self._i32(self.B, T),
+                              torch.empty(size, dtype=torch.uint8, device=self.device))
+        return self._steps[T]
+
+    def owns(self, l):
+        return self.src[l] < 0
+
+    def cache_bytes(self):
+        return sum(p.numel() for p in self.pools.values())
+
+    def assign(self, new_lens, T, stream=None):
+        """Blocks for sequences that go to new_lens [B] positions with T new tokens at most (0 ends one).
+        Sets ``lens`` (what was granted) and ``start``; the T tokens' positions and slots serve append()."""
+        positions, slots, _ = self._step(T)
+        self.start.copy_(self.lens)
+        G.g4_kv4_assign_blocks(self.B, T, self.block_size, self.n_blocks, self.max_blocks, self.lens, new_lens,
+                               self.free_blocks, self.free_count, self.block_table, self.lens, self.free_count,
+                               positions, slots, stream=stream)
+        return positions, slots
+
+    def append(self, l, q, k, v, qw, kw, T, q_out, stream=None):
+        positions, slots, _ = self._step(T)
+        G.g4_kv4_append_normrope(self.params[l], self.table, l, q, k, v, qw, kw, positions,
+                                 slots if self.owns(l) else None, self.B, T, q_out, stream=stream)
+
+    def prefill_attn(self, l, q_out, T, out, stream=None):
+        ws = self._step(T)[2]
+        G.g4_kv4_attn_prefill(self.params[l], self.table, l, q_out, self.block_table, self.max_blocks, self.start,
+                              self.lens, self.B, T, self.max_len, out, ws, ws.numel(), stream=stream)
+
+    def decode_attn(self, l, q_out, out, stream=None):
+        G.g4_kv4_attn_decode(self.params[l], self.table, l, q_out, self.block_table, self.max_blocks, self.lens,
+                             self.B, self.max_len, out, self.ws, self.ws_bytes, stream=stream)
+
+    def gather(self, l, start, rows, k_out, v_out, stream=None):
+        """Positions [start[b], start[b] + rows) of every sequence as bf16 rows."""
+        G.g4_kv4_gather(self.params[l], self.table, l, self.block_table, self.max_blocks, start, self.lens, self.B,
+                        rows, k_out, v_out, stream=stream)

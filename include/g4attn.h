@@ -406,7 +406,8 @@ g4_status g4_attn_decode_noalloc(const g4_layer_params* params, const g4_kv_cach
  *   k_exp       k is stored divided by 2^k_exp, -32 .. 32.  The e4m3 scales
  *               reach from 2^-9 to 448: 0 suits k_norm_w around 1; with k
  *               rows of another size take log2 of that size.
- * n_blocks * block_size must not exceed 2^31 - 1.  Layers that read another
+ * n_blocks * block_size must not exceed 2^31 - 1, and max_blocks * block_size of
+ * a block table 2^30.  Layers that read another
  * layer's pool may leave their entry zeroed.
  */
 typedef struct {

@@ -403,3 +403,35 @@ def test_lifecycle_under_graphs():
                     q, at = qn[b:b + 1, :fresh], (old[b] + np.arange(fresh))[None]
                 ref, mag = attention_and_scale(q, k, v, at, np.array([m]), 2, g)
                 assert_within(f64(z["out"][b:b + 1, :fresh]), ref, mag, C_DECODE if T == 1 else C_PREFILL, f"step {step}", keys=m if T == 1 else 0)
+
+
+@pytest.mark.parametrize("geo", [(W.FULL, 256, 8, 2, 0), (W.FULL, 128, 8, 1, 0), (W.FULL, 512, 2, 2, 0)])
+def test_decode_nan_stays_in_its_head_and_large_scales(geo):
+    """A NaN in q or in a visible row reaches its own heads only; value scales up to e4m3's largest do not
+    overflow the fp16 products (rows of the append never come near: their mean square is 1)."""
+    g = geo_of(geo)
+    hd, H, Hkv = g["head_dim"], g["n_heads"], g["n_kv_heads"]
+    lens = np.array([90, 90])
+    pool = Pool(g, 2, 90, 32, seed=3).fill(lens, 4)
+    kc, ks, vc, vs = K.record_offsets(hd)
+    for b in range(2):
+        for p in range(90):
+            rec = pool.data[pool.table[b, p // 32], :, p % 32 // 16]
+            rec[:, vs[p % 16, 0::16]] = 126 - p % 3   # 448, 416, 384
+    q = bf16_normal((2, H, hd), 5)
+    q[1, H - 1, 7] = float("nan")
+    if Hkv > 1:
+        pool.data[pool.table[0, 1], 0, 0, ks[5, 32]] = 127   # position 37 of sequence 0, kv head 0
+    pool.to_device()
+    out = f64(decode_gpu(g, pool, q, lens))
+    bad = np.zeros((2, H), bool)
+    bad[1, H - 1] = True
+    if Hkv > 1:
+        bad[0, :H // Hkv] = True
+    assert np.isnan(out[bad]).all()
+    k, v = pool.rows(lens, 90)
+    ok = ~bad
+    with np.errstate(invalid="ignore"):
+        ref, mag = attention_and_scale(f64(q)[:, None], k, v, (lens - 1)[:, None], lens, Hkv, g)
+    # (keys * 2^-25 of kv4_common.assert_within is for scales up to 1.6)
+    assert_within(out[ok], ref[:, 0][ok], mag[:, 0][ok], C_DECODE, keys=90 * 449 / 2.6)
