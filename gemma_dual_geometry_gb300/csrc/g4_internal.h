@@ -224,7 +224,7 @@ struct Kv4DecodeArgs {
   void* out;
   float* ws_o;        // [2 nctas][G][hd] partial outputs: two units of a CTA's share may continue in other CTAs'
   float2* ws_ml;      // [2 nctas][8] their softmax references and denominators
-  unsigned* tickets;  // arrival counters (zero between calls): [kKv4MaxCtas] of units, [2 kKv4MaxCtas] of parts of them
+  unsigned* tickets;  // arrival counters (zero between calls), [4 levels of merges][2 kKv4MaxCtas]
   int* err;
   int B, H, Hkv, hd, max_blocks, n_blocks, block_shift;
   int window;  // 0 on a full layer
@@ -235,7 +235,7 @@ struct Kv4DecodeArgs {
 // Workspace: the tickets, then ws_ml, then ws_o.  The tickets are in front and of
 // a fixed size, so calls of different shapes may take turns on one workspace.
 constexpr int kKv4MaxCtas = 1024;
-constexpr size_t kKv4TicketBytes = 3 * kKv4MaxCtas * 4;
+constexpr size_t kKv4TicketBytes = 4 * 2 * kKv4MaxCtas * 4;
 struct Kv4DecodePlan {
   int nctas;
   size_t ml_bytes, o_bytes, ws_bytes;

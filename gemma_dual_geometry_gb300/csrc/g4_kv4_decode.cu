@@ -61,10 +61,8 @@ constexpr int kHeads = 8;  // columns of the tensor-core product
 constexpr float kSlack = 3.0f;
 constexpr float kShift = 4.0f;  // (2^(kSlack + kShift) times the largest scale, 448, stays within fp16)
 constexpr float kNoKey = -1e30f;  // reference of a state that has seen no key
-constexpr int kFan = 16;      // partials that a first merge takes
+constexpr int kFan = 8;        // partials merged at once
 constexpr int kCutSteps = 4;   // longest shares, in steps, that are cut at units
-constexpr int kFew = 6;        // partials that one round of loads takes
-constexpr int kMaxLevel = 64;  // partials that a last merge may be left with (CTAs / kFan at most)
 
 // Shape of the kernel at one head_dim (also used by the plan).
 template <int HD>
@@ -85,7 +83,6 @@ struct Kv4Cfg {
   static constexpr int P_B = 2 * STEP * 32 * 8;
   static constexpr int RED_OFF = P_OFF + P_B;                   // partial O of warps that share a piece
   static constexpr int SMEM_B = RED_OFF + (KS > 1 ? kHeads * HD * KS * 4 : 0);
-  static_assert(P_B >= kHeads * kMaxLevel * 4, "the merge's weights take the place of the probabilities");
   static_assert(MINB * (SMEM_B + 1024 + 1024) <= 227 * 1024, "shared memory of the resident CTAs");
 };
 
@@ -122,106 +119,55 @@ __device__ __forceinline__ Kv4Seq seq_of(const Kv4DecodeArgs& a, int b) {
 // where the unit begins, else the first.
 __device__ __forceinline__ int part_slot(int c_first, int i) { return 2 * (c_first + i) + (i == 0 ? 1 : 0); }
 
-// Merges n <= kMaxLevel parts first, first + step, ... of a unit into out, or
-// with out null (un-normalised) into the slot of the first.
+// Merges n <= kFan parts first, first + step, ... of a unit into out, or with out
+// null (un-normalised) into the slot of the first.  Every thread forms the weights
+// itself, so that all its loads are in flight at once.  s_ml: 2 kHeads floats.
 template <int HD, int W>
 __device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first, int first, int step, int n, int G,
-                                         __nv_bfloat16* out, float* s_w) {  // (W warps)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+                                            __nv_bfloat16* out, float* s_ml) {  // (W warps)
   const int row = G * HD / 4;  // float4 of a slot
-  if (n <= kFew) {
-    // Few parts: every thread forms the weights itself, so that all its loads
-    // are in flight at once.
-#pragma unroll 1
-    for (int idx = threadIdx.x; idx < row; idx += W * 32) {
-      const int h = idx * 4 / HD;
-      const float4* src = reinterpret_cast<const float4*>(a.ws_o) + idx;
-      float2 ml[kFew];
-      float4 v[kFew];
-#pragma unroll
-      for (int i = 0; i < kFew; ++i) {
-        const int slot = part_slot(c_first, first + min(i, n - 1) * step);
-        ml[i] = __ldcg(&a.ws_ml[slot * kHeads + h]);
-        v[i] = __ldcg(src + static_cast<size_t>(slot) * row);
-      }
-      float M = kNoKey, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < kFew; ++i) M = fmaxf(M, ml[i].x);
-#pragma unroll
-      for (int i = 0; i < kFew; ++i) {
-        const float w = i < n ? ex2_approx(ml[i].x - M) : 0.0f;
-        if (i < n) {
-          l = fmaf(w, ml[i].y, l);
-          acc[0] = fmaf(w, v[i].x, acc[0]);
-          acc[1] = fmaf(w, v[i].y, acc[1]);
-          acc[2] = fmaf(w, v[i].z, acc[2]);
-          acc[3] = fmaf(w, v[i].w, acc[3]);
-        }
-      }
-      if (out != nullptr) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const float f[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
-        store_elems<4>(out + idx * 4, f);
-      } else {
-        store_elems<4>(a.ws_o + static_cast<size_t>(part_slot(c_first, first)) * G * HD + idx * 4, acc);
-        if (idx * 4 % HD == 0) s_w[h] = M, s_w[kHeads + h] = l;
-      }
-    }
-    if (out == nullptr) {
-      asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
-      if (static_cast<int>(threadIdx.x) < G)
-        a.ws_ml[part_slot(c_first, first) * kHeads + threadIdx.x] = make_float2(s_w[threadIdx.x], s_w[kHeads + threadIdx.x]);
-    }
-    return;
-  }
-  for (int h = warp; h < G; h += W) {
-    float M = kNoKey;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&a.ws_ml[part_slot(c_first, first + i * step) * kHeads + h]).x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    float l = 0.0f;
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = __ldcg(&a.ws_ml[part_slot(c_first, first + i * step) * kHeads + h]);
-      const float w = ex2_approx(ml.x - M);
-      s_w[h * kMaxLevel + i] = w;
-      l += w * ml.y;
-    }
-    l = warp_sum(l);
-    __syncwarp();
-    if (out != nullptr) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      for (int i = lane; i < n; i += 32) s_w[h * kMaxLevel + i] *= inv;
-    } else if (lane == 0) {
-      a.ws_ml[part_slot(c_first, first) * kHeads + h] = make_float2(M, l);
-    }
-  }
-  asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
-  constexpr int kBatch = 4;
 #pragma unroll 1
   for (int idx = threadIdx.x; idx < row; idx += W * 32) {
-    const float* sw = s_w + (idx * 4 / HD) * kMaxLevel;
+    const int h = idx * 4 / HD;
     const float4* src = reinterpret_cast<const float4*>(a.ws_o) + idx;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-      float4 v[kBatch];  // loads in flight
+    float2 ml[kFan];
+    float4 v[kFan];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (i0 + i < n) v[i] = __ldcg(src + static_cast<size_t>(part_slot(c_first, first + (i0 + i) * step)) * row);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (i0 + i < n) {
-          const float w = sw[i0 + i];
-          acc[0] = fmaf(w, v[i].x, acc[0]);
-          acc[1] = fmaf(w, v[i].y, acc[1]);
-          acc[2] = fmaf(w, v[i].z, acc[2]);
-          acc[3] = fmaf(w, v[i].w, acc[3]);
-        }
+    for (int i = 0; i < kFan; ++i) {
+      const int slot = part_slot(c_first, first + min(i, n - 1) * step);
+      ml[i] = __ldcg(&a.ws_ml[slot * kHeads + h]);
+      v[i] = __ldcg(src + static_cast<size_t>(slot) * row);
     }
-    if (out != nullptr)
-      store_elems<4>(out + idx * 4, acc);
-    else
+    float M = kNoKey, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kFan; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < kFan; ++i) {
+      if (i < n) {
+        const float w = ex2_approx(ml[i].x - M);
+        l = fmaf(w, ml[i].y, l);
+        acc[0] = fmaf(w, v[i].x, acc[0]);
+        acc[1] = fmaf(w, v[i].y, acc[1]);
+        acc[2] = fmaf(w, v[i].z, acc[2]);
+        acc[3] = fmaf(w, v[i].w, acc[3]);
+      }
+    }
+    if (out != nullptr) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float f[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+      store_elems<4>(out + idx * 4, f);
+    } else {
       store_elems<4>(a.ws_o + static_cast<size_t>(part_slot(c_first, first)) * G * HD + idx * 4, acc);
+      if (idx * 4 % HD == 0) {
+        s_ml[h] = M;
+        s_ml[kHeads + h] = l;
+      }
+    }
+  }
+  if (out == nullptr) {  // (the first part's M and l are overwritten once every thread has read them)
+    asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+    if (static_cast<int>(threadIdx.x) < G)
+      a.ws_ml[part_slot(c_first, first) * kHeads + threadIdx.x] = make_float2(s_ml[threadIdx.x], s_ml[kHeads + threadIdx.x]);
   }
 }
 
@@ -255,7 +201,6 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = a.H / a.Hkv;
-  float* s_w = reinterpret_cast<float*>(smem + C::P_OFF);  // merge weights (no probabilities then)
   const int h0 = PAIR ? 2 * (t & 1) : 2 * t;               // this lane's columns are heads h0 and h0 + 1
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) mbar_init(smem_u32(&s_bar[i]), 1);
@@ -811,20 +756,14 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
         if (h0 < G) a.ws_ml[slot * kHeads + h0] = make_float2(m0, l0);
         if (h0 + 1 < G) a.ws_ml[slot * kHeads + h0 + 1] = make_float2(m1, l1);
       }
-      // Up to kFan parts are merged at once by the CTA that completes them; more
-      // go through one level of merges of kFan neighbours, each left in the
-      // slot of its first part.
-      unsigned* ticket = a.tickets + c_first;  // (a CTA's share has one unit that begins in it and goes on)
-      int first = 0, step = 1, n = nparts;
-      bool final = true;
-      if (nparts > kFan) {
-        first = (static_cast<int>(blockIdx.x) - c_first) / kFan * kFan;
-        n = min(kFan, nparts - first);
-        ticket = a.tickets + kKv4MaxCtas + part_slot(c_first, first);
-        final = false;
-      }
+      // Parts are merged kFan neighbours at a time by the CTA that completes them,
+      // each merge left in the slot of its first part, until one is left.
+      int mine = static_cast<int>(blockIdx.x) - c_first, left = nparts, step = 1;
+      unsigned* tickets = a.tickets;  // [level][slot of a merge's first part]
 #pragma unroll 1
       while (true) {
+        const int first = mine / kFan * kFan, n = min(kFan, left - first);
+        unsigned* ticket = tickets + part_slot(c_first, first * step);
         __threadfence();
         sync_compute();
         if (tid == 0) {
@@ -834,13 +773,13 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
         sync_compute();
         if (!s_last) break;
         __threadfence();
-        merge_parts<HD, W>(a, c_first, first, step, n, G, final ? out : nullptr, s_w);
+        const bool final = left <= kFan;
+        merge_parts<HD, W>(a, c_first, first * step, step, n, G, final ? out : nullptr, s_top);
         if (final) break;
-        ticket = a.tickets + c_first;
-        first = 0;
-        step = kFan;
-        n = (nparts + kFan - 1) / kFan;
-        final = true;
+        mine /= kFan;
+        left = (left + kFan - 1) / kFan;
+        step *= kFan;
+        tickets += 2 * kKv4MaxCtas;
       }
     }
     if (cp.left <= nrec) break;
@@ -891,7 +830,7 @@ Kv4DecodePlan plan_h(int window, int H, int Hkv, int B, int max_seq_len) {
   long long n = units * ((groups + C::STEP - 1) / C::STEP + 1);
   const long long slots = static_cast<long long>(sm_count()) * C::MINB;
   if (n > slots) n = slots;
-  static_assert(kKv4MaxCtas <= kFan * kMaxLevel, "two levels of merges");
+  static_assert(kKv4MaxCtas <= kFan * kFan * kFan * kFan, "levels of merges");
   if (n > kKv4MaxCtas) n = kKv4MaxCtas;
   Kv4DecodePlan p;
   p.nctas = static_cast<int>(n);

@@ -435,3 +435,18 @@ def test_decode_nan_stays_in_its_head_and_large_scales(geo):
         ref, mag = attention_and_scale(f64(q)[:, None], k, v, (lens - 1)[:, None], lens, Hkv, g)
     # (keys * 2^-25 of kv4_common.assert_within is for scales up to 1.6)
     assert_within(out[ok], ref[:, 0][ok], mag[:, 0][ok], C_DECODE, keys=90 * 449 / 2.6)
+
+
+def test_decode_one_sequence_over_the_whole_gpu():
+    """One kv head of one long sequence: every CTA holds a part, three levels of merges."""
+    g = geometry(W.FULL, 64, H=2, Hkv=1)
+    L = 60000
+    pool = Pool(g, 1, L, 128, seed=4).fill([L], 5).to_device()
+    q = bf16_normal((1, 2, 64), 6)
+    k, v = pool.rows([L], L)
+    ref, mag = attention_and_scale(f64(q)[:, None], k, v, np.array([[L - 1]]), [L], 1, g)
+    nb = G.g4_kv4_decode_workspace_size(params_of(g), 1, pool.per * 128)
+    ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
+    first = f64(decode_gpu(g, pool, q, [L], ws=ws))
+    assert_within(first, ref[:, 0], mag[:, 0], C_DECODE, keys=L)
+    assert np.array_equal(f64(decode_gpu(g, pool, q, [L], ws=ws)), first)
