@@ -60,7 +60,7 @@ namespace {
 constexpr int kHeads = 8;  // columns of the tensor-core product
 constexpr float kSlack = 3.0f;
 constexpr float kShift = 4.0f;  // (2^(kSlack + kShift) times the largest scale, 448, stays within fp16)
-constexpr float kNoKey = -1e30f;  // reference of a state that has seen no key
+constexpr float kNoKey = -3e38f;  // reference of a state that has seen no key (finite: no inf - inf)
 constexpr int kFan = 8;        // partials merged at once
 constexpr int kCutSteps = 4;   // longest shares, in steps, that are cut at units
 
@@ -758,11 +758,11 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
       }
       // Parts are merged kFan neighbours at a time by the CTA that completes them,
       // each merge left in the slot of its first part, until one is left.
-      int mine = static_cast<int>(blockIdx.x) - c_first, left = nparts, step = 1;
+      int part = static_cast<int>(blockIdx.x) - c_first, left = nparts, step = 1;
       unsigned* tickets = a.tickets;  // [level][slot of a merge's first part]
 #pragma unroll 1
       while (true) {
-        const int first = mine / kFan * kFan, n = min(kFan, left - first);
+        const int first = part / kFan * kFan, n = min(kFan, left - first);
         unsigned* ticket = tickets + part_slot(c_first, first * step);
         __threadfence();
         sync_compute();
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
         const bool final = left <= kFan;
         merge_parts<HD, W>(a, c_first, first * step, step, n, G, final ? out : nullptr, s_top);
         if (final) break;
-        mine /= kFan;
+        part /= kFan;
         left = (left + kFan - 1) / kFan;
         step *= kFan;
         tickets += 2 * kKv4MaxCtas;

@@ -97,12 +97,13 @@ def test_assign_no_sequences():
 # ---------------------------------------------------------------- append
 
 @pytest.mark.parametrize("geo", GEOS)
-@pytest.mark.parametrize("B,T,bs,k_exp", [(3, 1, 16, 0), (2, 37, 32, -2), (1, 150, 128, 3)])
+@pytest.mark.parametrize("B,T,bs,k_exp", [(3, 1, 16, 0), (2, 37, 32, -2), (1, 150, 128, 3), (7, 18, 64, 0)])
 def test_append_bytes(geo, B, T, bs, k_exp):
     g = geo_of(geo)
     hd, H, Hkv = g["head_dim"], g["n_heads"], g["n_kv_heads"]
     rng = np.random.default_rng(hd + T)
     start = rng.integers(0, 100, B)
+    start[1:3] = start[0]        # neighbours that share a cos/sin table
     pool = Pool(g, B, 100 + T, bs, seed=hd + B, k_exp=k_exp)
     x = {c: bf16_normal((B, T, h, hd), 50 + i) for i, (c, h) in enumerate((("q", H), ("k", Hkv), ("v", Hkv)))}
     x["k"][0, 0, 0, 3] = 1e-30   # a tiny value, and an all-zero row
@@ -256,6 +257,12 @@ def test_decode_extreme_queries():
     k, v = pool.rows(lens, 130)
     ref, mag = attention_and_scale(f64(q)[:, None], k, v, (lens - 1)[:, None], lens, 1, g)
     assert_within(out, ref[:, 0], mag[:, 0], C_DECODE, keys=130)
+    # scores far below zero (log2 around -1e32) still weigh against each other: one key is all of it
+    one = Pool(g, 1, 16, 16, seed=5).fill([1], 6).to_device()
+    big = torch.full((1, 8, 128), -(2.0 ** 100), dtype=torch.bfloat16)
+    k, v = one.rows([1], 16)
+    big = torch.sign(torch.from_numpy(k[0, :, 0])).to(torch.bfloat16) * big
+    assert_within(f64(decode_gpu(g, one, big, [1])), np.repeat(v[:, :, 0], 8, 1), np.abs(np.repeat(v[:, :, 0], 8, 1)), C_DECODE)
 
 
 def test_decode_absent_blocks_and_clamped_lengths():
@@ -450,3 +457,36 @@ def test_decode_one_sequence_over_the_whole_gpu():
     first = f64(decode_gpu(g, pool, q, [L], ws=ws))
     assert_within(first, ref[:, 0], mag[:, 0], C_DECODE, keys=L)
     assert np.array_equal(f64(decode_gpu(g, pool, q, [L], ws=ws)), first)
+
+
+def test_offsets_past_32_bits():
+    """A pool of 5.3 GB: rows in its last blocks are those of a small pool, byte for byte, and attend alike."""
+    g = geometry(W.FULL, 512, H=8, Hkv=2)
+    p = params_of(g)
+    n, bs, T = 36000, 128, 200
+    q, k, v = (bf16_normal((1, T, h, 512), s).to(DEV) for h, s in ((8, 1), (2, 2), (2, 3)))
+    qw, kw = W.norm_weight(512, 4).to(DEV), W.norm_weight(512, 5).to(DEV)
+    pos = np.arange(T)[None]
+    res = []
+    for blocks, count in (([[1, 0]], 2), ([[n - 1, n - 2]], n)):
+        data = torch.zeros(G.kv4_pool_bytes(count, 2, bs, 512), dtype=torch.uint8, device=DEV)
+        pools = G.kv4_pool_table(1)
+        G.set_kv4_pool(pools, 0, data, W.FULL, 512, 2, count, bs)
+        slots = np.asarray(blocks)[0][pos // bs] * bs + pos % bs
+        qo, out = torch.empty_like(q), torch.empty_like(q)
+        G.g4_kv4_append_normrope(p, pools, 0, q, k, v, qw, kw, i32(pos), i32(slots), 1, T, qo)
+        table = i32(blocks)
+        nb = G.g4_kv4_decode_workspace_size(p, 1, T)
+        ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
+        dec = torch.empty((1, 8, 512), dtype=torch.bfloat16, device=DEV)
+        G.g4_kv4_attn_decode(p, pools, 0, qo[:, -1].contiguous(), table, 2, i32([T]), 1, T, dec, ws, nb)
+        nb = G.g4_kv4_prefill_workspace_size(p, 1, T, T)
+        ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+        G.g4_kv4_attn_prefill(p, pools, 0, qo, table, 2, i32([0]), i32([T]), 1, T, T, out, ws, nb)
+        ko, vo = (torch.empty((1, 2, T, 512), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        G.g4_kv4_gather(p, pools, 0, table, 2, i32([0]), i32([T]), 1, T, ko, vo)
+        res.append((dec, out, ko, vo))
+        del data
+    for a, b in zip(*res):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+    torch.cuda.empty_cache()
