@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     }
   };
   // O^T += V^T (P s)^T for 64 elements of a record's values
-  auto add_piece = [&](float (*o)[4], const uint8_t* rec, int p, uint2 pp, uint32_t vmask) {
+  auto add_piece = [&](float (*o)[4], const uint8_t* rec, int p, uint2 pp) {
     const uint4 vc = *reinterpret_cast<const uint4*>(rec + p * 512 + lane * 16);
     const __half2 pa = as_half2(pp.x), pb = as_half2(pp.y);
     // pairs of positions side by side, for the even and the odd elements
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     if constexpr (PAIR) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t sw = *reinterpret_cast<const uint32_t*>(vs + (2 * j + (g >> 2)) * 4) & vmask;
+        const uint32_t sw = *reinterpret_cast<const uint32_t*>(vs + (2 * j + (g >> 2)) * 4);
         const uint32_t b0 = as_u32(__hmul2(pa, as_half2(e4m3x2_f16x2(sw))));
         const uint32_t b1 = as_u32(__hmul2(pb, as_half2(e4m3x2_hi_f16x2(sw))));
         if (j == 0) {
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
       }
     } else {
       const uint4 v4 = *reinterpret_cast<const uint4*>(vs);
-      const uint32_t vsw[4] = {v4.x & vmask, v4.y & vmask, v4.z & vmask, v4.w & vmask};
+      const uint32_t vsw[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint32_t b0 = as_u32(__hmul2(pa, as_half2(e4m3x2_f16x2(vsw[w]))));
@@ -506,8 +506,18 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
       }
     }
   };
-  auto part_at = [&](int n) { return smem + (n % SLOTS) * C::SLOT_B; };
-  auto wait_part = [&](int n) { return warp_wait(smem_u32(&s_bar[n % SLOTS]), (n / SLOTS) & 1, a.err, &s_abort); };
+  // The parts in turn: buffer and parity of the next one.
+  int slot = 0;
+  uint32_t parity = 0;
+  auto wait_part = [&](const uint8_t*& part) {
+    part = smem + slot * C::SLOT_B;
+    const bool ok = warp_wait(smem_u32(&s_bar[slot]), parity, a.err, &s_abort);
+    if (++slot == SLOTS) {
+      slot = 0;
+      parity ^= 1;
+    }
+    return ok;
+  };
 
   int k = 0;  // step of the share
   while (true) {
@@ -574,8 +584,9 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
       float s[RW][4];
 #pragma unroll
       for (int i = 0; i < RW; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-      if (wait_part(2 * k)) {
-        const uint8_t* kpart = part_at(2 * k) + qrec * C::HALF_B;
+      const uint8_t* kpart;
+      if (wait_part(kpart)) {
+        kpart += qrec * C::HALF_B;
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
 #pragma unroll
@@ -668,26 +679,32 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
       l1 += ps1;
 
       // ---- P V of the step for this warp's pieces
-      // V scales of positions outside [kbeg, L) and of absent records may be any
-      // bytes, even NaN: they read as zero
-      const bool masked = edge || gaps;
-      auto vmask_of = [&](int i) -> uint32_t {
-        if (!masked) return 0xffffffffu;
-        if (!((ok >> i) & 1u)) return 0u;
-        const int pos0 = (base + i) * kKv4Group;
-        auto seen = [&](int m) { return pos0 + m >= kbeg && pos0 + m < L; };
-        return (seen(2 * t) ? 0xffu : 0u) | (seen(2 * t + 1) ? 0xff00u : 0u) | (seen(2 * t + 8) ? 0xff0000u : 0u) |
-               (seen(2 * t + 9) ? 0xff000000u : 0u);
-      };
-      if (wait_part(2 * k + 1)) {
-        const uint8_t* vpart = part_at(2 * k + 1);
+      const uint8_t* vpart;
+      const bool vthere = wait_part(vpart);
+      if (edge || gaps) {
+        // V scales of positions outside [kbeg, L) and of absent records may be
+        // any bytes, even NaN: each warp zeroes those of the records it scored.
+#pragma unroll
+        for (int i = qrec; i < qrec + RW; ++i) {
+          uint32_t* vs = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(vpart) + i * C::HALF_B + 8 * HD);
+          for (int x = lane; x < HD / 4; x += 32) {
+            const int m = (base + i) * kKv4Group + 2 * ((x >> 2) & 3);  // the word's positions: m, m + 1, m + 8, m + 9
+            auto seen = [&](int pos) { return pos >= kbeg && pos < L; };
+            const uint32_t mask = (seen(m) ? 0xffu : 0u) | (seen(m + 1) ? 0xff00u : 0u) |
+                                  (seen(m + 8) ? 0xff0000u : 0u) | (seen(m + 9) ? 0xff000000u : 0u);
+            vs[x] = (ok >> i) & 1u ? vs[x] & mask : 0u;
+          }
+        }
+        fence_proxy_async_smem();  // (the next copy into this buffer comes after these stores)
+        sync_compute();
+      }
+      if (vthere) {
 #pragma unroll
         for (int ii = 0; ii < STEP / KS; ++ii) {
           const int i = vrec0 + ii * KS;
           const uint2 pp = pbuf[i * 32 + lane];
-          const uint32_t vmask = vmask_of(i);
 #pragma unroll
-          for (int pi = 0; pi < PW; ++pi) add_piece(o + pi * 4, vpart + i * C::HALF_B, vpiece + pi, pp, vmask);
+          for (int pi = 0; pi < PW; ++pi) add_piece(o + pi * 4, vpart + i * C::HALF_B, vpiece + pi, pp);
         }
       }
     }
@@ -723,7 +740,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     const int c_first = cut_units ? s_c_first : static_cast<int>(unit0 / share);
     const int nparts = cut_units ? s_nparts : static_cast<int>((unit0 + cp.n - 1) / share) - c_first + 1;
     const bool whole = nparts == 1;
-    const int slot = part_slot(c_first, static_cast<int>(blockIdx.x) - c_first);
+    const int place = part_slot(c_first, static_cast<int>(blockIdx.x) - c_first);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(cp.b) * a.H + cp.kvh * G) * HD;
     if (vrec0 == 0) {
       // (l is zero only where no key was present; a NaN stays one)
@@ -745,7 +762,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
           if (h0 < G) *reinterpret_cast<uint32_t*>(out + h0 * HD + d) = pack_bf16x2(u.x * i0, u.y * i0);
           if (h0 + 1 < G) *reinterpret_cast<uint32_t*>(out + (h0 + 1) * HD + d) = pack_bf16x2(v.x * i1, v.y * i1);
         } else {
-          float* w = a.ws_o + static_cast<size_t>(slot) * G * HD + d;
+          float* w = a.ws_o + static_cast<size_t>(place) * G * HD + d;
           if (h0 < G) *reinterpret_cast<float2*>(w + h0 * HD) = u;
           if (h0 + 1 < G) *reinterpret_cast<float2*>(w + (h0 + 1) * HD) = v;
         }
@@ -753,8 +770,8 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     }
     if (!whole) {
       if (warp == 0 && g == 0) {
-        if (h0 < G) a.ws_ml[slot * kHeads + h0] = make_float2(m0, l0);
-        if (h0 + 1 < G) a.ws_ml[slot * kHeads + h0 + 1] = make_float2(m1, l1);
+        if (h0 < G) a.ws_ml[place * kHeads + h0] = make_float2(m0, l0);
+        if (h0 + 1 < G) a.ws_ml[place * kHeads + h0 + 1] = make_float2(m1, l1);
       }
       // Parts are merged kFan neighbours at a time by the CTA that completes them,
       // each merge left in the slot of its first part, until one is left.
