@@ -110,11 +110,10 @@ def lib():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:  # an address, or None
         return x
-    return x.data_ptr()
 
 
 _raw_stream = None  # device index -> the address of its current stream
