@@ -106,14 +106,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return as_u
 struct Kv4Seq {
   int L, kbeg, first, n;  // visible keys [kbeg, L) in records [first, first + n)
 };
-__device__ __forceinline__ Kv4Seq seq_of(const Kv4DecodeArgs& a, int b) {
+__device__ __forceinline__ Kv4Seq seq_of_len(const Kv4DecodeArgs& a, int len) {
   Kv4Seq s;
-  s.L = min(max(a.lens[b], 0), a.len_cap);
+  s.L = min(max(len, 0), a.len_cap);
   s.kbeg = a.window > 0 ? max(0, s.L - a.window) : 0;
   s.first = s.kbeg >> 4;
   s.n = ((s.L - 1) >> 4) + 1 - s.first;  // (none if L is 0)
   return s;
 }
+
+// (Lengths are read past L1, which may hold what they were before the wait.)
+__device__ __forceinline__ Kv4Seq seq_of(const Kv4DecodeArgs& a, int b) { return seq_of_len(a, __ldcg(a.lens + b)); }
 
 // The slot of a unit's part i, left by CTA c_first + i: the second of its two
 // where the unit begins, else the first.
@@ -174,7 +177,7 @@ __device__ __forceinline__ void merge_parts(const Kv4DecodeArgs& a, int c_first,
 // A place in the units laid end to end: `off` records into (b, kvh), whose
 // sequence has n records from `first` on; `left` records of the share remain.
 struct Kv4Place {
-  int b, kvh, off, left, first, n;
+  int b, kvh, off, left, first, n, L;
 };
 
 // GM: most heads per kv head, 4 (two scale blocks per product) or 8.
@@ -207,10 +210,10 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     fence_mbar_init();
     s_abort = 0;
   }
-  pdl_wait();
-  pdl_trigger();
-
-  // ---- this CTA's share
+  // ---- this CTA's share.  Formed before the wait from the lengths as they stand
+  // (a batch of at most a sequence per thread), while the kernel before this one
+  // finishes; after the wait it stands if no length has changed, else it is
+  // formed again.  Nothing else is read before the wait, nothing written.
   const int per = (a.B + NT - 1) / NT;  // consecutive sequences per thread
   const int sb0 = min(a.B, tid * per), sb1 = min(a.B, sb0 + per);
   // exclusive sum of x over the threads, and its total
@@ -234,17 +237,91 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
   };
   const int nctas = gridDim.x;
   const long long cta = blockIdx.x;
-  long long sum = 0, total, at;
-  for (int b = sb0; b < sb1; ++b) sum += seq_of(a, b).n;
-  at = scan(sum, total) * a.Hkv;  // records before this thread's sequences
-  total *= a.Hkv;
-  auto steps_up = [](long long n) { return (n + STEP - 1) / STEP * STEP; };
-  long long share = steps_up((total + nctas - 1) / nctas);
-  // Cut at every unit: parts of `cut` records (the last of a unit fewer), which
-  // are at most total / cut + units.
   const long long units = static_cast<long long>(a.B) * a.Hkv;
-  const long long cut = nctas > units ? steps_up((total + nctas - units - 1) / (nctas - units)) : 0;
-  const bool cut_units = cut > 0 && cut <= kCutSteps * STEP;
+  auto steps_up = [](long long n) { return (n + STEP - 1) / STEP * STEP; };
+  long long share = 0;
+  bool cut_units = false;
+  const bool one_each = per <= 1;
+  int my_len = 0;  // one_each: this thread's sequence's
+  auto my_seq = [&](int b) { return one_each ? seq_of_len(a, my_len) : seq_of(a, b); };
+  auto read_len = [&] { return sb0 < sb1 ? __ldcg(a.lens + sb0) : 0; };
+  // Sets share, cut_units and, where this CTA has work, the places; false if it has none.
+  auto form_share = [&]() -> bool {
+    long long sum = 0, total, at;
+    for (int b = sb0; b < sb1; ++b) sum += my_seq(b).n;
+    at = scan(sum, total) * a.Hkv;  // records before this thread's sequences
+    total *= a.Hkv;
+    share = steps_up((total + nctas - 1) / nctas);
+    // Cut at every unit: parts of `cut` records (the last of a unit fewer), which
+    // are at most total / cut + units.
+    const long long cut = nctas > units ? steps_up((total + nctas - units - 1) / (nctas - units)) : 0;
+    cut_units = cut > 0 && cut <= kCutSteps * STEP;
+    Kv4Place p;  // where the share begins, set by the thread that finds it there
+    p.left = 0;
+    auto set = [&](int b, const Kv4Seq& seq, long long kvh, long long off, long long left) {
+      p.b = b;
+      p.kvh = static_cast<int>(kvh);
+      p.off = static_cast<int>(off);
+      p.left = static_cast<int>(left);
+      p.first = seq.first;
+      p.n = seq.n;
+      p.L = seq.L;
+    };
+    bool work;
+    if (cut_units) {
+      long long parts = 0, nparts;
+      for (int b = sb0; b < sb1; ++b) parts += (my_seq(b).n + cut - 1) / cut;
+      long long before = scan(parts, nparts) * a.Hkv;
+      work = cta < nparts * a.Hkv;
+      if (cta >= before && cta < before + parts * a.Hkv) {
+        for (int b = sb0; b < sb1; ++b) {
+          const Kv4Seq seq = my_seq(b);
+          const int np = static_cast<int>((seq.n + cut - 1) / cut);
+          if (cta < before + static_cast<long long>(np) * a.Hkv) {
+            const int rank = static_cast<int>(cta - before), part = rank % np;
+            set(b, seq, rank / np, part * cut, min(cut, seq.n - part * cut));
+            s_c_first = static_cast<int>(cta) - part;
+            s_nparts = np;
+            break;
+          }
+          before += static_cast<long long>(np) * a.Hkv;
+        }
+      }
+    } else {
+      const long long w0 = min(total, share * cta), w1 = min(total, w0 + share);
+      work = w0 < w1;
+      if (work && w0 >= at && w0 < at + sum * a.Hkv) {
+        for (int b = sb0; b < sb1; ++b) {
+          const Kv4Seq seq = my_seq(b);
+          const long long n = seq.n;
+          if (w0 < at + n * a.Hkv) {
+            const long long kvh = (w0 - at) / n;
+            set(b, seq, kvh, w0 - at - kvh * n, w1 - w0);
+            s_unit0 = at + kvh * n;
+            break;
+          }
+          at += n * a.Hkv;
+        }
+      }
+    }
+    if (p.left > 0) s_ip = s_cp = p;
+    __syncthreads();
+    return work;
+  };
+  bool work = false;
+  if (one_each) {
+    my_len = read_len();
+    work = form_share();
+  }
+  pdl_wait();
+  pdl_trigger();
+  bool again = !one_each;
+  if (one_each) {
+    const int len = read_len();
+    again = __syncthreads_or(len != my_len);
+    my_len = len;
+  }
+  if (again) work = form_share();
   // sequences without keys, spread over the CTAs
   for (int b = blockIdx.x; b < a.B; b += nctas) {
     if (seq_of(a, b).n == 0) {
@@ -252,55 +329,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
       for (int i = tid; i < a.H * HD / 2; i += NT) o[i] = 0u;
     }
   }
-  Kv4Place mine;  // where the share begins, set by the thread that finds it there
-  mine.left = 0;
-  if (cut_units) {
-    long long parts = 0, nparts;
-    for (int b = sb0; b < sb1; ++b) parts += (seq_of(a, b).n + cut - 1) / cut;
-    long long before = scan(parts, nparts) * a.Hkv;
-    if (cta >= nparts * a.Hkv) return;
-    if (cta >= before && cta < before + parts * a.Hkv) {
-      for (int b = sb0; b < sb1; ++b) {
-        const Kv4Seq seq = seq_of(a, b);
-        const int np = static_cast<int>((seq.n + cut - 1) / cut);
-        if (cta < before + static_cast<long long>(np) * a.Hkv) {
-          mine.b = b;
-          mine.kvh = static_cast<int>(cta - before) / np;
-          const int part = static_cast<int>(cta - before) % np;
-          mine.off = part * static_cast<int>(cut);
-          mine.left = min(static_cast<int>(cut), seq.n - mine.off);
-          mine.first = seq.first;
-          mine.n = seq.n;
-          s_c_first = static_cast<int>(cta) - part;
-          s_nparts = np;
-          break;
-        }
-        before += static_cast<long long>(np) * a.Hkv;
-      }
-    }
-  } else {
-    const long long w0 = min(total, share * cta), w1 = min(total, w0 + share);
-    if (w0 >= w1) return;
-    if (w0 >= at && w0 < at + sum * a.Hkv) {
-      for (int b = sb0; b < sb1; ++b) {
-        const Kv4Seq seq = seq_of(a, b);
-        const long long n = seq.n;
-        if (w0 < at + n * a.Hkv) {
-          mine.b = b;
-          mine.kvh = static_cast<int>((w0 - at) / n);
-          mine.off = static_cast<int>(w0 - at - mine.kvh * n);
-          mine.left = static_cast<int>(w1 - w0);
-          mine.first = seq.first;
-          mine.n = seq.n;
-          s_unit0 = at + mine.kvh * n;
-          break;
-        }
-        at += n * a.Hkv;
-      }
-    }
-  }
-  if (mine.left > 0) s_ip = s_cp = mine;
-  __syncthreads();
+  if (!work) return;
   // Moves a place n records on within its unit, or to the next unit that has any.
   auto advance = [&](Kv4Place& p, int n) {
     p.off += n;
@@ -315,6 +344,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     } while (seq.n == 0);
     p.first = seq.first;
     p.n = seq.n;
+    p.L = seq.L;
   };
 
   // The computing warps' barrier.
@@ -524,12 +554,7 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     // ---- a unit (or the part of one in this share) begins
     const int r0 = s_cp.first + s_cp.off;                  // first record
     const int nrec = min(s_cp.n - s_cp.off, s_cp.left);
-    int L, kbeg;
-    {
-      const Kv4Seq seq = seq_of(a, s_cp.b);
-      L = seq.L;
-      kbeg = seq.kbeg;
-    }
+    const int L = s_cp.L, kbeg = seq_of_len(a, L).kbeg;
     // q fragments: lane (column g, t) holds elements 4t .. 4t+3 of every 16, two
     // blocks side by side, zeros in columns without a head (and, two blocks to a
     // product, where the other block's elements stand); each head scaled by the

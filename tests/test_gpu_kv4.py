@@ -490,3 +490,41 @@ def test_offsets_past_32_bits():
     for a, b in zip(*res):
         assert torch.equal(a, b) and torch.isfinite(a).all()
     torch.cuda.empty_cache()
+
+
+def test_decode_right_behind_the_kernel_that_sets_the_lengths():
+    """Lengths change in the kernel launched just before, with nothing waited for in between."""
+    g = geometry(W.FULL, 128, H=4, Hkv=2)
+    p = params_of(g)
+    B, bs, steps = 3, 128, 20
+    pool = Pool(g, B, bs, bs, seed=2).fill([bs] * B, 3).to_device()
+    q = bf16_normal((B, 4, 128), 4).to(DEV)
+    nb = G.g4_kv4_decode_workspace_size(p, B, bs)
+    ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
+    lens, left, free = i32([3, 40, 100]), i32([0]), i32(np.zeros(pool.n))
+    want = [i32([3 + i, 40 + i, 100 + i]) for i in range(1, steps + 1)]
+    pos, slots = i32(np.zeros((B, 1))), i32(np.zeros((B, 1)))
+    outs = [torch.empty_like(q) for _ in want]
+    for w, out in zip(want, outs):   # (no sequence leaves its first block)
+        G.g4_kv4_assign_blocks(B, 1, bs, pool.n, 1, lens, w, free, left, pool.d_table, lens, left, pos, slots)
+        G.g4_kv4_attn_decode(p, pool.pools, 0, q, pool.d_table, 1, lens, B, bs, out, ws, nb)
+    for w, out in zip(want, outs):
+        torch.cuda.synchronize()
+        again = torch.empty_like(q)
+        G.g4_kv4_attn_decode(p, pool.pools, 0, q, pool.d_table, 1, w, B, bs, again, ws, nb)
+        assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("B,window", [(300, 0), (700, 20)])
+def test_decode_many_sequences(B, window):
+    """More sequences than a CTA has threads."""
+    g = geometry(W.SLIDING if window else W.FULL, 64, H=2, Hkv=1, window=window)
+    lens = np.random.default_rng(B).integers(0, 50, B)
+    lens[-3:] = 0
+    pool = Pool(g, B, 50, 16, seed=6).fill(lens, 7).to_device()
+    q = bf16_normal((B, 2, 64), 8)
+    out = f64(decode_gpu(g, pool, q, lens))
+    k, v = pool.rows(lens, 50)
+    ref, mag = attention_and_scale(f64(q)[:, None], k, v, (lens - 1)[:, None], lens, 1, g)
+    assert (out[lens == 0] == 0).all()
+    assert_within(out, ref[:, 0], mag[:, 0], C_DECODE, keys=50)
