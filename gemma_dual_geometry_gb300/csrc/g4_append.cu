@@ -524,11 +524,17 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
   };
 
   // Rows of tokens [bA, bB) (all at position pos), flattened in (b, row)
-  // order; warp w takes items w, w + 4, ...  The next item's loads are issued
-  // before the current one is computed.
+  // order; warp w takes items w, w + 4, ... (KV4 with four tokens: those of
+  // token w).  The next item's loads are issued before the current one is computed.
   // `then` runs after the first item's loads have been issued.
   auto run = [&](int bA, int bB, int pos, auto then) {
-    int b = bA, row = row0 + warp;
+    int b = bA, row = row0 + warp, stride = 4;
+    if (KV4 && bB - bA == 4) {  // a token per warp: its cos / sin are loaded once
+      b = bA + warp;
+      bB = b + 1;
+      row = row0;
+      stride = 1;
+    }
     while (row >= row1 && b < bB) { row -= nr; ++b; }
     RowRef rr = {};
     HalfBits<T, E> lo, hi;
@@ -542,7 +548,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     }
     then();
     while (b < bB) {
-      int bn = b, rn = row + 4;
+      int bn = b, rn = row + stride;
       while (rn >= row1 && bn < bB) { rn -= nr; ++bn; }
       RowRef rrn = {};
       HalfBits<T, E> lon, hin;
