@@ -140,9 +140,9 @@ __device__ __forceinline__ void rotate_elems(float* oa, float* ob, const float* 
 // rounding is that of every value within e of it).
 __device__ __forceinline__ bool bf16_decided(float v, float e) { return fabsf(v - bf16_midpoint(v)) > e; }
 
-// Where element d of a row that waits to be quantised lies: 64-element pieces
-// are 32 bytes apart, so that lanes of different pieces meet other banks.
-__host__ __device__ constexpr int kv4_row_at(int d) { return d + (d >> 6) * 16; }
+// Where element d of a finished row lies: 64-element pieces are 16 bytes apart,
+// so that the 16-byte halves of neighbouring lanes' 32 bytes meet other banks.
+__host__ __device__ constexpr int kv4_row_at(int d) { return d + (d >> 6) * 8; }
 
 // Quantises a finished row (bf16 values in shared memory, by kv4_row_at) and
 // stores codes and scales of position m into its record.  Lane l takes the
