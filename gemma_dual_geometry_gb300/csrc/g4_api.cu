@@ -10,7 +10,7 @@
 #include <string>
 
 #include "../../include/g4attn.h"
-#include "g4_internal.h"
+#include "g4_kv4_internal.h"
 
 namespace {
 
@@ -758,7 +758,7 @@ g4_status g4_kv4_append_normrope(const g4_layer_params* params, const g4_kv4_poo
   if (!aligned16(q_in) || !aligned16(q_out) || !aligned16(q_norm_w))
     return fail(G4_ERR_INVALID_ARG, "q_in, q_out and q_norm_w must be 16-byte aligned");
   const bool shared = params->kv_share_src >= 0;
-  g4::AppendArgs a;
+  g4::Kv4AppendArgs a;
   memset(&a, 0, sizeof(a));
   if (shared) {
     if (k_in != nullptr || v_in != nullptr || k_norm_w != nullptr)

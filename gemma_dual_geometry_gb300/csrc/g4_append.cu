@@ -39,6 +39,7 @@
 #include "g4_device.cuh"
 #include "g4_internal.h"
 #include "g4_kv4.cuh"
+#include "g4_kv4_internal.h"
 #include "g4_normrope.cuh"
 
 namespace g4 {
@@ -252,8 +253,11 @@ __device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t*
   }
 }
 
+template <bool KV4>
+using ArgsOf = std::conditional_t<KV4, Kv4AppendArgs, AppendArgs>;
+
 template <typename T, int HD, bool KV4>
-__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ ArgsOf<KV4> a) {
   constexpr int HALF = HD / 2;
   constexpr int E = HD / 64;
   constexpr bool kBF16 = sizeof(T) == 2;
@@ -628,8 +632,8 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
   }
 }
 
-template <typename Kern>
-cudaError_t launch_pdl(Kern kern, dim3 grid, cudaStream_t s, const AppendArgs& a) {
+template <typename Kern, typename Args>
+cudaError_t launch_pdl(Kern kern, dim3 grid, cudaStream_t s, const Args& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(128);
@@ -643,7 +647,7 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, cudaStream_t s, const AppendArgs& a
 }
 
 template <typename T, bool KV4>
-cudaError_t launch_t(const AppendArgs& a, cudaStream_t s) {
+cudaError_t launch_t(const ArgsOf<KV4>& a, cudaStream_t s) {
   const int nrows = a.H + (a.k_in ? 2 * a.Hkv : 0);
   dim3 grid(a.T * ((a.B + a.tok_per_cta - 1) / a.tok_per_cta), (nrows + a.rows_per_cta - 1) / a.rows_per_cta);
   switch (a.hd) {
@@ -661,6 +665,6 @@ cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s) {
   return dtype == 1 ? launch_t<__nv_bfloat16, false>(a, s) : launch_t<float, false>(a, s);
 }
 
-cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t s) { return launch_t<__nv_bfloat16, true>(a, s); }
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) { return launch_t<__nv_bfloat16, true>(a, s); }
 
 }  // namespace g4

@@ -33,7 +33,6 @@ cudaError_t set_smem_limit_once(int bytes) {
 constexpr int kMaxHalf = 256;  // head_dim / 2 for the widest supported head (512)
 
 // Step a4: norm -> RoPE -> cache append.
-constexpr int kAppendMaxTokens = 4;  // tok_per_cta at most of the 4-bit append
 struct AppendArgs {
   const void* q_in;
   const void* k_in;  // null on a shared layer
@@ -50,11 +49,6 @@ struct AppendArgs {
   int tok_per_cta;   // tokens (same t, consecutive b) handled per CTA
   int n_rot;         // rotated pairs; inv_freq[j] == 0 for j >= n_rot
   float eps;
-  // the 4-bit cache: k and v of a token go to its slot of the pool
-  const int32_t* slots;  // [B*T]
-  int n_slots;           // n_blocks * block_size
-  int block_shift;       // log2(block_size)
-  float k_mul;           // 2^-k_exp
   float inv_freq[kMaxHalf];
 };
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s);
@@ -175,72 +169,5 @@ struct DecodePlan {
 };
 DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len);
 int sm_count();  // SMs of the current device
-
-// ---------------------------------------------------------------- the paged 4-bit cache
-// (its layout: include/g4attn.h and g4_kv4.cuh)
-
-struct Kv4AssignArgs {
-  int B, T, block_shift, n_blocks, max_blocks;
-  const int32_t* old_lens;
-  const int32_t* new_lens;
-  int32_t* free_blocks;
-  const int32_t* free_count;
-  int32_t* table;
-  int32_t* lens_out;
-  int32_t* count_out;
-  int32_t* positions;
-  int32_t* slots;
-};
-constexpr int kKv4MaxBatch = 8192;  // a CTA keeps 8 to 16 bytes per sequence in shared memory
-cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s);
-
-// AppendArgs with the 4-bit fields set; cache_k is the layer's pool.
-cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t s);
-
-// Positions [first, first + rows) of every sequence as bf16 rows
-// k, v [B][Hkv][rows][hd].  first is start[b], or with q_start set (prefill)
-// the first position that any of T queries from q_start[b] on sees; then only
-// rows up to the last query are written, and q_rel[b] is the first query's row.
-struct Kv4GatherArgs {
-  const uint8_t* data;
-  const int32_t* table;
-  const int32_t* start;
-  const int32_t* lens;
-  const int32_t* q_start;
-  int32_t* q_rel;
-  void* k;
-  void* v;
-  int B, Hkv, hd, rows, max_blocks, n_blocks, block_shift;
-  int T, window, max_seq_len;  // prefill; window 0 on a full layer
-  float k_mul;                 // 2^k_exp
-};
-cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
-
-struct Kv4DecodeArgs {
-  const void* q;  // [B][H][hd] bf16
-  const uint8_t* data;
-  const int32_t* table;
-  const int32_t* lens;
-  void* out;
-  float* ws_o;        // [2 nctas][G][hd] partial outputs: two units of a CTA's share may continue in other CTAs'
-  float2* ws_ml;      // [2 nctas][8] their softmax references and denominators
-  unsigned* tickets;  // arrival counters (zero between calls), [4 levels of merges][2 kKv4MaxCtas]
-  int* err;
-  int B, H, Hkv, hd, max_blocks, n_blocks, block_shift;
-  int window;  // 0 on a full layer
-  int len_cap;
-  int nctas;
-  float scale_log2;  // attn_scale * log2(e) * 2^k_exp
-};
-// Workspace: the tickets, then ws_ml, then ws_o.  The tickets are in front and of
-// a fixed size, so calls of different shapes may take turns on one workspace.
-constexpr int kKv4MaxCtas = 1024;
-constexpr size_t kKv4TicketBytes = 4 * 2 * kKv4MaxCtas * 4;
-struct Kv4DecodePlan {
-  int nctas;
-  size_t ml_bytes, o_bytes, ws_bytes;
-};
-Kv4DecodePlan kv4_decode_plan(int window, int hd, int H, int Hkv, int B, int max_seq_len);
-cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 
 }  // namespace g4

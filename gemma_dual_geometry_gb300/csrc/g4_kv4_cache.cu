@@ -4,7 +4,7 @@
 #include <cooperative_groups.h>
 
 #include "g4_device.cuh"
-#include "g4_internal.h"
+#include "g4_kv4_internal.h"
 #include "g4_kv4.cuh"
 
 namespace g4 {

@@ -51,7 +51,7 @@
 #include <math.h>
 
 #include "g4_device.cuh"
-#include "g4_internal.h"
+#include "g4_kv4_internal.h"
 #include "g4_kv4.cuh"
 
 namespace g4 {
