@@ -692,10 +692,12 @@ g4_status kv4_check_table(const void* table, int max_blocks, int block_size) {
 }
 
 // The bf16 rows that a prefill's keys are laid out in: per sequence, and the bytes of K (as of V).
+// (T tokens from max_seq_len on at most, the padding of a padded batch; T + max_seq_len < 2^31.)
 int kv4_prefill_rows(const g4_layer_params* p, int T, int max_seq_len) {
-  if (p->layer_type != G4_SLIDING) return max_seq_len;
+  const int all = max_seq_len + T;
+  if (p->layer_type != G4_SLIDING) return all;
   const long long rows = static_cast<long long>(T) + p->window - 1;
-  return rows < max_seq_len ? static_cast<int>(rows) : max_seq_len;
+  return rows < all ? static_cast<int>(rows) : all;
 }
 size_t kv4_prefill_kv_bytes(const g4_layer_params* p, int B, int T, int max_seq_len) {
   return static_cast<size_t>(B) * p->n_kv_heads * kv4_prefill_rows(p, T, max_seq_len) * p->head_dim * 2;
@@ -905,7 +907,7 @@ g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* p
 }
 
 size_t g4_kv4_prefill_workspace_size(const g4_layer_params* params, int32_t B, int32_t T, int32_t max_seq_len) {
-  if (kv4_check_params(params) != G4_OK || B < 1 || T < 1 || max_seq_len < T) return 0;
+  if (kv4_check_params(params) != G4_OK || B < 1 || T < 1 || max_seq_len < T || max_seq_len > 0x7fffffff - T) return 0;
   return kv4_prefill_head_bytes(B) + 2 * kv4_prefill_kv_bytes(params, B, T, max_seq_len);
 }
 
@@ -927,7 +929,8 @@ g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* 
   if (st != G4_OK) return st;
   if (max_seq_len < 1 || max_seq_len > max_blocks * c->block_size)
     return fail(G4_ERR_CAPACITY, "max_seq_len %d outside [1, %d blocks of %d]", max_seq_len, max_blocks, c->block_size);
-  if (T > max_seq_len) return fail(G4_ERR_CAPACITY, "T %d exceeds max_seq_len %d", T, max_seq_len);
+  if (T > max_seq_len || max_seq_len > 0x7fffffff - T)
+    return fail(G4_ERR_CAPACITY, "T %d exceeds max_seq_len %d, or both together 2^31 - 1", T, max_seq_len);
   if (B == 0 || T == 0) return ok();
   const size_t head = kv4_prefill_head_bytes(B), kv = kv4_prefill_kv_bytes(params, B, T, max_seq_len);
   if (workspace_bytes < head + 2 * kv)

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
   long long first;
   int rows = a.rows;
   if (a.q_start != nullptr) {
-    const int q0 = min(max(a.q_start[b], 0), a.max_seq_len - a.T);
+    const int q0 = min(max(a.q_start[b], 0), a.max_seq_len);
     const int low = a.window > 0 ? max(0, q0 - a.window + 1) : 0;
     if (gi == 0 && kvh == 0 && p == 0 && lane == 0) a.q_rel[b] = q0 - low;
     first = low;

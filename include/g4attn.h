@@ -506,13 +506,14 @@ size_t g4_kv4_prefill_workspace_size(const g4_layer_params* params, int32_t B, i
  *                batch) makes the tokens from seq_lens[b] - q_start_pos[b] on
  *                padding: their rows are computed as if the positions past
  *                seq_lens[b] held zero keys and values.
- *   max_seq_len  bound on q_start_pos[b] + T, T .. max_blocks * block_size;
- *                q_start_pos is clamped into [0, max_seq_len - T]
+ *   max_seq_len  bound on seq_lens[b], T .. max_blocks * block_size.
+ *                q_start_pos is clamped into [0, max_seq_len]; the padding of
+ *                a sequence that ends near max_seq_len may lie past it
  *   workspace    16-byte aligned, no contents needed; not shared by calls
  *                that overlap
  * The keys that the T tokens see are laid out in the workspace as bf16 (a
- * sliding layer's T + window - 1, a full layer's max_seq_len per sequence) and
- * attention runs on the tensor cores as in g4_attn_prefill, whose limits on
+ * sliding layer's T + window - 1, a full layer's max_seq_len + T per sequence)
+ * and attention runs on the tensor cores as in g4_attn_prefill, whose limits on
  * launches in flight hold.
  */
 g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,

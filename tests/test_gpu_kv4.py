@@ -318,6 +318,36 @@ def test_prefill(geo, T, bs, k_exp):
     assert_within(f64(out), ref, mag, C_PREFILL, f"{geo} T {T}")
 
 
+@pytest.mark.parametrize("geo", GEOS)
+def test_prefill_padding_past_the_table(geo):
+    """A padded batch whose sequences end at, near and before the table's end: the new tokens keep their
+    positions, whatever of the padding would lie past the end."""
+    g = geo_of(geo)
+    hd, H, Hkv = g["head_dim"], g["n_heads"], g["n_kv_heads"]
+    T, cap = 150, 160
+    start = np.array([158, 160, 20, 0, 100])
+    fresh = np.array([2, 0, 140, 150, 1])
+    B, lens = 5, start + fresh
+    pool = Pool(g, B, cap, 32, seed=hd).fill(lens, 4).to_device()
+    q = bf16_normal((B, T, H, hd), 15)
+    p = params_of(g)
+    nb = G.g4_kv4_prefill_workspace_size(p, B, T, cap)
+    ws = torch.full((nb,), 255, dtype=torch.uint8, device=DEV)   # NaNs
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+    G.g4_kv4_attn_prefill(p, pool.pools, 0, q.to(DEV), pool.d_table, pool.per, i32(start), i32(lens), B, T, cap, out, ws,
+                          nb)
+    assert bool(torch.isfinite(out).all())
+    k, v = pool.rows(lens, cap)
+    for b in range(B):
+        n = fresh[b]
+        if n == 0:
+            continue
+        one = slice(b, b + 1)
+        pos = (start[b] + np.arange(n))[None]
+        ref, mag = attention_and_scale(f64(q)[one, :n], k[one], v[one], pos, lens[one], Hkv, g)
+        assert_within(f64(out)[one, :n], ref, mag, C_PREFILL, f"{geo} sequence {b}")
+
+
 # ---------------------------------------------------------------- as they are used
 
 def test_lifecycle_under_graphs():

@@ -124,6 +124,7 @@ def test_prefill_refusals():
     assert prefill(start=None) == G.G4_ERR_INVALID_ARG
     assert prefill(T=201) == G.G4_ERR_CAPACITY
     assert prefill(T=-1) == G.G4_ERR_INVALID_ARG
+    assert prefill(t=pools(block_size=128), width=1 << 23, most=1 << 30, T=1 << 30) == G.G4_ERR_CAPACITY
 
 
 def test_workspace_sizes():
@@ -133,7 +134,8 @@ def test_workspace_sizes():
     assert G.g4_kv4_decode_workspace_size(p, 0, 100) == 0
     # T + window - 1 rows of K and V per sequence and head, and the sequences' first rows
     assert G.g4_kv4_prefill_workspace_size(p, 3, 100, 5000) == 256 + 2 * 3 * 2 * 611 * 256 * 2
-    assert G.g4_kv4_prefill_workspace_size(p, 3, 100, 300) == 256 + 2 * 3 * 2 * 300 * 256 * 2
+    # but no more than max_seq_len and T positions of padding behind it
+    assert G.g4_kv4_prefill_workspace_size(p, 3, 100, 300) == 256 + 2 * 3 * 2 * 400 * 256 * 2
     assert G.g4_kv4_prefill_workspace_size(p, 3, 100, 99) == 0
     assert G.kv4_pool_bytes(10, 2, 64, 256) == 10 * 64 * 2 * 2 * (256 // 2 + 256 // 16)
 
