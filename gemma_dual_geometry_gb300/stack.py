@@ -14,6 +14,8 @@ Every step runs in the CUDA kernels; this module only allocates and calls.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import g4attn as G
@@ -136,6 +138,14 @@ class PagedAttnStack:
                               torch.empty(size, dtype=torch.uint8, device=self.device))
         return self._steps[T]
 
+    def _on(self, stream):
+        """What torch does within runs on ``stream`` (a stream, an address, or None: the current one)."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        return torch.cuda.stream(stream)
+
     def owns(self, l):
         return self.src[l] < 0
 
@@ -145,8 +155,9 @@ class PagedAttnStack:
     def assign(self, new_lens, T, stream=None):
         """Blocks for sequences that go to new_lens [B] positions with T new tokens at most (0 ends one).
         Sets ``lens`` (what was granted) and ``start``; the T tokens' positions and slots serve append()."""
-        positions, slots, _ = self._step(T)
-        self.start.copy_(self.lens)
+        with self._on(stream):
+            positions, slots, _ = self._step(T)
+            self.start.copy_(self.lens)
         G.g4_kv4_assign_blocks(self.B, T, self.block_size, self.n_blocks, self.max_blocks, self.lens, new_lens,
                                self.free_blocks, self.free_count, self.block_table, self.lens, self.free_count,
                                positions, slots, stream=stream)

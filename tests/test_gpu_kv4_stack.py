@@ -86,6 +86,26 @@ def test_paged_stack_lifecycle():
                 assert np.array_equal(f64(got[b]), ref)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_assign_on_a_stream_of_its_own(raw):
+    """All that assign() does comes after what its stream still has to do: here two assignments that wait on it."""
+    st = S.PagedAttnStack(CFG, max_len=160, n_blocks=26, block_size=32, device=DEV)
+    want = [i32(x) for x in ([9, 40, 0, 33, 2], [12, 45, 6, 33, 0])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    on = side.cuda_stream if raw else side
+    st.assign(want[0], 40, stream=on)
+    positions, slots = st.assign(want[1], 7, stream=on)
+    torch.cuda.synchronize()
+    assert torch.equal(st.start, want[0]) and torch.equal(st.lens, want[1])
+    t = torch.arange(7, device=DEV)
+    at = want[0][:, None] + t
+    assert torch.equal(positions, torch.where(at < want[1][:, None], at, -1).int())
+    assert torch.equal(slots >= 0, positions >= 0)
+
+
 def test_stored_rows_are_the_bf16_caches_quantised():
     """The same tokens through g4_kv_append_normrope and g4_kv4_append_normrope: equal q, and the pool stands
     for the bf16 cache's rows quantised, bit for bit."""
