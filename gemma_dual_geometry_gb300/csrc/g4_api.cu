@@ -872,6 +872,10 @@ g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* p
   const int window = params->layer_type == G4_SLIDING ? params->window : 0;
   const g4::Kv4DecodePlan plan =
       g4::kv4_decode_plan(window, params->head_dim, params->n_heads, params->n_kv_heads, B, max_seq_len);
+  // A CTA counts its share's records in 32 bits.
+  const long long span = window > 0 && window < max_seq_len ? window : max_seq_len;
+  if (static_cast<long long>(B) * params->n_kv_heads > 0x7fffff00LL / (span / 16 + 2) * plan.nctas)
+    return fail(G4_ERR_UNSUPPORTED, "%d sequences of %lld keys are more than a call can count", B, span);
   if (workspace_bytes < plan.ws_bytes)
     return fail(G4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
   if (plan.ws_bytes > 0 && (workspace == nullptr || !aligned16(workspace)))

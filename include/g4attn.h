@@ -482,7 +482,8 @@ size_t g4_kv4_decode_workspace_size(const g4_layer_params* params, int32_t B, in
  *   seq_lens     [B] keys per sequence including the new token (append it
  *                first), clamped into [0, max_seq_len].  A sequence of no
  *                keys gets an output of zeros.
- *   max_seq_len  1 .. max_blocks * block_size
+ *   max_seq_len  1 .. max_blocks * block_size; B * n_kv_heads * max_seq_len (or
+ *                the window) must stay below some 10^13 (G4_ERR_UNSUPPORTED)
  * q and out as g4_attn_decode.  The workspace is zero-filled once before its
  * first use; every call leaves it ready for the next, whatever that call's
  * layer, batch and lengths (size it for the largest).  Calls that overlap on

@@ -120,6 +120,13 @@ def test_attention_refusals(call):
     assert call(ws=FAKE + 8, **full) == G.G4_ERR_INVALID_ARG
 
 
+def test_decode_refuses_what_32_bits_cannot_count():
+    huge = dict(p=params(layer_type=G.G4_FULL), t=pools(layer_type=G.G4_FULL, block_size=128), width=1 << 23)
+    assert decode(B=1 << 16, most=1 << 30, **huge) == G.G4_ERR_UNSUPPORTED
+    assert decode(B=(1 << 31) - 1, most=1 << 20, **huge) == G.G4_ERR_UNSUPPORTED
+    assert decode(B=1 << 14, most=1 << 20, nb=16, **huge) == G.G4_ERR_WORKSPACE   # counted
+
+
 def test_prefill_refusals():
     assert prefill(start=None) == G.G4_ERR_INVALID_ARG
     assert prefill(T=201) == G.G4_ERR_CAPACITY
