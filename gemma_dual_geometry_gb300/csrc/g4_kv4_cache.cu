@@ -166,33 +166,48 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
   }
   __syncthreads();
 
-  // positions and slots, four neighbours of a row per thread where rows allow it
+  // positions and slots, four neighbours of a row (in at most two blocks) per
+  // thread where rows allow it
   const int nb = b1 - b0;
-  auto slot_at = [&](const int32_t* row, int pos, int& entry, int& id) {
-    if ((pos >> a.block_shift) != entry) {
-      entry = pos >> a.block_shift;
-      id = row[entry];
-    }
-    return id >= 0 && id < a.n_blocks ? (id << a.block_shift) + (pos & mask) : -1;
+  // What is added to a position of table entry e to get its slot, and what is or-ed to the sum (-1: an id outside the pool).
+  auto slot_base = [&](int id, int e, int& none) {
+    none = id >= 0 && id < a.n_blocks ? 0 : -1;
+    return static_cast<int>(static_cast<unsigned>(id - e) << a.block_shift);
   };
   if ((a.T & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0) {
     const unsigned quads = static_cast<unsigned>(a.T) / 4, n = static_cast<unsigned>(nb) * quads;
+    const unsigned dr = quads > 0 ? kAssignThreads / quads : 0, dt = kAssignThreads - dr * quads;
+    unsigned r = quads > 0 ? tid / quads : 0, t = tid - r * quads;  // row and quad of i
+    int4* const pos4 = reinterpret_cast<int4*>(a.positions) + static_cast<size_t>(b0) * quads;
+    int4* const slot4 = reinterpret_cast<int4*>(a.slots) + static_cast<size_t>(b0) * quads;
 #pragma unroll 2
     for (unsigned i = tid; i < n; i += kAssignThreads) {
-      const unsigned r = i / quads, t = (i - r * quads) * 4;
-      const int b = b0 + static_cast<int>(r), end = s_new[r];
-      const long long at = static_cast<long long>(s_old[r]) + t;
-      const int32_t* row = a.table + static_cast<size_t>(b) * a.max_blocks;
-      int p[4], q[4], entry = -1, id = -1;
+      const unsigned at = static_cast<unsigned>(s_old[r]) + 4 * t, end = static_cast<unsigned>(s_new[r]);  // (at < 2^32)
+      int p[4] = {-1, -1, -1, -1}, q[4] = {-1, -1, -1, -1};
+      if (at < end) {
+        const int32_t* row = a.table + static_cast<size_t>(b0 + static_cast<int>(r)) * a.max_blocks;
+        const int e = static_cast<int>(at >> a.block_shift);
+        const unsigned next = static_cast<unsigned>(e + 1) << a.block_shift;  // first position of the next block
+        int none0, none1, base0 = slot_base(row[e], e, none0), base1 = base0;
+        none1 = none0;
+        if (next < min(at + 4, end)) base1 = slot_base(row[e + 1], e + 1, none1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool in = at + k < end;
-        p[k] = in ? static_cast<int>(at) + k : -1;
-        q[k] = in ? slot_at(row, p[k], entry, id) : -1;
+        for (int k = 0; k < 4; ++k) {
+          const unsigned pos = at + k;
+          if (pos < end) {
+            p[k] = static_cast<int>(pos);
+            q[k] = (static_cast<int>(pos) + (pos < next ? base0 : base1)) | (pos < next ? none0 : none1);
+          }
+        }
       }
-      const size_t o = (static_cast<size_t>(b) * a.T + t) / 4;
-      reinterpret_cast<int4*>(a.positions)[o] = make_int4(p[0], p[1], p[2], p[3]);
-      reinterpret_cast<int4*>(a.slots)[o] = make_int4(q[0], q[1], q[2], q[3]);
+      pos4[i] = make_int4(p[0], p[1], p[2], p[3]);
+      slot4[i] = make_int4(q[0], q[1], q[2], q[3]);
+      r += dr;
+      t += dt;
+      if (t >= quads) {
+        t -= quads;
+        ++r;
+      }
     }
   } else if (a.T > 0) {
     const unsigned T = static_cast<unsigned>(a.T), n = static_cast<unsigned>(nb) * T;
@@ -200,11 +215,17 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
       const unsigned r = i / T, t = i - r * T;
       const int b = b0 + static_cast<int>(r);
       const long long at = static_cast<long long>(s_old[r]) + t;
-      int entry = -1, id = -1;
       const bool in = at < s_new[r];
       const size_t o = static_cast<size_t>(b) * a.T + t;
+      int slot = -1;
+      if (in) {
+        const int e = static_cast<int>(at >> a.block_shift);
+        int none;
+        slot = slot_base(a.table[static_cast<size_t>(b) * a.max_blocks + e], e, none);
+        slot = (slot + static_cast<int>(at)) | none;
+      }
       a.positions[o] = in ? static_cast<int>(at) : -1;
-      a.slots[o] = in ? slot_at(a.table + static_cast<size_t>(b) * a.max_blocks, static_cast<int>(at), entry, id) : -1;
+      a.slots[o] = slot;
     }
   }
 }
@@ -315,10 +336,27 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
-  // Positions and slots are what grows: a CTA per 4096 of them, up to the portable cluster size.
+  // Positions and slots are what grows: a CTA per 4096 of them, up to 16 (the
+  // largest cluster, where one of them fits the device; 8 are always allowed).
+  static const unsigned most = [] {
+    if (cudaFuncSetAttribute(kv4_assign_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 8u;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kAssignThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool fits = cudaOccupancyMaxActiveClusters(&n, kv4_assign_kernel, &cfg) == cudaSuccess && n > 0;
+    (void)cudaGetLastError();
+    return fits ? 16u : 8u;
+  }();
   const long long work = static_cast<long long>(a.B) * a.T;
   unsigned n = 1;
-  while (n < 8 && n < static_cast<unsigned>(a.B) && work > 4096LL * n) n *= 2;
+  while (n < most && n < static_cast<unsigned>(a.B) && work > 4096LL * n) n *= 2;
   const size_t per = (static_cast<size_t>(a.B) + n - 1) / n;
   const size_t smem = (2 * static_cast<size_t>(a.B) + 2 * per) * 4;
   const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 16);
