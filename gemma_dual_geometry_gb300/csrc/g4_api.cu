@@ -944,6 +944,10 @@ g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* 
   int* err = device_error_ptr();
   if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Two launches: a key is read by every query tile of every head of its group, so
+  // it is widened once, into the rows that the tensor-core prefill loads by TMA.  The
+  // gather is 14 us of 203 at 2 x 2048 tokens of 8 heads of 512 (full layer), 4 of 20
+  // at 4 x 256 tokens of a sliding layer.
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   g4::Kv4GatherArgs ga;
   memset(&ga, 0, sizeof(ga));

@@ -28,7 +28,11 @@
 //
 // The 4-bit cache's append (KV4) differs in where rows go: a row is finished in
 // shared memory, then a q row is copied out and a k or v row quantised by
-// kv4_store_row.
+// kv4_store_row; all tokens' cos/sin tables are built at once.  Bound by
+// instruction issue (2.7 per cycle): 8 sequences x 2048 tokens of 8 + 2 + 2 rows
+// of 512 take 155 us where the sequences' positions differ, 138 where they agree (the bf16
+// append: 179 and 114), 59 us of which are bytes; with the stores left out 2 %
+// less.
 //
 // Lane l of a warp owns elements [l*E, l*E + E) of the lower half and the
 // same offsets of the upper half (E = head_dim / 64), so each rotate_half

@@ -21,9 +21,9 @@
 //
 // Work.  The records of all (sequence, kv head) units, laid end to end, are
 // dealt out in equal contiguous shares to as many CTAs as are resident, so
-// ragged lengths leave no SM idle.  Where shares are short (a few steps: windows,
-// short sequences) they are cut anew at every unit instead, so that no CTA pays
-// for the start of a second one.  A unit inside one share is written directly;
+// ragged lengths leave no SM idle.  Where that makes no share much longer, they are
+// cut anew at every unit instead, so that no CTA pays for the start of a second
+// one.  A unit inside one share is written directly;
 // the CTAs of a unit that spans shares leave partials in the workspace and the one
 // that takes the last ticket merges them.
 //
@@ -48,6 +48,17 @@
 // only moves (rescaling O) when a score exceeds it by 2^kSlack, so most steps
 // need no reduction over positions.  Probabilities are formed as
 // 2^(s - m + kShift): fp16's 11 bits then reach down to 2^-18 of the reference.
+//
+// Measured (device time, calls back to back; copy rate: 6.78 TB/s):
+//   head_dim 512, 8 heads, 2 kv heads, 4 sequences of 131072 keys (604 MB) 110.7 us,
+//     5.5 TB/s, 0.80 of a copy; every product left out: 101 us, so the copies in
+//     flight (3 CTAs of 3 x 18 KB per SM) bound it;
+//   the same, 64 sequences of 1024 to 8192 keys (340 MB) 70.5 us, 0.71 of a copy:
+//     the start (lengths, block ids, first copies) and the merges take 8 us;
+//   head_dim 256, window 512, 64 sequences (19 MB) 13.2 us; head_dim 128, one of 333
+//     keys 6.6 us: latency of that chain (the bytes take 2.9 and 0.01 us).
+//   head_dim 256, 64 sequences of 1024 to 8192 keys, 8 heads per kv head 52.6 us, 4
+//     heads 46.1 us.
 #include <math.h>
 
 #include "g4_device.cuh"
@@ -58,11 +69,18 @@ namespace g4 {
 namespace {
 
 constexpr int kHeads = 8;  // columns of the tensor-core product
-constexpr float kSlack = 3.0f;
+constexpr float kSlack = 3.0f;  // (0, a reference that follows every maximum: 0.6 % slower at 4 x 131072 keys)
 constexpr float kShift = 4.0f;  // (2^(kSlack + kShift) times the largest scale, 448, stays within fp16)
 constexpr float kNoKey = -3e38f;  // reference of a state that has seen no key (finite: no inf - inf)
-constexpr int kFan = 8;        // partials merged at once
-constexpr int kCutSteps = 4;   // longest shares, in steps, that are cut at units
+// Partials merged at once.  6: 113.6 us at 4 x 131072 keys against 110.6 (more
+// levels); 16: 113.8, and 15.4 against 13.2 at 64 windows (more loads than registers).
+constexpr int kFan = 8;
+// Shares are cut at units where that makes the longest at most so many steps longer.
+// Never: 15.6 us against 13.3 at 64 windows of 512 (head_dim 256), 30.2 against 26.4
+// at 256 of them, 23.4 against 15.8 at 16 sequences of 100 to 2000 keys (head_dim 512),
+// 48.8 against 45.6 at 32 of 1000 to 8000.  2 to 6 steps: the same; 8: 82 against 70.5
+// at 64 sequences of 1024 to 8192 keys.
+constexpr int kCutSteps = 4;
 
 // Shape of the kernel at one head_dim (also used by the plan).
 template <int HD>
@@ -74,8 +92,11 @@ struct Kv4Cfg {
   static constexpr int STEP = W * RW;                           // records per step
   static constexpr int PW = NP >= W ? NP / W : 1;               // pieces of O per warp
   static constexpr int KS = NP >= W ? 1 : W / NP;               // warps that share a piece
-  static constexpr int MINB = HD >= 512 ? 3 : 4;                // CTAs per SM
-  static constexpr int SLOTS = HD >= 512 ? 3 : 4;               // what MINB leaves room for
+  // CTAs per SM, and the buffers that this leaves room for.  At 512: 2 CTAs of 5
+  // buffers the same within 1 %, 3 of 2 10 % slower.  At 256 (64 windows): 3 CTAs of
+  // 6 buffers 14.1 us, 5 of 4 14.0, 4 of 4 13.2.
+  static constexpr int MINB = HD >= 512 ? 3 : 4;
+  static constexpr int SLOTS = HD >= 512 ? 3 : 4;
   static constexpr int HALF_B = 9 * HD;                         // K (or V) part of a record
   static constexpr int SLOT_B = STEP * HALF_B;
   static constexpr int Q_OFF = SLOTS * SLOT_B;                  // q fragments, fp16 (8 columns)
@@ -253,9 +274,11 @@ __global__ void __launch_bounds__(Kv4Cfg<HD>::NT, Kv4Cfg<HD>::MINB)
     total *= a.Hkv;
     share = steps_up((total + nctas - 1) / nctas);
     // Cut at every unit: parts of `cut` records (the last of a unit fewer), which
-    // are at most total / cut + units.
-    const long long cut = nctas > units ? steps_up((total + nctas - units - 1) / (nctas - units)) : 0;
-    cut_units = cut > 0 && cut <= kCutSteps * STEP;
+    // are at most total / cut + units; or as many as units, where no unit is longer.
+    const int span = a.window > 0 && a.window < a.len_cap ? a.window : a.len_cap;
+    const long long longest = steps_up((span + 15) / 16 + 1);
+    const long long cut = nctas > units ? min(longest, steps_up((total + nctas - units - 1) / (nctas - units))) : 0;
+    cut_units = cut > 0 && cut <= share + kCutSteps * STEP;
     Kv4Place p;  // where the share begins, set by the thread that finds it there
     p.left = 0;
     auto set = [&](int b, const Kv4Seq& seq, long long kvh, long long off, long long left) {
@@ -856,6 +879,8 @@ cudaError_t launch_hg(const Kv4DecodeArgs& a, cudaStream_t s) {
 
 template <int HD>
 cudaError_t launch_h(const Kv4DecodeArgs& a, cudaStream_t s) {
+  // Up to 4 heads: two scale blocks per product (133 us against 152 with one at head_dim
+  // 512, 4 x 131072 keys, before the copies had a warp of their own).
   if (a.H <= 4 * a.Hkv) return launch_hg<HD, 4>(a, s);
   if constexpr (HD <= 256) return launch_hg<HD, 8>(a, s);
   return cudaErrorInvalidValue;

@@ -545,6 +545,22 @@ def test_decode_right_behind_the_kernel_that_sets_the_lengths():
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("hd,B", [(512, 200), (256, 290), (256, 150), (64, 200)])
+def test_decode_one_long_among_many_short(hd, B):
+    """Shares that are not cut at units, with a unit spread over many of them (512, 290 of 256); the others are cut."""
+    g = geometry(W.FULL, hd, H=2, Hkv=2)
+    lens = np.random.default_rng(B).integers(60, 112, B)
+    lens[B // 3] = 4000
+    pool = Pool(g, B, 4000, 128, seed=9).fill(lens, 10).to_device()
+    q = bf16_normal((B, 2, hd), 11)
+    out = f64(decode_gpu(g, pool, q, lens))
+    for b in [*range(0, B, 9), B // 3 - 1, B // 3, B // 3 + 1, B - 1]:
+        heads = [K.read_rows(pool.data, pool.table[b], h, range(lens[b]), 128) for h in (0, 1)]
+        kk, vv = (np.stack([h[i] for h in heads])[None] for i in (0, 1))
+        ref, mag = attention_and_scale(f64(q)[b:b + 1, None], kk, vv, lens[b:b + 1, None] - 1, lens[b:b + 1], 2, g)
+        assert_within(out[b:b + 1], ref[:, 0], mag[:, 0], C_DECODE, f"sequence {b}", keys=lens[b])
+
+
 @pytest.mark.parametrize("B,window", [(300, 0), (700, 20)])
 def test_decode_many_sequences(B, window):
     """More sequences than a CTA has threads."""
