@@ -49,7 +49,8 @@ cudaError_t launch_pdl(void (*kern)(Args), dim3 grid, unsigned block, size_t sme
 // one cluster barrier between them; with many new tokens also by the
 // instructions that form positions and slots.  Measured: 64 sequences of a token
 // each 4.2 us (the host's call takes 5.4); 96 sequences of up to 2048 tokens (1.6 MB
-// of positions and slots) 6.6 us with a cluster of 16, 8.5 with 8, 12.6 with 4.
+// of positions and slots) 6.4 us with a cluster of 16, 8.5 with 8, 12.6 with 4; rows of
+// 2047 tokens, which are not written four at a time, 7.3.
 
 // (512: 12.0 us against 9.3 in that case, when the largest cluster had 8 CTAs.)
 constexpr int kAssignThreads = 1024;
@@ -215,21 +216,29 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
     }
   } else if (a.T > 0) {
     const unsigned T = static_cast<unsigned>(a.T), n = static_cast<unsigned>(nb) * T;
+    const unsigned dr = kAssignThreads / T, dt = kAssignThreads - dr * T;
+    unsigned r = tid / T, t = tid - r * T;
+    int32_t* const pos1 = a.positions + static_cast<size_t>(b0) * T;
+    int32_t* const slot1 = a.slots + static_cast<size_t>(b0) * T;
+#pragma unroll 4
     for (unsigned i = tid; i < n; i += kAssignThreads) {
-      const unsigned r = i / T, t = i - r * T;
-      const int b = b0 + static_cast<int>(r);
-      const long long at = static_cast<long long>(s_old[r]) + t;
-      const bool in = at < s_new[r];
-      const size_t o = static_cast<size_t>(b) * a.T + t;
-      int slot = -1;
-      if (in) {
+      const unsigned at = static_cast<unsigned>(s_old[r]) + t;
+      int pos = -1, slot = -1;
+      if (at < static_cast<unsigned>(s_new[r])) {
         const int e = static_cast<int>(at >> a.block_shift);
         int none;
-        slot = slot_base(a.table[static_cast<size_t>(b) * a.max_blocks + e], e, none);
-        slot = (slot + static_cast<int>(at)) | none;
+        slot = slot_base(a.table[static_cast<size_t>(b0 + static_cast<int>(r)) * a.max_blocks + e], e, none);
+        pos = static_cast<int>(at);
+        slot = (slot + pos) | none;
       }
-      a.positions[o] = in ? static_cast<int>(at) : -1;
-      a.slots[o] = slot;
+      pos1[i] = pos;
+      slot1[i] = slot;
+      r += dr;
+      t += dt;
+      if (t >= T) {
+        t -= T;
+        ++r;
+      }
     }
   }
 }
@@ -344,9 +353,10 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
-  // Positions and slots are what grows: a CTA per 4096 of them (2048 or 8192:
-  // the same within 1 %), up to 16 (the largest cluster, where one of them fits the
-  // device; 8 are always allowed).
+  // A CTA per 4096 positions (2048 or 8192: the same within 1 %) or 64 sequences
+  // (1000 that gain a token or end: 5.1 us against 11.3 with one CTA, 6.6 with one per
+  // 256; one per 32 makes 64 of them 4.5 against 4.2), up to 16 (the largest cluster,
+  // where one of them fits the device; 8 are always allowed).
   static const unsigned most = [] {
     if (cudaFuncSetAttribute(kv4_assign_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 8u;
     cudaLaunchConfig_t cfg = {};
@@ -365,7 +375,7 @@ cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
   }();
   const long long work = static_cast<long long>(a.B) * a.T;
   unsigned n = 1;
-  while (n < most && n < static_cast<unsigned>(a.B) && work > 4096LL * n) n *= 2;
+  while (n < most && n < static_cast<unsigned>(a.B) && (work > 4096LL * n || a.B > 64 * static_cast<int>(n))) n *= 2;
   const size_t per = (static_cast<size_t>(a.B) + n - 1) / n;
   const size_t smem = (2 * static_cast<size_t>(a.B) + 2 * per) * 4;
   const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 16);
