@@ -515,7 +515,9 @@ size_t g4_kv4_prefill_workspace_size(const g4_layer_params* params, int32_t B, i
  * The keys that the T tokens see are laid out in the workspace as bf16 (a
  * sliding layer's T + window - 1, a full layer's max_seq_len + T per sequence)
  * and attention runs on the tensor cores as in g4_attn_prefill, whose limits on
- * launches in flight hold.
+ * launches in flight hold.  As there, a masked key has the weight zero, and zero
+ * times NaN is NaN: a NaN or an infinity held at a position may reach every query
+ * of the tiles (128 queries, 128 keys) that contain it.
  */
 g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
                               int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,
