@@ -254,19 +254,24 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
 // take 24 at the rate of a copy (a part of them stays in L2); one of 700 rows 2.9
 // us.  (A warp for a whole record, its pieces one after another: 34.8 and 4.0 us.)
 
+// Most CTAs of a launch, which take turns beyond that.  A prefill's rows are
+// bounded on the host and counted on the device: 4 sequences of 2000 keys and 256
+// new tokens (head_dim 512) under a bound of 131072 take 63.5 us against 119.6 with
+// a CTA for every 16 rows of the bound, 61 under one of 4096.  9728 CTAs: 66.2; 2736:
+// 62.0, but 8 sequences of 4096 rows 28.3 us against 26.9.
+constexpr int kGatherCtas = 4864;
+
 template <int HD>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__ Kv4GatherArgs a) {
   using R = Kv4Rec<HD>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int ngroups = a.rows / kKv4Group + 2;  // that rows positions can touch
   const int p = (threadIdx.x >> 5) % R::NP;
-  const long long item = static_cast<long long>(blockIdx.x) * (8 / R::NP) + (threadIdx.x >> 5) / R::NP;
-  const long long unit = item / ngroups;
+  const int unit = blockIdx.x / a.per_unit;
+  constexpr int kPerCta = 8 / R::NP;  // records
   pdl_wait();
   pdl_trigger();
-  if (unit >= static_cast<long long>(a.B) * a.Hkv) return;
-  const int gi = static_cast<int>(item - unit * ngroups);
-  const int b = static_cast<int>(unit / a.Hkv), kvh = static_cast<int>(unit % a.Hkv);
+  const int b = unit / a.Hkv, kvh = unit % a.Hkv;
+  int gi = blockIdx.x % a.per_unit * kPerCta + (threadIdx.x >> 5) / R::NP;
 
   long long first;
   int rows = a.rows;
@@ -279,72 +284,76 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
   } else {
     first = a.start[b];
   }
-  // group numbers round towards minus infinity, so a group never straddles position 0
-  const long long pos0 = ((first >> 4) + gi) << 4;
-  if (pos0 >= first + rows) return;
   const int len = a.lens[b];
-  const int entry = pos0 >= 0 ? static_cast<int>(pos0 >> a.block_shift) : -1;
-  int block = -1;
-  if (pos0 >= 0 && pos0 < len && entry < a.max_blocks) block = a.table[static_cast<size_t>(b) * a.max_blocks + entry];
-  const bool there = block >= 0 && block < a.n_blocks;
-  const int in_block = static_cast<int>(pos0 & ((1 << a.block_shift) - 1));
-  const uint8_t* rec = there ? a.data + kv4_record<HD>(block, kvh, in_block >> 4, a.Hkv, a.block_shift) : nullptr;
   __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(a.k) + static_cast<size_t>(unit) * a.rows * HD;
   __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(a.v) + static_cast<size_t>(unit) * a.rows * HD;
 
-  // Of the record's 16 positions: the row of the first, and how many are held.
-  const int row0 = static_cast<int>(pos0 - first);
-  const int nheld = there ? static_cast<int>(min(16LL, len - pos0)) : 0;
+#pragma unroll 1
+  for (;; gi += a.per_unit * kPerCta) {
+    // group numbers round towards minus infinity, so a group never straddles position 0
+    const long long pos0 = ((first >> 4) + gi) << 4;
+    if (pos0 >= first + rows) return;
+    const int entry = pos0 >= 0 ? static_cast<int>(pos0 >> a.block_shift) : -1;
+    int block = -1;
+    if (pos0 >= 0 && pos0 < len && entry < a.max_blocks) block = a.table[static_cast<size_t>(b) * a.max_blocks + entry];
+    const bool there = block >= 0 && block < a.n_blocks;
+    const int in_block = static_cast<int>(pos0 & ((1 << a.block_shift) - 1));
+    const uint8_t* rec = there ? a.data + kv4_record<HD>(block, kvh, in_block >> 4, a.Hkv, a.block_shift) : nullptr;
 
-  // fp16x2 code times scale, then the exponent, as bf16x2
-  auto value = [](uint32_t codes, __half2 s, float mul) -> uint32_t {
-    const float2 v = __half22float2(__hmul2(as_half2(codes), s));
-    return pack_bf16x2(v.x * mul, v.y * mul);
-  };
-  uint4 kc = make_uint4(0, 0, 0, 0), vc = kc, vs = kc;
-  uint2 ks = make_uint2(0, 0);
-  if (there) {
-    kc = *reinterpret_cast<const uint4*>(rec + R::KC + p * 512 + lane * 16);
-    ks = *reinterpret_cast<const uint2*>(rec + R::KS + p * 64 + g * 8);
-    vc = *reinterpret_cast<const uint4*>(rec + R::VC + p * 512 + lane * 16);
-    vs = *reinterpret_cast<const uint4*>(rec + R::VS + p * 64 + t * 16);
-  }
-  const uint32_t kw[2][2] = {{kc.x, kc.y}, {kc.z, kc.w}};
-  const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
-  const uint32_t vsw[4] = {vs.x, vs.y, vs.z, vs.w};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const __half2 s = as_half2(w & 1 ? e4m3x2_hi_f16x2(w < 2 ? ks.x : ks.y) : e4m3x2_f16x2(w < 2 ? ks.x : ks.y));
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int m = 8 * r + g;
-      if (static_cast<unsigned>(row0 + m) < static_cast<unsigned>(rows)) {
-        const __half2 sr = r == 0 ? __low2half2(s) : __high2half2(s);
-        uint2 o = make_uint2(0, 0);
-        if (m < nheld) {
-          const uint32_t word = kw[r][w >> 1];
-          o.x = value(w & 1 ? e2m1x2_f16x2<2>(word) : e2m1x2_f16x2<0>(word), sr, a.k_mul);
-          o.y = value(w & 1 ? e2m1x2_f16x2<3>(word) : e2m1x2_f16x2<1>(word), sr, a.k_mul);
-        }
-        *reinterpret_cast<uint2*>(ko + static_cast<size_t>(row0 + m) * HD + p * 64 + w * 16 + t * 4) = o;
-      }
+    // Of the record's 16 positions: the row of the first, and how many are held.
+    const int row0 = static_cast<int>(pos0 - first);
+    const int nheld = there ? static_cast<int>(min(16LL, len - pos0)) : 0;
+
+    // fp16x2 code times scale, then the exponent, as bf16x2
+    auto value = [](uint32_t codes, __half2 s, float mul) -> uint32_t {
+      const float2 v = __half22float2(__hmul2(as_half2(codes), s));
+      return pack_bf16x2(v.x * mul, v.y * mul);
+    };
+    uint4 kc = make_uint4(0, 0, 0, 0), vc = kc, vs = kc;
+    uint2 ks = make_uint2(0, 0);
+    if (there) {
+      kc = *reinterpret_cast<const uint4*>(rec + R::KC + p * 512 + lane * 16);
+      ks = *reinterpret_cast<const uint2*>(rec + R::KS + p * 64 + g * 8);
+      vc = *reinterpret_cast<const uint4*>(rec + R::VC + p * 512 + lane * 16);
+      vs = *reinterpret_cast<const uint4*>(rec + R::VS + p * 64 + t * 16);
     }
-    const __half2 s01 = as_half2(e4m3x2_f16x2(vsw[w])), s23 = as_half2(e4m3x2_hi_f16x2(vsw[w]));
+    const uint32_t kw[2][2] = {{kc.x, kc.y}, {kc.z, kc.w}};
+    const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
+    const uint32_t vsw[4] = {vs.x, vs.y, vs.z, vs.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = 8 * (i >> 1) + 2 * t + (i & 1);
-      if (static_cast<unsigned>(row0 + m) < static_cast<unsigned>(rows)) {
-        const __half2 sp = i < 2 ? s01 : s23;
-        const __half2 si = i & 1 ? __high2half2(sp) : __low2half2(sp);
-        uint32_t codes;
-        switch (w) {
-          case 0: codes = e2m1x2_f16x2<0>(vw[i]); break;
-          case 1: codes = e2m1x2_f16x2<1>(vw[i]); break;
-          case 2: codes = e2m1x2_f16x2<2>(vw[i]); break;
-          default: codes = e2m1x2_f16x2<3>(vw[i]); break;
+    for (int w = 0; w < 4; ++w) {
+      const __half2 s = as_half2(w & 1 ? e4m3x2_hi_f16x2(w < 2 ? ks.x : ks.y) : e4m3x2_f16x2(w < 2 ? ks.x : ks.y));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int m = 8 * r + g;
+        if (static_cast<unsigned>(row0 + m) < static_cast<unsigned>(rows)) {
+          const __half2 sr = r == 0 ? __low2half2(s) : __high2half2(s);
+          uint2 o = make_uint2(0, 0);
+          if (m < nheld) {
+            const uint32_t word = kw[r][w >> 1];
+            o.x = value(w & 1 ? e2m1x2_f16x2<2>(word) : e2m1x2_f16x2<0>(word), sr, a.k_mul);
+            o.y = value(w & 1 ? e2m1x2_f16x2<3>(word) : e2m1x2_f16x2<1>(word), sr, a.k_mul);
+          }
+          *reinterpret_cast<uint2*>(ko + static_cast<size_t>(row0 + m) * HD + p * 64 + w * 16 + t * 4) = o;
         }
-        *reinterpret_cast<uint32_t*>(vo + static_cast<size_t>(row0 + m) * HD + p * 64 + w * 16 + g * 2) =
-            m < nheld ? value(codes, si, 1.0f) : 0u;
+      }
+      const __half2 s01 = as_half2(e4m3x2_f16x2(vsw[w])), s23 = as_half2(e4m3x2_hi_f16x2(vsw[w]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = 8 * (i >> 1) + 2 * t + (i & 1);
+        if (static_cast<unsigned>(row0 + m) < static_cast<unsigned>(rows)) {
+          const __half2 sp = i < 2 ? s01 : s23;
+          const __half2 si = i & 1 ? __high2half2(sp) : __low2half2(sp);
+          uint32_t codes;
+          switch (w) {
+            case 0: codes = e2m1x2_f16x2<0>(vw[i]); break;
+            case 1: codes = e2m1x2_f16x2<1>(vw[i]); break;
+            case 2: codes = e2m1x2_f16x2<2>(vw[i]); break;
+            default: codes = e2m1x2_f16x2<3>(vw[i]); break;
+          }
+          *reinterpret_cast<uint32_t*>(vo + static_cast<size_t>(row0 + m) * HD + p * 64 + w * 16 + g * 2) =
+              m < nheld ? value(codes, si, 1.0f) : 0u;
+        }
       }
     }
   }
@@ -383,12 +392,15 @@ cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
   return launch_pdl(kv4_assign_kernel, dim3(n), kAssignThreads, smem, n, s, a);
 }
 
-cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s) {
-  const long long items = static_cast<long long>(a.B) * a.Hkv * (a.rows / kKv4Group + 2);
-  const int per = 8 * 64 / a.hd;  // records per CTA of 8 warps
-  const long long ctas = (items + per - 1) / per;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(ctas));
+cudaError_t launch_kv4_gather(const Kv4GatherArgs& args, cudaStream_t s) {
+  const long long units = static_cast<long long>(args.B) * args.Hkv;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int per = 8 * 64 / args.hd;                            // records per CTA of 8 warps
+  const int need = (args.rows / kKv4Group + 2 + per - 1) / per;  // CTAs for the groups that rows positions can touch
+  const long long room = kGatherCtas / units;
+  Kv4GatherArgs a = args;
+  a.per_unit = need < room ? need : room > 0 ? static_cast<int>(room) : 1;
+  const dim3 grid(static_cast<unsigned>(units * a.per_unit));
   switch (a.hd) {
     case 64: return launch_pdl(kv4_gather_kernel<64>, grid, 256, 0, 1, s, a);
     case 128: return launch_pdl(kv4_gather_kernel<128>, grid, 256, 0, 1, s, a);

@@ -48,6 +48,7 @@ struct Kv4GatherArgs {
   int B, Hkv, hd, rows, max_blocks, n_blocks, block_shift;
   int T, window, max_seq_len;  // prefill; window 0 on a full layer
   float k_mul;                 // 2^k_exp
+  int per_unit;                // CTAs per sequence and kv head (set by the launch)
 };
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
 

@@ -56,7 +56,8 @@ def quantise(x, k_exp=0):
 def values(code, scale, k_exp=0):
     """The numbers that codes and scale bytes stand for."""
     v = GRID[code & 7] * np.where(code >> 3, -1.0, 1.0)
-    s = np.where(scale == NAN_SCALE, np.nan, E4M3[np.minimum(scale & 127, 126)]) * np.where(scale >> 7, -1.0, 1.0)
+    s = np.where(scale & 127 == NAN_SCALE, np.nan,  # (e4m3's 255 is a NaN too, though no quantiser writes it)
+                 E4M3[np.minimum(scale & 127, 126)]) * np.where(scale >> 7, -1.0, 1.0)
     out = v.reshape(v.shape[:-1] + (-1, 16)) * s[..., None] * 2.0 ** k_exp
     return out.reshape(v.shape)
 

@@ -348,6 +348,50 @@ def test_prefill_padding_past_the_table(geo):
         assert_within(f64(out)[one, :n], ref, mag, C_PREFILL, f"{geo} sequence {b}")
 
 
+@pytest.mark.parametrize("hd,H,window", [(512, 4, 0), (64, 2, 0), (256, 8, 9000)])
+def test_prefill_under_a_wide_bound(hd, H, window):
+    """The same result whatever the bound on the lengths, far above them too (and the gather's CTAs take turns)."""
+    g = geometry(W.SLIDING if window else W.FULL, hd, H=H, Hkv=2, window=window)
+    T, B, bs = 33, 4, 128
+    start = np.array([300, 0, 77, 512])
+    lens = start + T
+    pool = Pool(g, B, 640, bs, seed=hd).fill(lens, 4).to_device()
+    p, q = params_of(g), bf16_normal((B, T, H, hd), 15).to(DEV)
+    outs = []
+    for width in (pool.per, 300):
+        table = torch.full((B, width), 1 << 30, dtype=torch.int32, device=DEV)
+        table[:, :pool.per] = pool.d_table
+        most = width * bs
+        nb = G.g4_kv4_prefill_workspace_size(p, B, T, most)
+        ws = torch.full((nb,), 255, dtype=torch.uint8, device=DEV)
+        outs.append(torch.empty_like(q))
+        G.g4_kv4_attn_prefill(p, pool.pools, 0, q, table, width, i32(start), i32(lens), B, T, most, outs[-1], ws, nb)
+    assert torch.equal(*outs)
+    k, v = pool.rows(lens, 640)
+    ref, mag = attention_and_scale(f64(q), k, v, start[:, None] + np.arange(T), lens, 2, g)
+    assert_within(f64(outs[1]), ref, mag, C_PREFILL)
+
+
+def test_gather_of_many_rows():
+    """More rows than a launch has CTAs for, from before a sequence's first position to behind its last."""
+    g = geometry(W.FULL, 512, H=2, Hkv=2)
+    lens, start, rows = np.array([14000, 13990, 3000]), np.array([-5, 100, 7]), 14001
+    pool = Pool(g, 3, 14000, 64, seed=5).to_device()   # random bytes
+    k, v = (torch.empty((3, 2, rows, 512), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    G.g4_kv4_gather(params_of(g), pool.pools, 0, pool.d_table, pool.per, i32(start), i32(lens), 3, rows, k, v)
+    for b in range(3):
+        outside = np.ones(rows, bool)
+        outside[max(0, -start[b]):lens[b] - start[b]] = False
+        for x in (k, v):
+            assert not x[b][:, torch.from_numpy(outside).to(DEV)].any()
+        some = np.unique(np.concatenate([np.arange(0, lens[b], 211), np.arange(max(0, start[b]), max(0, start[b]) + 20),
+                                         np.arange(lens[b] - 20, lens[b])]))
+        some = some[(some >= start[b]) & (some < start[b] + rows)]
+        for h in range(2):
+            for got, want in zip((k, v), K.read_rows(pool.data, pool.table[b], h, some, 64)):
+                assert np.array_equal(f64(got[b, h, torch.from_numpy(some - start[b]).to(DEV)]), want, equal_nan=True)
+
+
 # ---------------------------------------------------------------- as they are used
 
 def test_lifecycle_under_graphs():
