@@ -45,6 +45,11 @@ cudaError_t launch_pdl(void (*kern)(Args), dim3 grid, unsigned block, size_t sme
 // returned blocks, waits for the cluster (blocks given back may be taken in the
 // same call), pops, and writes lengths, positions and slots.  Pushes and pops are
 // dealt out one block per thread, its sequence found in the sums by bisection.
+// The sums take every entry given back for a block.  Where one is no block of the
+// pool (a caller may have taken it away), the threads that meet such entries tell
+// all CTAs how many, and after the barrier the pushes are made again without
+// them, behind another barrier; where there are none this costs nothing but a
+// reduction over the warp.
 //   Bound by latency: lengths, free list and table are dependent reads, with
 // one cluster barrier between them; with many new tokens also by the
 // instructions that form positions and slots.  Measured: 64 sequences of a token
@@ -54,6 +59,7 @@ cudaError_t launch_pdl(void (*kern)(Args), dim3 grid, unsigned block, size_t sme
 
 // (512: 12.0 us against 9.3 in that case, when the largest cluster had 8 CTAs.)
 constexpr int kAssignThreads = 1024;
+constexpr int kAssignMaxCtas = 16;
 
 // The first i in [lo, hi) with v[i] > x (hi if there is none); v ascends.
 __device__ __forceinline__ int first_above(const int* v, int lo, int hi, int x) {
@@ -70,6 +76,7 @@ __device__ __forceinline__ int first_above(const int* v, int lo, int hi, int x) 
 __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid_constant__ Kv4AssignArgs a) {
   extern __shared__ int s_mem[];
   __shared__ unsigned long long s_warp[kAssignThreads / 32];
+  __shared__ int s_gone[kAssignMaxCtas];  // entries without a block among those that CTA r gives back
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = kAssignThreads / 32;
@@ -85,6 +92,8 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
   const int mask = (1 << a.block_shift) - 1;
   auto blocks_of = [&](int len) { return (len >> a.block_shift) + ((len & mask) != 0); };
 
+  if (tid < kAssignMaxCtas) s_gone[tid] = 0;
+  if (nctas > 1) cluster.barrier_arrive();  // (others may add to s_gone past the wait below)
   pdl_wait();
   pdl_trigger();
   const int count = min(max(__ldcg(a.free_count), 0), a.n_blocks);
@@ -127,24 +136,66 @@ __global__ void __launch_bounds__(kAssignThreads) kv4_assign_kernel(const __grid
     __syncthreads();
   }
   const int back = static_cast<int>(carry >> 32);
-  const int there = static_cast<int>(min(static_cast<long long>(count) + back, static_cast<long long>(a.n_blocks)));
+  if (nctas > 1) cluster.barrier_wait();
 
   // Blocks given back by this CTA's sequences: the x-th of the call goes behind
   // the free list's first `count`.
   const int g0 = b0 > 0 ? given[b0 - 1] : 0, g1 = b1 > b0 ? given[b1 - 1] : g0;
-  for (int x = g0 + tid; x < g1; x += kAssignThreads) {
+  auto given_id = [&](int x) {
     const int b = first_above(given, b0, b1, x);
     const int e = blocks_of(s_new[b - b0]) + x - (b > 0 ? given[b - 1] : 0);
-    const long long at = static_cast<long long>(count) + x;
-    if (at < a.n_blocks) a.free_blocks[at] = __ldcg(a.table + static_cast<size_t>(b) * a.max_blocks + e);
+    return __ldcg(a.table + static_cast<size_t>(b) * a.max_blocks + e);
+  };
+  auto in_pool = [&](int id) { return id >= 0 && id < a.n_blocks; };
+  auto push = [&](long long at, int id) {
+    if (at < a.n_blocks) a.free_blocks[at] = id;
+  };
+  auto sync_all = [&] {
+    if (nctas > 1) {
+      cluster.sync();
+    } else {
+      __syncthreads();
+    }
+  };
+  int gone = 0;
+  for (int x = g0 + tid; x < g1; x += kAssignThreads) {
+    const int id = given_id(x);
+    if (in_pool(id))
+      push(static_cast<long long>(count) + x, id);
+    else
+      ++gone;
   }
+  gone = __reduce_add_sync(0xffffffffu, gone);
+  if (gone != 0 && lane < nctas) atomicAdd(nctas > 1 ? cluster.map_shared_rank(&s_gone[rank], lane) : &s_gone[0], gone);
   // Blocks given back are in place, and every CTA has read the lengths and the
   // count, which the outputs may overwrite.
-  if (nctas > 1) {
-    cluster.sync();
-  } else {
-    __syncthreads();
+  sync_all();
+  int gone_all = 0;
+  const int gone_of = lane < nctas ? s_gone[lane] : 0;
+  if (__any_sync(0xffffffffu, gone_of != 0)) {  // (the same for all CTAs)
+    gone_all = __reduce_add_sync(0xffffffffu, gone_of);
+    const int gone_before = __reduce_add_sync(0xffffffffu, lane < rank ? gone_of : 0);
+    long long at = static_cast<long long>(count) + g0 - gone_before;
+    for (int x0 = g0; x0 < g1; x0 += kAssignThreads) {
+      const int x = x0 + tid;
+      const int id = x < g1 ? given_id(x) : -1;
+      const unsigned votes = __ballot_sync(0xffffffffu, in_pool(id));
+      if (lane == 0) s_warp[warp] = __popc(votes);
+      __syncthreads();
+      int before = 0, all = 0;  // in the warps before this one; in all
+      for (int w = 0; w < NW; ++w) {
+        const int n = static_cast<int>(s_warp[w]);
+        if (w < warp) before += n;
+        all += n;
+      }
+      if (in_pool(id)) push(at + before + __popc(votes & ((1u << lane) - 1)), id);
+      at += all;
+      __syncthreads();
+    }
+    sync_all();
   }
+  const int there =
+      static_cast<int>(min(static_cast<long long>(count) + back - gone_all, static_cast<long long>(a.n_blocks)));
   // Blocks taken: the x-th of the call is the free list's x-th from its top.  A
   // sequence is served if the blocks of all up to it are there.
   const int t0 = b0 > 0 ? taken[b0 - 1] : 0, t1 = b1 > b0 ? min(taken[b1 - 1], there) : t0;

@@ -436,13 +436,14 @@ typedef struct {
  *   positions, slots  [B][T]: token t of sequence b is position old_lens[b]
  *                   + t and its slot, or -1 and -1 past its granted length
  *                   (g4_kv4_append_normrope's arguments).
- * Blocks given back are pushed first, in the order of sequences and entries;
- * then blocks are popped in the same order.  Sequences are served first come,
+ * Blocks given back are pushed first, in the order of sequences and entries
+ * (an entry that holds no block of the pool, because the caller has taken it
+ * away, gives none back); then blocks are popped in the same order.  Sequences are served first come,
  * first served: one that needs blocks is granted its new length if the
  * blocks of all sequences up to it fit, else it keeps old_lens and gets no
- * slots.  Writes the table entries of the blocks taken, the free_blocks
- * entries of those given back, and the outputs; table entries of blocks given
- * back keep their stale ids.  With lens_out and free_count_out apart from
+ * slots.  Writes the table entries of the blocks taken, at most as many
+ * free_blocks entries behind the first free_count[0] as table entries are given
+ * back, and the outputs; table entries of blocks given back keep their stale ids.  With lens_out and free_count_out apart from
  * the inputs, a repeated call (a replayed graph) repeats its results.  B is at
  * most 8192 and B * max_blocks, B * T at most 2^31 - 1.
  */

@@ -108,7 +108,9 @@ def read_rows(data, table_row, kvh, positions, block_size, k_exp=0):
 
 
 def assign_blocks(old, new, T, block_size, n_blocks, free, count, table):
-    """Simulates one call: returns (table, free, count, lens, positions, slots); inputs are not changed."""
+    """Simulates one call: returns (table, free, count, lens, positions, slots); inputs are not changed.
+
+    Entries given back that hold no block of the pool do not go onto the free list."""
     table, stack = np.array(table), [int(x) for x in free[:count]]
     free = np.array(free)
     B, width = table.shape
@@ -118,7 +120,8 @@ def assign_blocks(old, new, T, block_size, n_blocks, free, count, table):
     new = [min(max(int(x), 0), cap, o + T) for x, o in zip(new, old)]
     for b in range(B):
         for e in range(ceil(new[b]), ceil(old[b])):
-            stack.append(int(table[b, e]))
+            if 0 <= table[b, e] < n_blocks:
+                stack.append(int(table[b, e]))
     free[:len(stack)] = stack
     lens = list(old)
     refused = False

@@ -1,0 +1,71 @@
+"""The paged 4-bit cache where its callers go past the plain run of things: tables whose blocks were taken away.
+Everything here is exact: bytes, ids, lengths."""
+
+import numpy as np
+import pytest
+
+from gemma_dual_geometry_gb300 import build as g4build
+
+from kv4_common import G, K, i32, torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    g4build.build()
+    G.lib()
+    yield
+    assert G.g4_take_device_error() == 0
+
+
+# ---------------------------------------------------------------- block assignment
+
+@pytest.mark.parametrize("B,T,bs,width,gone", [(1, 1, 16, 5, "some"), (6, 3, 16, 40, "some"), (64, 1, 64, 130, "front"),
+                                               (64, 5, 16, 300, "some"), (96, 2048, 16, 130, "front"), (9, 4, 32, 20, "all"),
+                                               (700, 3, 16, 70, "some"), (700, 3, 16, 70, "front"), (130, 1, 16, 3, "all")])
+@pytest.mark.parametrize("short", [False, True])
+@pytest.mark.parametrize("alias", [False, True])
+def test_assign_gives_back_only_blocks_of_the_pool(B, T, bs, width, gone, short, alias):
+    """Entries that hold no block (a caller took it away: those before a window, or any) are not put on the free
+    list when their sequence shrinks or ends; all that does go there, and who is served from it, stays exact."""
+    rng = np.random.default_rng(B * 7 + T + len(gone))
+    n = B * width + 9
+    lens = rng.integers(0, width * bs + 1, B)
+    lens[0] = width * bs
+    table = np.full((B, width), -1)
+    order = rng.permutation(n)
+    at = 0
+    for b in range(B):
+        have = -(-int(lens[b]) // bs)
+        ids = order[at:at + have].copy()
+        at += have
+        if gone == "all":
+            away = np.ones(have, bool)
+        elif gone == "front":
+            away = np.arange(have) < have - 2
+        else:
+            away = rng.random(have) < 0.3
+        ids[away] = rng.choice([-1, n, n + 7, -2 ** 31, 2 ** 31 - 1], int(away.sum()))
+        table[b, :have] = ids
+    free = np.full(n, -1)
+    count = min(3, n - at) if short else n - at
+    free[:count] = order[at:at + count]
+    kind = rng.random(B)
+    new = np.where(kind < 0.4, 0, np.where(kind < 0.6, lens // 2, lens + rng.integers(0, T + 1, B)))
+    new[0] = 0
+    want = K.assign_blocks(lens, new, T, bs, n, free, count, table)
+    assert all(0 <= x < n for x in want[1][:want[2]])
+    d_old, d_new, d_free, d_count, d_table = i32(lens), i32(new), i32(free), i32([count]), i32(table)
+    out = d_old if alias else i32(np.zeros(B))
+    left = d_count if alias else i32([0])
+    pos, slots = i32(np.zeros((B, T))), i32(np.zeros((B, T)))
+    for _ in range(1 if alias else 2):   # a repeated call repeats its results
+        G.g4_kv4_assign_blocks(B, T, bs, n, width, d_old, d_new, d_free, d_count, d_table, out, left, pos, slots)
+    got = [x.cpu().numpy().ravel() for x in (d_table, d_free, left, out, pos, slots)]
+    got[1], want = got[1][:want[2]], list(want)
+    want[1] = want[1][:want[2]]          # (what lies behind the count is nobody's)
+    for name, g, w in zip(("table", "free", "count", "lens", "positions", "slots"), got, want):
+        assert np.array_equal(g, np.asarray(w).ravel()), name
