@@ -30,6 +30,40 @@ cudaError_t set_smem_limit_once(int bytes) {
   return cudaSuccess;
 }
 
+// The largest cluster of at most 16 CTAs (of `threads` threads and `smem` bytes
+// of dynamic shared memory each, a limit raised before) that kernel Kern may be
+// launched with on the current device: 16 where one of them fits, else 8, which
+// are always allowed.  The opt-in past 8 belongs to the device too, so it is made,
+// and the answer kept, once per device, under a lock.
+template <auto Kern>
+unsigned cluster_limit_once(int threads, size_t smem) {
+  static std::mutex mu;
+  static unsigned limit[128] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 8;
+  std::lock_guard<std::mutex> lock(mu);
+  if (limit[dev] == 0) {
+    bool fits = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    if (fits) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(16);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 16;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      fits = cudaOccupancyMaxActiveClusters(&n, Kern, &cfg) == cudaSuccess && n > 0;
+    }
+    if (!fits) (void)cudaGetLastError();
+    limit[dev] = fits ? 16 : 8;
+  }
+  return limit[dev];
+}
+
 constexpr int kMaxHalf = 256;  // head_dim / 2 for the widest supported head (512)
 
 // Step a4: norm -> RoPE -> cache append.

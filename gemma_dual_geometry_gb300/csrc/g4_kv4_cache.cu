@@ -417,29 +417,15 @@ cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
   // (1000 that gain a token or end: 5.1 us against 11.3 with one CTA, 6.6 with one per
   // 256; one per 32 makes 64 of them 4.5 against 4.2), up to 16 (the largest cluster,
   // where one of them fits the device; 8 are always allowed).
-  static const unsigned most = [] {
-    if (cudaFuncSetAttribute(kv4_assign_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 8u;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(16);
-    cfg.blockDim = dim3(kAssignThreads);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 16;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    const bool fits = cudaOccupancyMaxActiveClusters(&n, kv4_assign_kernel, &cfg) == cudaSuccess && n > 0;
-    (void)cudaGetLastError();
-    return fits ? 16u : 8u;
-  }();
+  const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 16);
+  if (e != cudaSuccess) return e;
+  constexpr size_t kMostSmem = (2 * kKv4MaxBatch + 2 * (kKv4MaxBatch / kAssignMaxCtas)) * 4;  // of a CTA of 16
+  const unsigned most = cluster_limit_once<kv4_assign_kernel>(kAssignThreads, kMostSmem);
   const long long work = static_cast<long long>(a.B) * a.T;
   unsigned n = 1;
   while (n < most && n < static_cast<unsigned>(a.B) && (work > 4096LL * n || a.B > 64 * static_cast<int>(n))) n *= 2;
   const size_t per = (static_cast<size_t>(a.B) + n - 1) / n;
   const size_t smem = (2 * static_cast<size_t>(a.B) + 2 * per) * 4;
-  const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 16);
-  if (e != cudaSuccess) return e;
   return launch_pdl(kv4_assign_kernel, dim3(n), kAssignThreads, smem, n, s, a);
 }
 
