@@ -156,7 +156,8 @@ __host__ __device__ constexpr int kv4_row_at(int d) { return d + (d >> 6) * 8; }
 // blocks that the record keeps side by side are then exchanged between their
 // lanes, so that each lane has bytes that lie together.
 //   The divisions x / s and max / 6 are products with a rounded reciprocal,
-// brought back by a rounding to 2^-12 (x / s, which is at most 12) or to 16
+// brought back by a rounding to 2^-12 (x / s: at most 12 where s did not saturate
+// at 448, and past that the code saturates too) or to 16
 // significant bits (max / 6).  That is as good as the exact quotient: x and max
 // have 8 significant bits, the numbers between which codes and scales change, times s
 // or 6, at most 7 (3 of a code times 4 of a scale; 5 of a scale times 2 of a 6), so
@@ -197,8 +198,8 @@ __device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t*
   const float s = e4m3_value(byte);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  inv = s > 0.0f ? inv * mul : 0.0f;  // an all-zero block, or a NaN one: codes 0
-  const uint32_t sign = s > 0.0f ? 0x80000000u : 0u;
+  const bool coded = s > 0.0f;  // else a block of zeros (or all too small), or one that holds a NaN or an infinity: codes 0
+  inv = coded ? inv * mul : 0.0f;
   uint32_t code[(N + 7) / 8] = {};    // code bytes, in order
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
@@ -206,11 +207,13 @@ __device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t*
     const float2 x = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
     float2 q = __fmul2_rn(x, make_float2(inv, inv));
     q = __fadd2_rn(__fadd2_rn(q, make_float2(kSnap, kSnap)), make_float2(-kSnap, -kSnap));
-    // (a quotient that rounds to zero keeps its sign, except in a block without a scale)
-    code[i / 4] |= e2m1x2_byte(__uint_as_float(__float_as_uint(q.x) | (__float_as_uint(x.x) & sign)),
-                               __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(x.y) & sign)))
+    // (a quotient that rounds to zero keeps its sign)
+    code[i / 4] |= e2m1x2_byte(__uint_as_float(__float_as_uint(q.x) | (__float_as_uint(x.x) & 0x80000000u)),
+                               __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(x.y) & 0x80000000u)))
                    << (8 * (i % 4));
   }
+#pragma unroll
+  for (int i = 0; i < (N + 7) / 8; ++i) code[i] = coded ? code[i] : 0u;  // (a NaN's would be 6's)
   if (lane % LPB == 0)
     rec[is_k ? kv4_k_scale_at<HD>(m, d0) : kv4_v_scale_at<HD>(m, d0)] = static_cast<uint8_t>(byte);
 

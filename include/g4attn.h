@@ -369,7 +369,7 @@ g4_status g4_attn_decode_noalloc(const g4_layer_params* params, const g4_kv_cach
  * their negatives and saturates at 6), and the row stands for code_d s 2^e,
  * which bf16 holds exactly.  x is itself correctly rounded, so the bytes are
  * a function of the raw inputs alone, whatever kernel wrote them.  A 16 that
- * holds a NaN or an infinity gets the scale NaN and stands for NaNs.
+ * holds a NaN or an infinity gets the scale NaN and codes 0, and stands for NaNs.
  *
  * Where it lies.  data[n_blocks][n_kv_heads][block_size / 16] records of
  * 18 head_dim bytes, one per 16 positions of one kv head: K codes (8

@@ -1,12 +1,12 @@
-"""The paged 4-bit cache where its callers go past the plain run of things: tables whose blocks were taken away.
-Everything here is exact: bytes, ids, lengths."""
+"""The paged 4-bit cache where its callers go past the plain run of things: tables whose blocks were taken away,
+rows that hold no numbers.  Everything here is exact: bytes, ids, lengths."""
 
 import numpy as np
 import pytest
 
 from gemma_dual_geometry_gb300 import build as g4build
 
-from kv4_common import G, K, i32, torch
+from kv4_common import DEV, G, K, O, Pool, W, bf16_normal, f64, geometry, i32, params_of, torch
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,44 @@ def test_assign_gives_back_only_blocks_of_the_pool(B, T, bs, width, gone, short,
     want[1] = want[1][:want[2]]          # (what lies behind the count is nobody's)
     for name, g, w in zip(("table", "free", "count", "lens", "positions", "slots"), got, want):
         assert np.array_equal(g, np.asarray(w).ravel()), name
+
+
+# ---------------------------------------------------------------- append
+
+def store(data, slots, k, v, block_size, k_exp=0):
+    """Rows k, v [N, Hkv, hd] (bf16 values) into data at slots [N] >= 0, by the oracle."""
+    kc, ks, vc, vs = K.record_offsets(k.shape[-1])
+    (kq, ksc), (vq, vsc) = K.quantise(k, k_exp), K.quantise(v)
+    at = np.arange(k.shape[1])[None, :, None]
+    block, group, m = (slots // block_size)[:, None, None], (slots % block_size // 16)[:, None, None], slots % 16
+    for code, scale, co, so in ((kq, ksc, kc, ks), (vq, vsc, vc, vs)):
+        data[block, at, group, co[m][:, None, 0::2]] = code[..., 0::2] | code[..., 1::2] << 4
+        data[block, at, group, so[m][:, None, 0::16]] = scale
+
+
+@pytest.mark.parametrize("geo", [(W.SLIDING, 64, 3, 3, 17), (W.FULL, 128, 8, 1, 0), (W.SLIDING, 256, 8, 2, 40),
+                                 (W.FULL, 512, 4, 2, 0)])
+def test_append_bytes_of_blocks_without_numbers(geo):
+    """A 16 that holds a NaN or an infinity: scale NaN and codes 0, the other 16s of its row as ever."""
+    g = geometry(geo[0], geo[1], H=geo[2], Hkv=geo[3], window=geo[4])
+    hd, H, Hkv, T, bs = g["head_dim"], g["n_heads"], g["n_kv_heads"], 3, 16
+    pool = Pool(g, 1, T, bs, seed=1)
+    q, k, v = (bf16_normal((1, T, h, hd), s) for h, s in ((H, 1), (Hkv, 2), (Hkv, 3)))
+    kw = W.norm_weight(hd, 4)
+    kw[20], kw[40] = float("nan"), float("inf")   # elements of k (and what RoPE turns with them)
+    v[0, 1, 0, 9] = float("nan")                  # a whole row of v
+    pos = np.arange(T)[None]
+    slots = np.array([[pool.slot(0, p) for p in range(T)]])
+    pool.to_device()
+    G.g4_kv4_append_normrope(params_of(g), pool.pools, 0, q.to(DEV), k.to(DEV), v.to(DEV), W.norm_weight(hd, 5).to(DEV),
+                             kw.to(DEV), i32(pos), i32(slots), 1, T, torch.empty_like(q, device=DEV))
+    with np.errstate(invalid="ignore"):
+        kn, vn = O.normrope_kv(f64(k), f64(v), f64(kw), pos, hd, g["theta"], g["rotary_fraction"], g["eps"])
+    # pairs past the rotated ones pass through as they are (the oracle adds 0 times the other element: NaN next to an infinity)
+    still = np.arange(hd) % (hd // 2) >= O.rotated_pairs(hd, g["rotary_fraction"])
+    kn[..., still] = O.rms_norm(f64(k), f64(kw), g["eps"])[..., still]
+    assert np.isnan(vn[0, 1, 0]).all() and np.isfinite(kn).any() and not np.isfinite(kn[..., 20]).any()
+    want = pool.data.copy()
+    store(want, slots[0], O.round_bf16(kn)[0], O.round_bf16(vn)[0], bs)
+    got = pool.d.cpu().numpy()
+    assert np.array_equal(got, want), f"{(got != want).sum()} bytes differ"
