@@ -1,5 +1,5 @@
 """The paged 4-bit cache where its callers go past the plain run of things: tables whose blocks were taken away,
-rows that hold no numbers.  Everything here is exact: bytes, ids, lengths."""
+rows that hold no numbers, prompt-sized batches.  Everything here is exact: bytes, ids, lengths."""
 
 import numpy as np
 import pytest
@@ -82,6 +82,44 @@ def store(data, slots, k, v, block_size, k_exp=0):
     for code, scale, co, so in ((kq, ksc, kc, ks), (vq, vsc, vc, vs)):
         data[block, at, group, co[m][:, None, 0::2]] = code[..., 0::2] | code[..., 1::2] << 4
         data[block, at, group, so[m][:, None, 0::16]] = scale
+
+
+@pytest.mark.parametrize("geo", [(W.SLIDING, 64, 3, 3, 17), (W.FULL, 128, 8, 1, 0), (W.SLIDING, 256, 8, 2, 40),
+                                 (W.FULL, 512, 4, 2, 0)])
+@pytest.mark.parametrize("B,T", [(5, 520), (7, 520), (8, 515), (1, 1030)])
+def test_append_bytes_of_prompts(geo, B, T):
+    """From 1024 CTAs on a CTA takes all rows of its tokens: groups of four tokens, and a remainder of one or three."""
+    g = geometry(geo[0], geo[1], H=geo[2], Hkv=geo[3], window=geo[4])
+    hd, H, Hkv, bs = g["head_dim"], g["n_heads"], g["n_kv_heads"], 64
+    rng = np.random.default_rng(hd + B)
+    start = rng.integers(0, 300, B)
+    start[1:3] = start[0]           # neighbours whose positions agree
+    pool = Pool(g, B, 300 + T, bs, seed=hd + B)
+    x = {c: bf16_normal((B, T, h, hd), 70 + i) for i, (c, h) in enumerate((("q", H), ("k", Hkv), ("v", Hkv)))}
+    qw, kw = W.norm_weight(hd, 7), W.norm_weight(hd, 8)
+    pos = start[:, None] + np.arange(T)[None, :]
+    slots = np.take_along_axis(pool.table, pos // bs, 1) * bs + pos % bs
+    slots[rng.random((B, T)) < 0.1] = -1
+    slots[B - 1, T - 3:] = pool.n * bs   # outside the pool
+    pool.to_device()
+    q = x["q"].to(DEV)
+    q_out = torch.empty_like(q)
+    G.g4_kv4_append_normrope(params_of(g), pool.pools, 0, q, x["k"].to(DEV), x["v"].to(DEV), qw.to(DEV), kw.to(DEV),
+                             i32(pos), i32(slots), B, T, q_out)
+    kn, vn = O.normrope_kv(f64(x["k"]), f64(x["v"]), f64(kw), pos, hd, g["theta"], g["rotary_fraction"], g["eps"])
+    there = (slots >= 0) & (slots < pool.n * bs)
+    want = pool.data.copy()
+    store(want, slots[there], O.round_bf16(kn)[there], O.round_bf16(vn)[there], bs)
+    got = pool.d.cpu().numpy()
+    assert np.array_equal(got, want), f"{(got != want).sum()} bytes differ"
+    ref_q = O.round_bf16(O.normrope_q(f64(x["q"]), f64(qw), pos, hd, g["theta"], g["rotary_fraction"], g["eps"]))
+    assert np.array_equal(f64(q_out), ref_q)
+    # a layer that reads the pool of another: q alone, the pool left as it was
+    pools = G.kv4_pool_table(2)
+    pools[0] = pool.pools[0]
+    again = torch.empty_like(q)
+    G.g4_kv4_append_normrope(params_of(g, src=0), pools, 1, q, None, None, qw.to(DEV), None, i32(pos), None, B, T, again)
+    assert torch.equal(again, q_out) and np.array_equal(pool.d.cpu().numpy(), want)
 
 
 @pytest.mark.parametrize("geo", [(W.SLIDING, 64, 3, 3, 17), (W.FULL, 128, 8, 1, 0), (W.SLIDING, 256, 8, 2, 40),
