@@ -112,8 +112,10 @@ def lib():
 def _ptr(x):
     try:
         return x.data_ptr()
-    except AttributeError:  # an address, or None
-        return x
+    except AttributeError:
+        if x is None or isinstance(x, int):  # an address
+            return x
+        raise
 
 
 _raw_stream = None  # device index -> the address of its current stream
