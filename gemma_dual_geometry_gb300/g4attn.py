@@ -118,26 +118,37 @@ def _ptr(x):
         raise
 
 
-_raw_stream = None  # device index -> the address of its current stream
+_raw_stream = None      # device index -> the address of its current stream
+_current_device = None  # () -> the current device's index; None where there is one device only
 
 
-def _find_raw_stream():
+def _find_device_calls():
+    global _raw_stream, _current_device
     import torch
     # (building a torch.cuda.Stream object takes as long as a launch)
     get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get if get is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.device_count() > 1:
+        _current_device = torch.cuda.current_device
+    _raw_stream = get if get is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream, *tensors):
-    global _raw_stream
+    raw = None
     if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+        if raw != 0:
+            return raw
     for t in tensors:
         if t is not None and not isinstance(t, int) and t.is_cuda:
             if _raw_stream is None:
-                _raw_stream = _find_raw_stream()
-            return _raw_stream(t.get_device())
-    return None
+                _find_device_calls()
+            device = t.get_device()
+            # 0 is every device's default stream, and a launch there goes to the current device
+            if _current_device is not None and device != _current_device():
+                raise ValueError(f"tensors of cuda:{device}, but the current device is cuda:{_current_device()}: "
+                                 f"call under torch.cuda.device({device})")
+            return _raw_stream(device) if raw is None else raw
+    return raw
 
 
 def _check(status):
