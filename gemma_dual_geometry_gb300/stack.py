@@ -129,14 +129,20 @@ class PagedAttnStack:
         self.ws_bytes = max(G.g4_kv4_decode_workspace_size(p, self.B, self.max_len) for p in self.params)
         self.ws = torch.zeros(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
         self._i32 = i32
-        self._steps = {}           # T -> (positions, slots, prefill workspace)
+        self._steps = {}           # T -> (positions, slots)
+        self._prefill_ws = {}      # T -> workspace
 
     def _step(self, T):
         if T not in self._steps:
-            size = max(G.g4_kv4_prefill_workspace_size(p, self.B, T, self.max_len) for p in self.params) if T > 1 else 0
-            self._steps[T] = (self._i32(self.B, T), self._i32(self.B, T),
-                              torch.empty(size, dtype=torch.uint8, device=self.device))
+            self._steps[T] = self._i32(self.B, T), self._i32(self.B, T)
         return self._steps[T]
+
+    def _prefill_workspace(self, T, stream):
+        if T not in self._prefill_ws:
+            size = max(G.g4_kv4_prefill_workspace_size(p, self.B, T, self.max_len) for p in self.params)
+            with self._on(stream):
+                self._prefill_ws[T] = torch.empty(size, dtype=torch.uint8, device=self.device)
+        return self._prefill_ws[T]
 
     def _on(self, stream):
         """What torch does within runs on ``stream`` (a stream, an address, or None: the current one)."""
@@ -156,7 +162,7 @@ class PagedAttnStack:
         """Blocks for sequences that go to new_lens [B] positions with T new tokens at most (0 ends one).
         Sets ``lens`` (what was granted) and ``start``; the T tokens' positions and slots serve append()."""
         with self._on(stream):
-            positions, slots, _ = self._step(T)
+            positions, slots = self._step(T)
             self.start.copy_(self.lens)
         G.g4_kv4_assign_blocks(self.B, T, self.block_size, self.n_blocks, self.max_blocks, self.lens, new_lens,
                                self.free_blocks, self.free_count, self.block_table, self.lens, self.free_count,
@@ -164,12 +170,12 @@ class PagedAttnStack:
         return positions, slots
 
     def append(self, l, q, k, v, qw, kw, T, q_out, stream=None):
-        positions, slots, _ = self._step(T)
+        positions, slots = self._step(T)
         G.g4_kv4_append_normrope(self.params[l], self.table, l, q, k, v, qw, kw, positions,
                                  slots if self.owns(l) else None, self.B, T, q_out, stream=stream)
 
     def prefill_attn(self, l, q_out, T, out, stream=None):
-        ws = self._step(T)[2]
+        ws = self._prefill_workspace(T, stream)
         G.g4_kv4_attn_prefill(self.params[l], self.table, l, q_out, self.block_table, self.max_blocks, self.start,
                               self.lens, self.B, T, self.max_len, out, ws, ws.numel(), stream=stream)
 

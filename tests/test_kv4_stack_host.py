@@ -1,0 +1,81 @@
+"""What PagedAttnStack holds and hands to the library's calls, on the host: the calls that launch are replaced by
+ones that note their arguments (no GPU needed)."""
+
+import pytest
+import torch
+
+from gemma_dual_geometry_gb300 import build as g4build
+from gemma_dual_geometry_gb300 import g4attn as G
+from gemma_dual_geometry_gb300 import stack as S
+from gemma_dual_geometry_gb300 import workloads as W
+
+CFG = dict(B=3, H=4, Hkv=2, dtype=W.BF16, seed=0, types=[W.SLIDING, W.FULL, W.SLIDING, W.FULL], n_shared=2,
+           geom={W.SLIDING: dict(head_dim=64, theta=1e4, rotary_fraction=1.0, window=24),
+                 W.FULL: dict(head_dim=128, theta=1e6, rotary_fraction=0.25, window=0)})
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(name, arguments by position) of the calls made."""
+    g4build.build()
+    G.lib()
+    seen = []
+    for name in ("g4_kv4_assign_blocks", "g4_kv4_append_normrope", "g4_kv4_attn_prefill", "g4_kv4_attn_decode"):
+        monkeypatch.setattr(G, name, lambda *a, stream=None, name=name: seen.append((name, a)))
+    return seen
+
+
+def make(**kw):
+    return S.PagedAttnStack(CFG, max_len=160, n_blocks=26, block_size=32, device="cpu", **kw)
+
+
+def lens(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def prefill(st, T, calls, l=1):
+    q = torch.zeros((3, T, 4, 128), dtype=torch.bfloat16)
+    st.prefill_attn(l, q, T, q)
+    name, a = calls[-1]
+    assert name == "g4_kv4_attn_prefill"
+    return a[-2], a[-1]   # workspace and its bytes
+
+
+def need(st, T, l=1):
+    return G.g4_kv4_prefill_workspace_size(st.params[l], 3, T, st.max_len)
+
+
+@pytest.mark.parametrize("T", [1, 2, 40])
+def test_prefill_has_the_workspace_it_needs(calls, T):
+    """A prompt of one token too."""
+    st = make()
+    st.assign(lens(T, T, T), T)
+    ws, size = prefill(st, T, calls)
+    assert size >= need(st, T) > 0 and ws.numel() >= size
+
+
+def test_decode_steps_hold_no_prefill_workspace(calls):
+    st = make()
+    before = held(st)
+    st.assign(lens(1, 1, 1), 1)
+    q = torch.zeros((3, 4, 128), dtype=torch.bfloat16)
+    st.decode_attn(1, q, q)
+    assert held(st) - before <= 2 * 4 * 3 + 64
+
+
+def held(st):
+    """Bytes of the tensors that an object keeps, in containers too."""
+    found = {}
+
+    def look(x):
+        if isinstance(x, torch.Tensor):
+            found[x.data_ptr()] = x.untyped_storage().nbytes()
+        elif isinstance(x, dict):
+            for y in x.values():
+                look(y)
+        elif isinstance(x, (list, tuple, set)):
+            for y in x:
+                look(y)
+
+    look(vars(st))
+    return sum(found.values())
