@@ -130,19 +130,34 @@ class PagedAttnStack:
         self.ws = torch.zeros(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
         self._i32 = i32
         self._steps = {}           # T -> (positions, slots)
-        self._prefill_ws = {}      # T -> workspace
+        self._prefill_ws, self._prefill_T = None, 0  # one workspace for prefills of up to so many tokens
+        self._captured_ws = False  # whether a graph was captured with it
+        self._kept_ws = []         # outgrown ones that graphs still use
 
     def _step(self, T):
         if T not in self._steps:
             self._steps[T] = self._i32(self.B, T), self._i32(self.B, T)
         return self._steps[T]
 
+    def _capturing(self, stream):
+        if self.device.type != "cuda":
+            return False
+        with self._on(stream):
+            return torch.cuda.is_current_stream_capturing()
+
     def _prefill_workspace(self, T, stream):
-        if T not in self._prefill_ws:
+        """The workspace of the longest prefill yet, which serves all of them in turn; outgrown ones go, but for
+        those that a graph was captured with."""
+        if T > self._prefill_T:
             size = max(G.g4_kv4_prefill_workspace_size(p, self.B, T, self.max_len) for p in self.params)
+            if self._captured_ws:
+                self._kept_ws.append(self._prefill_ws)
+            self._prefill_ws, self._prefill_T, self._captured_ws = None, 0, False  # (gone before the next is taken)
             with self._on(stream):
-                self._prefill_ws[T] = torch.empty(size, dtype=torch.uint8, device=self.device)
-        return self._prefill_ws[T]
+                self._prefill_ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+            self._prefill_T = T
+        self._captured_ws = self._captured_ws or self._capturing(stream)
+        return self._prefill_ws
 
     def _on(self, stream):
         """What torch does within runs on ``stream`` (a stream, an address, or None: the current one)."""

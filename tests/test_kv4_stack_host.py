@@ -79,3 +79,37 @@ def held(st):
 
     look(vars(st))
     return sum(found.values())
+
+
+def test_prefills_share_one_workspace(calls):
+    """Chunks of any lengths: what is held is the longest one's, not one per length."""
+    st = make()
+    before = held(st)
+    order = [40, 2, 39, 1, 17, 80] + list(range(3, 60))
+    for T in order:
+        st.assign(lens(T, T, T), T)
+        for l in range(4):
+            ws, size = prefill(st, T, calls, l)
+            assert size >= max(need(st, T, i) for i in range(4)) and ws.numel() >= size
+    small = sum(2 * 4 * 3 * T for T in set(order))   # positions and slots
+    assert held(st) - before <= max(need(st, 80, i) for i in range(4)) + small
+
+
+def test_a_captured_workspace_outlives_a_larger_one(calls, monkeypatch):
+    """A graph goes on using the workspace that it was captured with."""
+    st = make()
+    monkeypatch.setattr(st, "_capturing", lambda stream: True)
+    first, size = prefill(st, 5, calls)
+    monkeypatch.setattr(st, "_capturing", lambda stream: False)
+    at = first.data_ptr()
+    del first
+    calls.clear()
+    prefill(st, 60, calls)
+    prefill(st, 70, calls)   # (not captured: replaced)
+    calls.clear()
+    kept = []
+    for x in vars(st).values():
+        kept += [y for y in (x if isinstance(x, list) else [x]) if isinstance(y, torch.Tensor)]
+    assert at in [x.data_ptr() for x in kept]
+    assert held(st) >= size + need(st, 70)
+    assert sum(x.untyped_storage().nbytes() == need(st, 60) for x in kept) == 0
