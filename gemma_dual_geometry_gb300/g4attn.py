@@ -132,6 +132,13 @@ def _find_device_calls():
     _raw_stream = get if get is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
+def current_stream(device):
+    """The address of the current stream of the device with this index."""
+    if _raw_stream is None:
+        _find_device_calls()
+    return _raw_stream(device)
+
+
 def _stream(stream, *tensors):
     raw = None
     if stream is not None:
@@ -140,14 +147,13 @@ def _stream(stream, *tensors):
             return raw
     for t in tensors:
         if t is not None and not isinstance(t, int) and t.is_cuda:
-            if _raw_stream is None:
-                _find_device_calls()
             device = t.get_device()
+            here = current_stream(device)
             # 0 is every device's default stream, and a launch there goes to the current device
             if _current_device is not None and device != _current_device():
                 raise ValueError(f"tensors of cuda:{device}, but the current device is cuda:{_current_device()}: "
                                  f"call under torch.cuda.device({device})")
-            return _raw_stream(device) if raw is None else raw
+            return here if raw is None else raw
     return raw
 
 

@@ -97,7 +97,10 @@ class AttnStack:
 
 class PagedAttnStack:
     """A stack over the paged 4-bit cache: B sequence slots of at most max_len positions, whose layers share
-    one block table and n_blocks blocks of block_size positions.  ``k_exp`` as in g4_kv4_pool."""
+    one block table and n_blocks blocks of block_size positions.  ``k_exp`` as in g4_kv4_pool.
+
+    Calls may go to any stream, one after another.  The stack's memory stays its own until the streams that it was
+    used on (torch's; not addresses) are done with it, also when the stack goes before that."""
 
     def __init__(self, cfg, max_len, n_blocks, block_size=64, device="cuda", B=None, k_exp=0):
         self.cfg = cfg
@@ -128,15 +131,41 @@ class PagedAttnStack:
         # one decode workspace serves all layers in turn
         self.ws_bytes = max(G.g4_kv4_decode_workspace_size(p, self.B, self.max_len) for p in self.params)
         self.ws = torch.zeros(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
+        self._streams = {}         # address -> stream, of those that have used the buffers
+        if self.device.type == "cuda":
+            home = torch.cuda.current_stream(self.device)
+            home.synchronize()     # what was queued above is there for any stream
+            self._streams[home.cuda_stream] = home
         self._i32 = i32
         self._steps = {}           # T -> (positions, slots)
         self._prefill_ws, self._prefill_T = None, 0  # one workspace for prefills of up to so many tokens
         self._captured_ws = False  # whether a graph was captured with it
         self._kept_ws = []         # outgrown ones that graphs still use
 
+    def _buffers(self):
+        own = [self.block_table, self.free_blocks, self.free_count, self.lens, self.start, self.ws, self._prefill_ws]
+        own += [*self.pools.values(), *self._kept_ws, *(t for step in self._steps.values() for t in step)]
+        return [t for t in own if t is not None]
+
+    def _use(self, stream):
+        """A call is about to go to ``stream``: no buffer is anyone else's before that stream is done with it."""
+        if self.device.type != "cuda" or isinstance(stream, int):
+            return
+        at = G.current_stream(self.lens.get_device()) if stream is None else stream.cuda_stream
+        if at not in self._streams:
+            self._streams[at] = torch.cuda.current_stream(self.device) if stream is None else stream
+            for t in self._buffers():
+                t.record_stream(self._streams[at])
+
+    def _new(self, t):
+        """A buffer taken later may come to be used on all those streams."""
+        for s in self._streams.values():
+            t.record_stream(s)
+        return t
+
     def _step(self, T):
         if T not in self._steps:
-            self._steps[T] = self._i32(self.B, T), self._i32(self.B, T)
+            self._steps[T] = self._new(self._i32(self.B, T)), self._new(self._i32(self.B, T))
         return self._steps[T]
 
     def _capturing(self, stream):
@@ -154,7 +183,7 @@ class PagedAttnStack:
                 self._kept_ws.append(self._prefill_ws)
             self._prefill_ws, self._prefill_T, self._captured_ws = None, 0, False  # (gone before the next is taken)
             with self._on(stream):
-                self._prefill_ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+                self._prefill_ws = self._new(torch.empty(size, dtype=torch.uint8, device=self.device))
             self._prefill_T = T
         self._captured_ws = self._captured_ws or self._capturing(stream)
         return self._prefill_ws
@@ -176,6 +205,7 @@ class PagedAttnStack:
     def assign(self, new_lens, T, stream=None):
         """Blocks for sequences that go to new_lens [B] positions with T new tokens at most (0 ends one).
         Sets ``lens`` (what was granted) and ``start``; the T tokens' positions and slots serve append()."""
+        self._use(stream)
         with self._on(stream):
             positions, slots = self._step(T)
             self.start.copy_(self.lens)
@@ -185,20 +215,24 @@ class PagedAttnStack:
         return positions, slots
 
     def append(self, l, q, k, v, qw, kw, T, q_out, stream=None):
+        self._use(stream)
         positions, slots = self._step(T)
         G.g4_kv4_append_normrope(self.params[l], self.table, l, q, k, v, qw, kw, positions,
                                  slots if self.owns(l) else None, self.B, T, q_out, stream=stream)
 
     def prefill_attn(self, l, q_out, T, out, stream=None):
+        self._use(stream)
         ws = self._prefill_workspace(T, stream)
         G.g4_kv4_attn_prefill(self.params[l], self.table, l, q_out, self.block_table, self.max_blocks, self.start,
                               self.lens, self.B, T, self.max_len, out, ws, ws.numel(), stream=stream)
 
     def decode_attn(self, l, q_out, out, stream=None):
+        self._use(stream)
         G.g4_kv4_attn_decode(self.params[l], self.table, l, q_out, self.block_table, self.max_blocks, self.lens,
                              self.B, self.max_len, out, self.ws, self.ws_bytes, stream=stream)
 
     def gather(self, l, start, rows, k_out, v_out, stream=None):
         """Positions [start[b], start[b] + rows) of every sequence as bf16 rows."""
+        self._use(stream)
         G.g4_kv4_gather(self.params[l], self.table, l, self.block_table, self.max_blocks, start, self.lens, self.B,
                         rows, k_out, v_out, stream=stream)
