@@ -203,8 +203,13 @@ class PagedAttnStack:
         return sum(p.numel() for p in self.pools.values())
 
     def assign(self, new_lens, T, stream=None):
-        """Blocks for sequences that go to new_lens [B] positions with T new tokens at most (0 ends one).
+        """Blocks for sequences that go to new_lens [B] (int32) positions with T new tokens at most (0 ends one).
         Sets ``lens`` (what was granted) and ``start``; the T tokens' positions and slots serve append()."""
+        if not isinstance(new_lens, int):   # (an address)
+            like = self.lens
+            if not (isinstance(new_lens, torch.Tensor) and new_lens.dtype == like.dtype and new_lens.numel() == self.B
+                    and new_lens.get_device() == like.get_device() and new_lens.is_contiguous()):
+                raise ValueError(f"new_lens must be {self.B} int32 lengths, contiguous, on the stack's device")
         self._use(stream)
         with self._on(stream):
             positions, slots = self._step(T)

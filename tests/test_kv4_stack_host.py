@@ -113,3 +113,16 @@ def test_a_captured_workspace_outlives_a_larger_one(calls, monkeypatch):
     assert at in [x.data_ptr() for x in kept]
     assert held(st) >= size + need(st, 70)
     assert sum(x.untyped_storage().nbytes() == need(st, 60) for x in kept) == 0
+
+
+@pytest.mark.parametrize("want", [[4, 4, 4], torch.tensor([4, 4, 4]), torch.tensor([4.0, 4.0, 4.0]), lens(4, 4), lens(4, 4, 4, 4),
+                                  lens(4, 0, 4, 0, 4, 0)[::2], None])
+def test_assign_takes_int32_lengths_of_its_sequences_only(calls, want):
+    """64-bit lengths, read as 32-bit ones, would end sequences."""
+    st = make()
+    with pytest.raises(ValueError, match="new_lens"):
+        st.assign(want, 4)
+    assert not calls and not st._steps
+    st.assign(lens(4, 4, 4), 4)
+    st.assign(lens(8, 8, 8).data_ptr(), 4)   # an address is the caller's word
+    assert len(calls) == 2
