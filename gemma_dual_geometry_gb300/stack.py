@@ -220,6 +220,8 @@ class PagedAttnStack:
         return positions, slots
 
     def append(self, l, q, k, v, qw, kw, T, q_out, stream=None):
+        if T not in self._steps:
+            raise ValueError(f"append of {T} tokens per sequence: assign() gave out no slots for so many")
         self._use(stream)
         positions, slots = self._step(T)
         G.g4_kv4_append_normrope(self.params[l], self.table, l, q, k, v, qw, kw, positions,

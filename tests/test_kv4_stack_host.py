@@ -126,3 +126,18 @@ def test_assign_takes_int32_lengths_of_its_sequences_only(calls, want):
     st.assign(lens(4, 4, 4), 4)
     st.assign(lens(8, 8, 8).data_ptr(), 4)   # an address is the caller's word
     assert len(calls) == 2
+
+
+def test_append_follows_an_assignment(calls):
+    """Before one of as many tokens there are no slots: the rows of all tokens would go to slot 0."""
+    st = make()
+    x = [torch.zeros((3, 4, n, 128), dtype=torch.bfloat16) for n in (4, 2, 2)]
+    w = torch.zeros(128)
+    st.assign(lens(1, 1, 1), 1)
+    calls.clear()
+    with pytest.raises(ValueError, match="assign"):
+        st.append(1, *x, w, w, 4, torch.empty_like(x[0]))
+    assert not calls
+    st.assign(lens(5, 5, 5), 4)
+    st.append(1, *x, w, w, 4, torch.empty_like(x[0]))
+    assert calls[-1][0] == "g4_kv4_append_normrope"
