@@ -31,7 +31,9 @@
  *     except a thread-local error message, one device-side error word (see
  *     g4_take_device_error), the built-in scratch of g4_attn_decode_noalloc
  *     and 64 pairs of work-item counters of the bf16 prefill (see
- *     g4_attn_prefill), all of them static device variables.
+ *     g4_attn_prefill), the last three static device variables; and on the
+ *     host, per thread, the RoPE frequencies of the last four (theta, head_dim,
+ *     rotated pairs) met, and per device its kernels' launch attributes.
  *   - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL is the legacy default stream).  A call that returns G4_OK has only
  *     enqueued work.
@@ -357,8 +359,15 @@ g4_status g4_attn_decode_noalloc(const g4_layer_params* params, const g4_kv_cach
  * The cache above is one rectangle of bf16 or float32 rows per layer.  A
  * server that holds many contexts of differing lengths keeps them instead in
  * blocks of 16 to 128 positions, dealt out of a pool as sequences grow, and
- * in 4.5 bits per element: decode streams the cache, so 2 / 0.5625 = 3.6
- * times fewer bytes are 3.6 times more contexts and as much less to stream.
+ * in 4.5 bits per element, 2 / 0.5625 = 3.6 times fewer bytes than bf16: as much
+ * less for decode to stream, and on layers that keep all positions 3.6 times more
+ * contexts.  A sequence's blocks hold all its positions on sliding layers too,
+ * where the bf16 ring above keeps one window: over a stack that is mostly sliding
+ * layers, one table for all of them saves little memory against rings (the
+ * 42-layer stack of 20 sliding and 4 full caches: 132 MB per context of 8192
+ * positions against 155).  Sliding layers with a table and free list of their own
+ * do not need the blocks behind the window: the caller may take such a block away
+ * at any time (its entry becomes -1, its id goes onto the free list).
  * (The pages have no counterpart: this is a cache of this library.)
  *
  * What a row holds.  x is the bf16 row that g4_kv_append_normrope would
@@ -490,8 +499,10 @@ size_t g4_kv4_decode_workspace_size(const g4_layer_params* params, int32_t B, in
  * layer, batch and lengths (size it for the largest).  Calls that overlap on
  * the GPU need a workspace each.  q.k and P.V run on
  * tensor cores from fp16 operands with float32 sums: keys and values are
- * exact in fp16, q is scaled by a power of two per head, and a probability
- * times its value's scale is rounded to 11 bits.
+ * exact in fp16, q is scaled by a power of two per head, and a probability and
+ * its product with its value's scale are each rounded to fp16: relative to the
+ * row's largest probability to 11 bits from 2^-18 on, below that to a multiple
+ * of 2^-28.
  */
 g4_status g4_kv4_attn_decode(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
                              int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,
@@ -514,11 +525,13 @@ size_t g4_kv4_prefill_workspace_size(const g4_layer_params* params, int32_t B, i
  *   workspace    16-byte aligned, no contents needed; not shared by calls
  *                that overlap
  * The keys that the T tokens see are laid out in the workspace as bf16 (a
- * sliding layer's T + window - 1, a full layer's max_seq_len + T per sequence)
- * and attention runs on the tensor cores as in g4_attn_prefill, whose limits on
- * launches in flight hold.  As there, a masked key has the weight zero, and zero
- * times NaN is NaN: a NaN or an infinity held at a position may reach every query
- * of the tiles (128 queries, 128 keys) that contain it.
+ * sliding layer's T + window - 1, a full layer's max_seq_len + T per sequence: for
+ * as many positions 3.6 times the pool's bytes, so max_seq_len is better the
+ * longest length at hand than the longest there may be) and attention runs on the
+ * tensor cores as in g4_attn_prefill, whose limits on launches in flight hold.  As
+ * there, a masked key has the weight zero, and zero times NaN is NaN: a NaN or an
+ * infinity held at a position may reach every query of the tiles (128 queries, 128
+ * keys) that contain it.
  */
 g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* pools, int32_t n_layers,
                               int32_t layer, const void* q, const int32_t* block_table, int32_t max_blocks,

@@ -1,12 +1,13 @@
 """The paged 4-bit cache where its callers go past the plain run of things: tables whose blocks were taken away,
-rows that hold no numbers, prompt-sized batches.  Everything here is exact: bytes, ids, lengths."""
+rows that hold no numbers, prompt-sized batches.  Bytes, ids and lengths are exact."""
 
 import numpy as np
 import pytest
 
 from gemma_dual_geometry_gb300 import build as g4build
 
-from kv4_common import DEV, G, K, O, Pool, W, bf16_normal, f64, geometry, i32, params_of, torch
+from kv4_common import (DEV, G, K, O, Pool, W, assert_within, attention_and_scale, bf16_normal, f64, geometry, i32,
+                        params_of, torch)
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +149,68 @@ def test_append_bytes_of_blocks_without_numbers(geo):
     store(want, slots[0], O.round_bf16(kn)[0], O.round_bf16(vn)[0], bs)
     got = pool.d.cpu().numpy()
     assert np.array_equal(got, want), f"{(got != want).sum()} bytes differ"
+
+
+# ---------------------------------------------------------------- as they are used
+
+def test_blocks_behind_a_window_are_taken_away():
+    """A sliding layer with a table of its own, whose caller takes blocks back as they fall behind the window: the
+    pool is a fraction of the contexts it serves, attention is that over all positions, prompts and steps alike,
+    and once the sequences have ended the free list holds every block once."""
+    window, bs, hd, H, Hkv, B, n = 20, 16, 64, 4, 2, 3, 15
+    g = geometry(W.SLIDING, hd, H=H, Hkv=Hkv, window=window)
+    p = params_of(g)
+    width = 12                                                     # 36 blocks' worth of positions, 15 blocks
+    pools = G.kv4_pool_table(1)
+    data = torch.full((G.kv4_pool_bytes(n, Hkv, bs, hd),), 255, dtype=torch.uint8, device=DEV)
+    G.set_kv4_pool(pools, 0, data, W.SLIDING, hd, Hkv, n, bs)
+    table, free, count = i32(np.full((B, width), -1)), i32(np.arange(n)), i32([n])
+    lens = i32(np.zeros(B))
+    qw, kw = W.norm_weight(hd, 1).to(DEV), W.norm_weight(hd, 2).to(DEV)
+    most = width * bs
+    rows = [[] for _ in range(B)]
+    held = np.zeros(B, int)
+    plan = [(40, [40, 17, 33])] + [(30, [40 + 30 * i, 17 + 25 * i, 33 + 14 * i]) for i in range(1, 4)]
+    plan += [(1, [130 + i, 92 + i, 75 + i]) for i in range(1, 25)] + [(1, [0, 0, 0])]
+    for step, (T, want) in enumerate(plan):
+        pos, slots, start = i32(np.zeros((B, T))), i32(np.zeros((B, T))), lens.clone()
+        G.g4_kv4_assign_blocks(B, T, bs, n, width, lens, i32(want), free, count, table, lens, count, pos, slots)
+        assert lens.tolist() == want, step
+        if not any(want):
+            break
+        q, k, v = (bf16_normal((B, T, h, hd), 10 * step + i) for i, h in enumerate((H, Hkv, Hkv)))
+        qo = torch.empty_like(q, device=DEV)
+        out = torch.empty_like(qo)
+        G.g4_kv4_append_normrope(p, pools, 0, q.to(DEV), k.to(DEV), v.to(DEV), qw, kw, pos, slots, B, T, qo)
+        if T == 1:
+            nb = G.g4_kv4_decode_workspace_size(p, B, most)
+            ws = torch.zeros(max(16, nb), dtype=torch.uint8, device=DEV)
+            G.g4_kv4_attn_decode(p, pools, 0, qo, table, width, lens, B, most, out, ws, nb)
+        else:
+            nb = G.g4_kv4_prefill_workspace_size(p, B, T, most)
+            ws = torch.full((nb,), 255, dtype=torch.uint8, device=DEV)
+            G.g4_kv4_attn_prefill(p, pools, 0, qo, table, width, start, lens, B, T, most, out, ws, nb)
+        at = pos.cpu().numpy()
+        qn = O.round_bf16(O.normrope_q(f64(q), f64(qw), at, hd, g["theta"], 1.0, g["eps"]))
+        kn, vn = O.normrope_kv(f64(k), f64(v), f64(kw), at, hd, g["theta"], 1.0, g["eps"])
+        kn, vn = (K.values(*K.quantise(O.round_bf16(x))) for x in (kn, vn))
+        for b in range(B):
+            fresh = want[b] - held[b]
+            rows[b] += [(kn[b, t], vn[b, t]) for t in range(fresh)]
+            kk, vv = (np.stack([r[i] for r in rows[b]], 1)[None] for i in (0, 1))
+            ref, mag = attention_and_scale(qn[b:b + 1, :fresh], kk, vv, held[b] + np.arange(fresh)[None],
+                                           np.array([want[b]]), Hkv, g)
+            assert_within(f64(out[b:b + 1, :fresh]), ref, mag, 2.0 ** -8 if T == 1 else 2.0 ** -7, f"step {step}",
+                          keys=window if T == 1 else 0)   # (the bounds of test_gpu_kv4)
+        held = np.array(want)
+        # the next token sees the positions from want - window + 1 on: blocks wholly before that go back
+        ids, stack = table.cpu().numpy(), free.cpu().numpy()[:count.item()].tolist()
+        for b in range(B):
+            for e in range(max(0, want[b] - window + 1) // bs):
+                if ids[b, e] >= 0:
+                    stack.append(int(ids[b, e]))
+                    ids[b, e] = -1
+        table.copy_(i32(ids))
+        free[:len(stack)] = i32(stack)
+        count.fill_(len(stack))
+    assert count.item() == n and sorted(free.tolist()) == list(range(n))
