@@ -138,14 +138,14 @@ class PagedAttnStack:
             self._streams[home.cuda_stream] = home
         self._i32 = i32
         self._steps = {}           # T -> (positions, slots)
-        self._prefill_ws, self._prefill_T = None, 0  # one workspace for prefills of up to so many tokens
+        self._no_ws = torch.empty(0, dtype=torch.uint8, device=self.device)
+        self._prefill_ws, self._prefill_T = self._no_ws, 0  # one workspace for prefills of up to so many tokens
         self._captured_ws = False  # whether a graph was captured with it
         self._kept_ws = []         # outgrown ones that graphs still use
 
     def _buffers(self):
         own = [self.block_table, self.free_blocks, self.free_count, self.lens, self.start, self.ws, self._prefill_ws]
-        own += [*self.pools.values(), *self._kept_ws, *(t for step in self._steps.values() for t in step)]
-        return [t for t in own if t is not None]
+        return own + [*self.pools.values(), *self._kept_ws, *(t for step in self._steps.values() for t in step)]
 
     def _use(self, stream):
         """A call is about to go to ``stream``: no buffer is anyone else's before that stream is done with it."""
@@ -177,11 +177,11 @@ class PagedAttnStack:
     def _prefill_workspace(self, T, stream):
         """The workspace of the longest prefill yet, which serves all of them in turn; outgrown ones go, but for
         those that a graph was captured with."""
-        if T > self._prefill_T:
+        if self._prefill_T < T <= self.max_len:   # (more are the call's to refuse)
             size = max(G.g4_kv4_prefill_workspace_size(p, self.B, T, self.max_len) for p in self.params)
             if self._captured_ws:
                 self._kept_ws.append(self._prefill_ws)
-            self._prefill_ws, self._prefill_T, self._captured_ws = None, 0, False  # (gone before the next is taken)
+            self._prefill_ws, self._prefill_T, self._captured_ws = self._no_ws, 0, False  # (gone before the next is taken)
             with self._on(stream):
                 self._prefill_ws = self._new(torch.empty(size, dtype=torch.uint8, device=self.device))
             self._prefill_T = T

@@ -141,3 +141,18 @@ def test_append_follows_an_assignment(calls):
     st.assign(lens(5, 5, 5), 4)
     st.append(1, *x, w, w, 4, torch.empty_like(x[0]))
     assert calls[-1][0] == "g4_kv4_append_normrope"
+
+
+def test_prefills_of_no_or_too_many_tokens_leave_the_workspace(calls):
+    """No tokens need none; more than fit a sequence are the call's to refuse, and those after it find what they need."""
+    st = make()
+    ws, size = prefill(st, 0, calls)
+    assert size == ws.numel() == 0
+    prefill(st, 9, calls)
+    before = held(st)
+    prefill(st, st.max_len + 1, calls)
+    assert held(st) == before
+    prefill(st, 0, calls)
+    for T in (5, 9, 30, st.max_len):
+        ws, size = prefill(st, T, calls)
+        assert ws.numel() >= size >= need(st, T)
