@@ -132,6 +132,7 @@ class PagedAttnStack:
         self.ws_bytes = max(G.g4_kv4_decode_workspace_size(p, self.B, self.max_len) for p in self.params)
         self.ws = torch.zeros(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
         self._streams = {}         # address -> stream, of those that have used the buffers
+        self._by_address = False   # whether others have, of which the address is all that is known
         if self.device.type == "cuda":
             home = torch.cuda.current_stream(self.device)
             home.synchronize()     # what was queued above is there for any stream
@@ -149,7 +150,10 @@ class PagedAttnStack:
 
     def _use(self, stream):
         """A call is about to go to ``stream``: no buffer is anyone else's before that stream is done with it."""
-        if self.device.type != "cuda" or isinstance(stream, int):
+        if isinstance(stream, int):
+            self._by_address = True
+            return
+        if self.device.type != "cuda":
             return
         at = G.current_stream(self.lens.get_device()) if stream is None else stream.cuda_stream
         if at not in self._streams:
@@ -168,6 +172,10 @@ class PagedAttnStack:
             self._steps[T] = self._new(self._i32(self.B, T)), self._new(self._i32(self.B, T))
         return self._steps[T]
 
+    def _wait_for_all(self):
+        if self.device.type == "cuda":
+            torch.cuda.synchronize(self.device)
+
     def _capturing(self, stream):
         if self.device.type != "cuda":
             return False
@@ -179,8 +187,10 @@ class PagedAttnStack:
         those that a graph was captured with."""
         if self._prefill_T < T <= self.max_len:   # (more are the call's to refuse)
             size = max(G.g4_kv4_prefill_workspace_size(p, self.B, T, self.max_len) for p in self.params)
-            if self._captured_ws:
+            if self._captured_ws or (self._by_address and self._capturing(stream)):
                 self._kept_ws.append(self._prefill_ws)
+            elif self._by_address and self._prefill_T > 0:
+                self._wait_for_all()
             self._prefill_ws, self._prefill_T, self._captured_ws = self._no_ws, 0, False  # (gone before the next is taken)
             with self._on(stream):
                 self._prefill_ws = self._new(torch.empty(size, dtype=torch.uint8, device=self.device))

@@ -135,3 +135,27 @@ def test_a_stack_that_goes_before_its_work_is_done():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert all(bool((x == 255).all()) for x in others)
+
+
+def test_a_workspace_outgrown_while_a_stream_known_by_address_uses_it():
+    """A longer prefill on the current stream replaces the workspace that a side stream, given by its address, is
+    still to write: what is taken after that is not written to."""
+    l, T = 1, 30
+    data, w = rows(T, 128, 1), W.norm_weight(128, 4).to(DEV)
+    st = S.PagedAttnStack(CFG, max_len=160, n_blocks=26, block_size=32, device=DEV)
+    st.assign(i32([T] * CFG["B"]), T)
+    q_out, out, late = (torch.empty_like(data[0]) for _ in range(3))
+    st.append(l, *data, w, w, T, q_out)
+    st.prefill_attn(l, q_out, T, out)
+    size = st._prefill_ws.numel()
+    long = torch.zeros((CFG["B"], 120, CFG["H"], 128), dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    st.prefill_attn(l, q_out, T, late, stream=side.cuda_stream)
+    st.prefill_attn(l, long, 120, long)
+    others = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(late, out)
+    assert all(bool((x == 255).all()) for x in others)

@@ -156,3 +156,21 @@ def test_prefills_of_no_or_too_many_tokens_leave_the_workspace(calls):
     for T in (5, 9, 30, st.max_len):
         ws, size = prefill(st, T, calls)
         assert ws.numel() >= size >= need(st, T)
+
+
+def test_an_outgrown_workspace_of_a_stream_known_by_address(calls, monkeypatch):
+    """Nothing tells when such a stream is done with it: it goes after the device has caught up, or not at all
+    while a capture forbids waiting."""
+    st = make()
+    waits = []
+    monkeypatch.setattr(st, "_wait_for_all", lambda: waits.append(st._prefill_T))
+    q = torch.zeros((3, 90, 4, 128), dtype=torch.bfloat16)
+    for T in (5, 7):
+        st.prefill_attn(1, q[:, :T], T, q[:, :T])
+    assert not waits
+    st.prefill_attn(1, q[:, :5], 5, q[:, :5], stream=0x1000)
+    st.prefill_attn(1, q[:, :30], 30, q[:, :30])
+    assert waits == [7]
+    monkeypatch.setattr(st, "_capturing", lambda stream: True)
+    ws, _ = prefill(st, 40, calls)
+    assert waits == [7] and len(st._kept_ws) == 1 and st._kept_ws[0].data_ptr() != ws.data_ptr()
