@@ -53,9 +53,9 @@ cudaError_t launch_pdl(void (*kern)(Args), dim3 grid, unsigned block, size_t sme
 //   Bound by latency: lengths, free list and table are dependent reads, with
 // one cluster barrier between them; with many new tokens also by the
 // instructions that form positions and slots.  Measured: 64 sequences of a token
-// each 4.2 us (the host's call takes 5.4); 96 sequences of up to 2048 tokens (1.6 MB
-// of positions and slots) 6.4 us with a cluster of 16, 8.5 with 8, 12.6 with 4; rows of
-// 2047 tokens, which are not written four at a time, 7.3.
+// each 4.3 us (the host's call takes 5.4); 96 sequences of up to 2048 tokens (1.6 MB
+// of positions and slots) 6.6 us with a cluster of 16, 8.5 with 8, 12.5 with 4; rows of
+// 2047 tokens, which are not written four at a time, 7.4.
 
 // (512: 12.0 us against 9.3 in that case, when the largest cluster had 8 CTAs.)
 constexpr int kAssignThreads = 1024;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__
 
 cudaError_t launch_kv4_assign(const Kv4AssignArgs& a, cudaStream_t s) {
   // A CTA per 4096 positions (2048 or 8192: the same within 1 %) or 64 sequences
-  // (1000 that gain a token or end: 5.1 us against 11.3 with one CTA, 6.6 with one per
+  // (1000 that gain a token or end: 5.0 us against 11.3 with one CTA, 6.6 with one per
   // 256; one per 32 makes 64 of them 4.5 against 4.2), up to 16 (the largest cluster,
   // where one of them fits the device; 8 are always allowed).
   const cudaError_t e = set_smem_limit_once<kv4_assign_kernel>(kKv4MaxBatch * 16);

@@ -51,8 +51,8 @@
 //
 // Measured (device time, calls back to back; copy rate: 6.78 TB/s):
 //   head_dim 512, 8 heads, 2 kv heads, 4 sequences of 131072 keys (604 MB) 110.7 us,
-//     5.5 TB/s, 0.80 of a copy; every product left out: 101 us, so the copies in
-//     flight (3 CTAs of 3 x 18 KB per SM) bound it;
+//     5.5 TB/s, 0.80 of a copy; every product left out: 101 us, so the copies (3
+//     CTAs of 3 x 18 KB per SM, issued again at the CTA's barrier) bound it;
 //   the same, 64 sequences of 1024 to 8192 keys (340 MB) 70.5 us, 0.71 of a copy:
 //     the start (lengths, block ids, first copies) and the merges take 8 us;
 //   head_dim 256, window 512, 64 sequences (19 MB) 13.2 us; head_dim 128, one of 333
