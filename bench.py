@@ -53,8 +53,8 @@ DECODE_EVENT_STEPS = (0, 32, 64, 96, 127)
 # own size.  Each figure carries the kernel's source files and the first 16
 # hex digits of their SHA-256 at the capture: once the sources differ, the
 # counters describe another kernel and the figure is not reported.
-PREFILL_SOURCES = ("g4_prefill_tc.cu", "g4_device.cuh", "g4_internal.h")
-DECODE_SOURCES = ("g4_attn_simt.cu", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
+PREFILL_SOURCES = ("g4_prefill_tc.cuh", "g4_device.cuh", "g4_internal.h")
+DECODE_SOURCES = ("g4_attn_simt.cuh", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
 WIN_SOURCES = ("g4_decode_win.cu", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
 GEMM_SOURCES = ("g4_gemm_tc.cu", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
 PROFILED_TRAFFIC = {

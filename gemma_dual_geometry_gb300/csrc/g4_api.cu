@@ -991,6 +991,289 @@ g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* 
   return cuda_status(g4::launch_prefill_tc(a, s), "tcgen05 prefill launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+// The mods of a call, checked against the layer; *m is `given` or, for none, all zeros.
+g4_status check_mods(const g4_layer_params* p, const g4_score_mods* given, g4_score_mods* m) {
+  memset(m, 0, sizeof(*m));
+  if (given == nullptr) return G4_OK;
+  *m = *given;
+  if (m->softcap != 0.0f && !(m->softcap >= 0x1.0p-10f && m->softcap <= 0x1.0p10f))
+    return fail(G4_ERR_UNSUPPORTED, "softcap %g is neither 0 nor in [2^-10, 2^10]", static_cast<double>(m->softcap));
+  if ((reinterpret_cast<uintptr_t>(m->slopes) | reinterpret_cast<uintptr_t>(m->key_begin) |
+       reinterpret_cast<uintptr_t>(m->key_end)) & 3u)
+    return fail(G4_ERR_INVALID_ARG, "slopes, key_begin and key_end must be 4-byte aligned");
+  if (m->softcap != 0.0f && !isfinite(p->attn_scale * 2.8853900817779268f / m->softcap))
+    return fail(G4_ERR_UNSUPPORTED, "attn_scale %g is too large for softcap %g", static_cast<double>(p->attn_scale),
+                static_cast<double>(m->softcap));
+  return G4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+g4_status g4_attn_visible_ranges(int32_t window, const int32_t* q_start_pos, const int32_t* seq_lens,
+                                 const int32_t* doc_ids, const int32_t* span_ids, int32_t max_len, int32_t B, int32_t T,
+                                 int32_t* key_begin, int32_t* key_end, void* stream) {
+  if (B < 0 || T < 0 || window < 0) return fail(G4_ERR_INVALID_ARG, "B %d, T %d and window %d must be >= 0", B, T, window);
+  if (max_len < 1) return fail(G4_ERR_INVALID_ARG, "max_len %d must be >= 1", max_len);
+  if (max_len > 1 << 24) return fail(G4_ERR_UNSUPPORTED, "max_len %d exceeds 2^24", max_len);
+  if (B > 1 << 20) return fail(G4_ERR_UNSUPPORTED, "B %d exceeds 2^20", B);
+  if (static_cast<long long>(B) * T > 0x7fffffffLL) return fail(G4_ERR_INVALID_ARG, "B * T exceeds 2^31 - 1");
+  if (q_start_pos == nullptr || seq_lens == nullptr || key_begin == nullptr || key_end == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q_start_pos, seq_lens, key_begin and key_end must be non-NULL");
+  if (B == 0 || T == 0) return ok();
+  g4::RangesArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q_start = q_start_pos;
+  a.lens = seq_lens;
+  a.doc = doc_ids;
+  a.span = span_ids;
+  a.begin = key_begin;
+  a.end = key_end;
+  a.B = B;
+  a.T = T;
+  a.max_len = max_len;
+  a.window = window;
+  return cuda_status(g4::launch_ranges(a, static_cast<cudaStream_t>(stream)), "visible ranges launch");
+}
+
+g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
+                                     int32_t layer, const g4_rope_axes* axes, const void* q_in, const void* k_in,
+                                     const void* v_in, const float* q_norm_w, const float* k_norm_w,
+                                     const int32_t* positions, const int32_t* rows, int32_t B, int32_t T, void* q_out,
+                                     void* stream) {
+  g4_status st = check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0 || T < 0) return fail(G4_ERR_INVALID_ARG, "B %d and T %d must be >= 0", B, T);
+  if (axes == nullptr || axes->axis == nullptr) return fail(G4_ERR_INVALID_ARG, "axes and their table must be non-NULL");
+  if (axes->n_axes < 1 || axes->n_axes > 4)
+    return fail(G4_ERR_UNSUPPORTED, "%d axes not supported (1 to 4)", axes->n_axes);
+  if (q_in == nullptr || q_out == nullptr || q_norm_w == nullptr || positions == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q_in, q_out, q_norm_w and positions must be non-NULL");
+  if (!aligned16(q_in) || !aligned16(q_out) || !aligned16(q_norm_w))
+    return fail(G4_ERR_INVALID_ARG, "q_in, q_out and q_norm_w must be 16-byte aligned");
+  const bool shared = params->kv_share_src >= 0;
+  g4::AxesAppendArgs a;
+  memset(&a, 0, sizeof(a));
+  if (shared) {
+    if (k_in != nullptr || v_in != nullptr || k_norm_w != nullptr)
+      return fail(G4_ERR_INVALID_ARG, "layer %d shares the cache of layer %d: k_in, v_in and k_norm_w must be NULL",
+                  layer, params->kv_share_src);
+    if (layer < 0 || layer >= n_layers) return fail(G4_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, n_layers);
+  } else {
+    if (k_in == nullptr || v_in == nullptr || k_norm_w == nullptr || rows == nullptr)
+      return fail(G4_ERR_INVALID_ARG, "layer %d owns its cache: k_in, v_in, k_norm_w and rows must be non-NULL", layer);
+    if (!aligned16(k_in) || !aligned16(v_in) || !aligned16(k_norm_w))
+      return fail(G4_ERR_INVALID_ARG, "k_in, v_in and k_norm_w must be 16-byte aligned");
+    const g4_kv_cache* c = nullptr;
+    st = resolve_src(params, caches, n_layers, layer, &c);
+    if (st != G4_OK) return st;
+    if (c->batch < B) return fail(G4_ERR_CAPACITY, "cache batch %d < B %d", c->batch, B);
+    a.cache_k = c->k;
+    a.cache_v = c->v;
+    a.max_len = c->max_len;
+    a.ring = c->ring;
+    a.k_in = k_in;
+    a.v_in = v_in;
+    a.k_w = k_norm_w;
+    a.rows = rows;
+  }
+  const long long tokens = static_cast<long long>(B) * T;
+  if (tokens > 0x7fffffffLL) return fail(G4_ERR_INVALID_ARG, "B * T exceeds 2^31 - 1");
+  rope_table(params, &a.n_rot, a.inv_freq);
+  for (int j = 0; j < a.n_rot; ++j) {
+    if (axes->axis[j] >= axes->n_axes)
+      return fail(G4_ERR_INVALID_ARG, "pair %d is turned by axis %d of %d", j, axes->axis[j], axes->n_axes);
+    a.axis[j] = axes->axis[j];
+    if (axes->inv_freq != nullptr) {
+      if (!(axes->inv_freq[j] >= 0.0f && axes->inv_freq[j] <= 1.0f))
+        return fail(G4_ERR_INVALID_ARG, "inv_freq of pair %d outside [0, 1]", j);
+      a.inv_freq[j] = axes->inv_freq[j];
+    }
+  }
+  if (tokens == 0) return ok();
+  a.n_axes = axes->n_axes;
+  a.q_in = q_in;
+  a.q_w = q_norm_w;
+  a.positions = positions;
+  a.q_out = q_out;
+  a.B = B;
+  a.T = T;
+  a.H = params->n_heads;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.eps = params->eps;
+  // Tokens and rows per CTA as in g4_kv4_append_normrope.
+  const int nrows = a.H + (shared ? 0 : 2 * a.Hkv);
+  a.tok_per_cta = T >= 16 ? (B < g4::kAppendMaxTokens ? B : g4::kAppendMaxTokens) : 1;
+  const long long ctas = static_cast<long long>(T) * ((B + a.tok_per_cta - 1) / a.tok_per_cta);
+  a.rows_per_cta = ctas >= 1024 ? nrows : 4;
+  return cuda_status(g4::launch_append_axes(a, params->dtype, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+g4_status g4_attn_prefill_mods(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
+                               int32_t layer, const g4_score_mods* mods, const void* q, const int32_t* q_start_pos,
+                               int32_t B, int32_t T, void* out, void* stream) {
+  g4_status st = check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0 || T < 0) return fail(G4_ERR_INVALID_ARG, "B %d and T %d must be >= 0", B, T);
+  if (q == nullptr || out == nullptr || q_start_pos == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q, out and q_start_pos must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(G4_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  g4_score_mods m;
+  st = check_mods(params, mods, &m);
+  if (st != G4_OK) return st;
+  const g4_kv_cache* c = nullptr;
+  st = resolve_src(params, caches, n_layers, layer, &c);
+  if (st != G4_OK) return st;
+  if (c->batch < B) return fail(G4_ERR_CAPACITY, "cache batch %d < B %d", c->batch, B);
+  if (c->ring) {
+    // As in g4_attn_prefill; intervals of the caller's own may begin where they like.
+    if (T > c->max_len || (m.key_begin == nullptr && static_cast<long long>(T) + params->window - 1 > c->max_len))
+      return fail(G4_ERR_CAPACITY, "ring cache of %d rows cannot hold the %d + %d - 1 keys a chunk of T = %d needs",
+                  c->max_len, T, params->window, T);
+    if (params->dtype == G4_BF16 && c->max_len % 128 != 0)
+      return fail(G4_ERR_UNSUPPORTED, "bf16 prefill on a ring cache needs max_len a multiple of 128 (got %d)",
+                  c->max_len);
+  } else if (T > c->max_len) {
+    return fail(G4_ERR_CAPACITY, "T %d exceeds the cache length %d", T, c->max_len);
+  }
+  if (B == 0 || T == 0) return ok();
+  int* err = device_error_ptr();
+  if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
+  const float scale_log2 = params->attn_scale * 1.4426950408889634f;
+  const float cap_log2 = m.softcap * 1.4426950408889634f;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (params->dtype == G4_BF16) {
+    g4::ModsTcArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.ck = c->k;
+    a.cv = c->v;
+    a.out = out;
+    a.q_start = q_start_pos;
+    a.err = err;
+    a.B = B;
+    a.T = T;
+    a.H = params->n_heads;
+    a.Hkv = params->n_kv_heads;
+    a.hd = params->head_dim;
+    a.max_len = c->max_len;
+    a.ring = c->ring;
+    a.sliding = params->layer_type == G4_SLIDING;
+    a.window = params->window;
+    a.scale_log2 = scale_log2;
+    a.cap_log2 = cap_log2;
+    a.cap_in = m.softcap != 0.0f ? 2.0f * scale_log2 / m.softcap : 0.0f;
+    a.slopes = m.slopes;
+    a.key_begin = m.key_begin;
+    a.key_end = m.key_end;
+    return cuda_status(g4::launch_prefill_mods(a, s), "tcgen05 prefill launch");
+  }
+  g4::ModsSimtArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.ck = c->k;
+  a.cv = c->v;
+  a.out = out;
+  a.base = q_start_pos;
+  a.err = err;
+  a.mode = 1;
+  a.B = B;
+  a.T = T;
+  a.H = params->n_heads;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.max_len = c->max_len;
+  a.ring = c->ring;
+  a.sliding = params->layer_type == G4_SLIDING;
+  a.window = params->window;
+  a.len_cap = c->max_len;
+  a.chunk = c->max_len;  // one split holds any interval
+  a.nsplit = 1;
+  a.scale_log2 = scale_log2;
+  a.cap_log2 = cap_log2;
+  a.slopes = m.slopes;
+  a.key_begin = m.key_begin;
+  a.key_end = m.key_end;
+  return cuda_status(g4::launch_attn_simt_mods(a, params->dtype, s), "float32 prefill launch");
+}
+
+size_t g4_attn_decode_mods_workspace_size(const g4_layer_params* params, int32_t B, int32_t max_seq_len) {
+  if (check_params(params) != G4_OK || B < 1 || max_seq_len < 1) return 0;
+  return g4::decode_plan(params->dtype, params->layer_type == G4_SLIDING, params->window, params->head_dim,
+                         params->n_heads, params->n_kv_heads, B, max_seq_len, /*split_only=*/true)
+      .ws_bytes;
+}
+
+g4_status g4_attn_decode_mods(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
+                              int32_t layer, const g4_score_mods* mods, const void* q, const int32_t* seq_lens,
+                              int32_t B, int32_t max_seq_len, void* out, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  g4_status st = check_params(params);
+  if (st != G4_OK) return st;
+  if (B < 0) return fail(G4_ERR_INVALID_ARG, "B %d must be >= 0", B);
+  if (q == nullptr || out == nullptr || seq_lens == nullptr)
+    return fail(G4_ERR_INVALID_ARG, "q, out and seq_lens must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(G4_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  g4_score_mods m;
+  st = check_mods(params, mods, &m);
+  if (st != G4_OK) return st;
+  if (m.key_end != nullptr) return fail(G4_ERR_INVALID_ARG, "the new token is its sequence's last key: key_end must be NULL");
+  const g4_kv_cache* c = nullptr;
+  st = resolve_src(params, caches, n_layers, layer, &c);
+  if (st != G4_OK) return st;
+  if (c->batch < B) return fail(G4_ERR_CAPACITY, "cache batch %d < B %d", c->batch, B);
+  if (max_seq_len < 1 || (!c->ring && max_seq_len > c->max_len))
+    return fail(G4_ERR_CAPACITY, "max_seq_len %d outside [1, cache length %d]", max_seq_len, c->max_len);
+  if (B == 0) return ok();
+  const g4::DecodePlan plan = g4::decode_plan(params->dtype, params->layer_type == G4_SLIDING, params->window,
+                                              params->head_dim, params->n_heads, params->n_kv_heads, B, max_seq_len,
+                                              /*split_only=*/true);
+  if (workspace_bytes < plan.ws_bytes)
+    return fail(G4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
+  if (plan.ws_bytes > 0 && (workspace == nullptr || !aligned16(workspace)))
+    return fail(G4_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
+  int* err = device_error_ptr();
+  if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
+  g4::ModsSimtArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.ck = c->k;
+  a.cv = c->v;
+  a.out = out;
+  a.base = seq_lens;
+  a.err = err;
+  a.B = B;
+  a.T = 1;
+  a.H = params->n_heads;
+  a.Hkv = params->n_kv_heads;
+  a.hd = params->head_dim;
+  a.max_len = c->max_len;
+  a.ring = c->ring;
+  a.sliding = params->layer_type == G4_SLIDING;
+  a.window = params->window;
+  a.len_cap = max_seq_len;
+  a.chunk = plan.chunk;
+  a.nsplit = plan.nsplit;
+  a.scale_log2 = params->attn_scale * 1.4426950408889634f;
+  a.cap_log2 = m.softcap * 1.4426950408889634f;
+  a.slopes = m.slopes;
+  a.key_begin = m.key_begin;
+  if (plan.nsplit > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.ws_o = reinterpret_cast<float*>(ws);
+    a.ws_m = reinterpret_cast<float*>(ws + plan.o_bytes);
+    a.ws_l = reinterpret_cast<float*>(ws + plan.o_bytes + plan.m_bytes);
+    a.tickets = reinterpret_cast<unsigned*>(ws + plan.o_bytes + 2 * plan.m_bytes);
+  }
+  return cuda_status(g4::launch_attn_simt_mods(a, params->dtype, static_cast<cudaStream_t>(stream)), "decode launch");
+}
+
 const char* g4_last_error(void) { return g_last_error.c_str(); }
 
 int32_t g4_take_device_error(void) {

@@ -87,6 +87,27 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s);
 
+// The same with positions of several axes, apart from the cache's rows; tok_per_cta at most
+// kAppendMaxTokens (g4_kv4_internal.h).
+struct AxesAppendArgs : AppendArgs {
+  const int32_t* rows;   // [B*T] position in the cache (positions: [n_axes][B*T]); null on a shared layer
+  int n_axes;
+  uint8_t axis[kMaxHalf];  // axis of pair j
+};
+cudaError_t launch_append_axes(const AxesAppendArgs& a, int dtype, cudaStream_t s);
+
+// The intervals of keys that tokens see (g4_attn_visible_ranges).
+struct RangesArgs {
+  const int32_t* q_start;
+  const int32_t* lens;
+  const int32_t* doc;   // [B][max_len] or null
+  const int32_t* span;
+  int32_t* begin;       // [B][T]
+  int32_t* end;
+  int B, T, max_len, window;
+};
+cudaError_t launch_ranges(const RangesArgs& a, cudaStream_t s);
+
 // Steps a5 (float32) and a6: split-KV softmax attention on CUDA cores.
 // mode 0 (decode): one query per sequence at position base[b] - 1, keys
 //   [kstart, base[b]); mode 1 (prefill): query t at position base[b] + t;
@@ -130,6 +151,15 @@ struct AttnSimtArgs {
 };
 cudaError_t launch_attn_simt(const AttnSimtArgs& a, int dtype, cudaStream_t s);
 
+// The same with modified scores, modes 0 and 1, not fused (include/g4attn.h, g4_score_mods).
+struct ModsSimtArgs : AttnSimtArgs {
+  float cap_log2;   // softcap * log2(e), 0: no cap
+  const float* slopes;
+  const int32_t* key_begin;  // [B][T]
+  const int32_t* key_end;
+};
+cudaError_t launch_attn_simt_mods(const ModsSimtArgs& a, int dtype, cudaStream_t s);
+
 // Step a5 (bf16): tcgen05 flash prefill.
 struct PrefillTcArgs {
   const void* q;     // [B][T][H][hd] bf16
@@ -147,6 +177,18 @@ struct PrefillTcArgs {
   unsigned* item_ctr;  // [2]: next work item, CTAs done (zero between launches; set by the launcher)
 };
 cudaError_t launch_prefill_tc(const PrefillTcArgs& a, cudaStream_t s);
+// The next pair of work-item counters, for a launch of the prefill kernel.
+cudaError_t take_prefill_counters(unsigned** ctr);
+
+// The same with modified scores (include/g4attn.h, g4_score_mods); bidir unused.
+struct ModsTcArgs : PrefillTcArgs {
+  float cap_log2;  // softcap * log2(e), 0: no cap
+  float cap_in;    // capped: e^(2 s / softcap) = 2^(cap_in q.k)
+  const float* slopes;
+  const int32_t* key_begin;  // [B][T]
+  const int32_t* key_end;
+};
+cudaError_t launch_prefill_mods(const ModsTcArgs& a, cudaStream_t s);
 
 // Step a6 (bf16) for key spans of at most kMaxWinSplits x 64 keys per
 // (sequence, kv head): one cluster of 64-key CTAs per (sequence, kv head),
@@ -201,7 +243,9 @@ struct DecodePlan {
   size_t o_bytes, m_bytes, t_bytes;  // sizes of the four regions (ws_m and ws_l share m_bytes)
   size_t ws_bytes;
 };
-DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len);
+// split_only: never win.
+DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len,
+                       bool split_only = false);
 int sm_count();  // SMs of the current device
 
 }  // namespace g4

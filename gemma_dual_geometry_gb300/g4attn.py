@@ -47,6 +47,16 @@ class G4KV4Pool(ctypes.Structure):
                 ("k_exp", ctypes.c_int32)]
 
 
+class G4ScoreMods(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("key_begin", ctypes.c_void_p),
+                ("key_end", ctypes.c_void_p)]
+
+
+class G4RopeAxes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("axis", ctypes.POINTER(ctypes.c_uint8)),
+                ("inv_freq", ctypes.POINTER(ctypes.c_float))]
+
+
 _P = ctypes.POINTER
 # Every function include/g4attn.h declares, with its ctypes signature.
 SIGNATURES = {
@@ -81,6 +91,14 @@ SIGNATURES = {
     "g4_kv4_attn_prefill": (_i32, [_P(G4LayerParams), _P(G4KV4Pool), _i32, _i32, _c_void_p, _c_void_p, _i32,
                                    _c_void_p, _c_void_p, _i32, _i32, _i32, _c_void_p, _c_void_p, ctypes.c_size_t,
                                    _c_void_p]),
+    "g4_attn_visible_ranges": (_i32, [_i32] + [_c_void_p] * 4 + [_i32] * 3 + [_c_void_p] * 3),
+    "g4_kv_append_normrope_axes": (_i32, [_P(G4LayerParams), _P(G4KVCache), _i32, _i32, _P(G4RopeAxes)] + [_c_void_p] * 7
+                                   + [_i32, _i32, _c_void_p, _c_void_p]),
+    "g4_attn_prefill_mods": (_i32, [_P(G4LayerParams), _P(G4KVCache), _i32, _i32, _P(G4ScoreMods), _c_void_p, _c_void_p,
+                                    _i32, _i32, _c_void_p, _c_void_p]),
+    "g4_attn_decode_mods_workspace_size": (ctypes.c_size_t, [_P(G4LayerParams), _i32, _i32]),
+    "g4_attn_decode_mods": (_i32, [_P(G4LayerParams), _P(G4KVCache), _i32, _i32, _P(G4ScoreMods), _c_void_p, _c_void_p,
+                                   _i32, _i32, _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
     "g4_last_error": (ctypes.c_char_p, []),
     "g4_take_device_error": (_i32, []),
 }
@@ -299,6 +317,66 @@ def g4_kv4_attn_prefill(params, pools, layer, q, block_table, max_blocks, q_star
     _check(lib().g4_kv4_attn_prefill(ctypes.byref(params), pools, len(pools), layer, _ptr(q), _ptr(block_table),
                                      max_blocks, _ptr(q_start_pos), _ptr(seq_lens), B, T, max_seq_len, _ptr(out),
                                      _ptr(workspace), int(workspace_bytes), _stream(stream, q)))
+
+
+def score_mods(softcap=0.0, slopes=None, key_begin=None, key_end=None):
+    """What is done to a layer's scores (g4_score_mods).  Holds on to the tensors that it is made of."""
+    for t, dtype in ((slopes, "float32"), (key_begin, "int32"), (key_end, "int32")):
+        if t is not None and not isinstance(t, int) and (str(t.dtype) != "torch." + dtype or not t.is_contiguous()):
+            raise ValueError(f"expected a contiguous tensor of {dtype}, got one of {t.dtype}")
+    m = G4ScoreMods(float(softcap), _ptr(slopes), _ptr(key_begin), _ptr(key_end))
+    m.tensors = (slopes, key_begin, key_end)
+    return m
+
+
+def rope_axes(n_axes, axis, head_dim, inv_freq=None):
+    """Positions of several axes (g4_rope_axes): ``axis[j]`` turns pair j, ``inv_freq[j]`` is its frequency (None: the
+    layer's).  Both may stop at the last rotated pair."""
+    half = head_dim // 2
+    for given in (axis, inv_freq):
+        if given is not None and len(given) > half:
+            raise ValueError(f"{len(given)} pairs in a head of {half}")
+    table = (ctypes.c_uint8 * half)(*[int(x) for x in axis])
+    freq = None if inv_freq is None else (ctypes.c_float * half)(*[float(x) for x in inv_freq])
+    return G4RopeAxes(int(n_axes), ctypes.cast(table, _P(ctypes.c_uint8)),
+                      None if freq is None else ctypes.cast(freq, _P(ctypes.c_float)))
+
+
+def g4_attn_visible_ranges(window, q_start_pos, seq_lens, doc_ids, span_ids, max_len, B, T, key_begin, key_end,
+                           stream=None):
+    """The interval of keys that each token sees, from documents and spans."""
+    _check(lib().g4_attn_visible_ranges(window, _ptr(q_start_pos), _ptr(seq_lens), _ptr(doc_ids), _ptr(span_ids),
+                                        max_len, B, T, _ptr(key_begin), _ptr(key_end), _stream(stream, q_start_pos)))
+
+
+def g4_kv_append_normrope_axes(params, caches, layer, axes, q_in, k_in, v_in, q_norm_w, k_norm_w, positions, rows, B, T,
+                               q_out, stream=None):
+    """g4_kv_append_normrope with positions of several axes [n_axes][B][T], apart from the cache's rows [B][T]."""
+    _check(lib().g4_kv_append_normrope_axes(ctypes.byref(params), caches, len(caches), layer, ctypes.byref(axes),
+                                            _ptr(q_in), _ptr(k_in), _ptr(v_in), _ptr(q_norm_w), _ptr(k_norm_w),
+                                            _ptr(positions), _ptr(rows), B, T, _ptr(q_out), _stream(stream, q_in)))
+
+
+def _mods(mods):
+    return None if mods is None else ctypes.byref(mods)
+
+
+def g4_attn_prefill_mods(params, caches, layer, mods, q, q_start_pos, B, T, out, stream=None):
+    """g4_attn_prefill with modified scores (score_mods(), or None)."""
+    _check(lib().g4_attn_prefill_mods(ctypes.byref(params), caches, len(caches), layer, _mods(mods), _ptr(q),
+                                      _ptr(q_start_pos), B, T, _ptr(out), _stream(stream, q)))
+
+
+def g4_attn_decode_mods_workspace_size(params, B, max_seq_len):
+    return int(lib().g4_attn_decode_mods_workspace_size(ctypes.byref(params), B, max_seq_len))
+
+
+def g4_attn_decode_mods(params, caches, layer, mods, q, seq_lens, B, max_seq_len, out, workspace=None,
+                        workspace_bytes=0, stream=None):
+    """g4_attn_decode with modified scores (score_mods(), or None)."""
+    _check(lib().g4_attn_decode_mods(ctypes.byref(params), caches, len(caches), layer, _mods(mods), _ptr(q),
+                                     _ptr(seq_lens), B, max_seq_len, _ptr(out), _ptr(workspace), int(workspace_bytes),
+                                     _stream(stream, q)))
 
 
 def g4_last_error():

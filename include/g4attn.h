@@ -539,6 +539,124 @@ g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* 
                               int32_t max_seq_len, void* out, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* ------------------------------------------------------------------------
+ * Modified scores, intervals of keys, several position axes
+ *
+ * What prompts with images, rows packed of documents, padded batches and models
+ * with capped or distance-biased scores need of the calls above.  (The pages have
+ * no counterpart: these are calls of this library.)
+ */
+
+/*
+ * What is done to the scores of a layer.  With s = attn_scale q_i . k_j, in this
+ * order:
+ *   softcap    > 0: s becomes softcap tanh(s / softcap).  0: no cap.  Otherwise 2^-10
+ *              .. 2^10 (G4_ERR_UNSUPPORTED outside).
+ *   slopes     [n_heads] float32 device, or NULL: s -= slopes[h] |i - j| (a bias that
+ *              falls with distance in either direction).
+ *   key_begin, key_end  int32 device, or NULL: query t of sequence b sees the
+ *              positions key_begin[b][t] <= j < key_end[b][t] that the cache holds,
+ *              whatever the layer's type and window say; g4_attn_visible_ranges makes
+ *              both.  With key_begin NULL the interval begins where the layer's window
+ *              does (at 0 on a full layer), with key_end NULL it ends with the query's own position.  A
+ *              query whose interval is empty gets an output of zeros.
+ * The arrays belong to the caller and are read by the kernels.
+ */
+typedef struct {
+  float softcap;
+  const float* slopes;
+  const int32_t* key_begin;
+  const int32_t* key_end;
+} g4_score_mods;
+
+/*
+ * The interval of keys that each token sees, for g4_score_mods, from what a row
+ * of positions is made of.  Token t of sequence b is position p = q_start_pos[b] + t.
+ *   window       the sliding window of the layers that the intervals are for (>= 1), or
+ *                0 for full layers
+ *   q_start_pos  [B]
+ *   seq_lens     [B] positions held, the new tokens among them
+ *   doc_ids      [B][max_len] or NULL (one document): a document is a run of equal
+ *                ids of neighbouring positions.  A token sees nothing before its
+ *                document.  Below 0: padding, which sees nothing.
+ *   span_ids     [B][max_len] or NULL (none): a run of equal ids >= 0 within a document is a span
+ *                (an image, a prefix), whose tokens see all of it, in both directions and
+ *                past the window.  Below 0: an ordinary token.
+ *   max_len      row length of both, at most 2^24
+ *   key_begin, key_end  [B][T].  With D the document's first position and S .. E the
+ *                span's first and one past its last (at most seq_lens[b]):
+ *                  key_begin = max(D, p - window + 1), key_end = p + 1,
+ *                  in a span the smaller of that and S, and E.
+ *                Both 0 (nothing) for tokens with p < 0, p >= seq_lens[b] or
+ *                p >= max_len, and for padding.
+ * Ids at positions from seq_lens[b] on are not read.  One call serves all layers of
+ * the same window.
+ */
+g4_status g4_attn_visible_ranges(int32_t window, const int32_t* q_start_pos, const int32_t* seq_lens,
+                                 const int32_t* doc_ids, const int32_t* span_ids, int32_t max_len, int32_t B, int32_t T,
+                                 int32_t* key_begin, int32_t* key_end, void* stream);
+
+/*
+ * Positions of several axes (time, height and width of images and video).
+ *   n_axes    1 .. 4
+ *   axis      HOST [head_dim / 2]: the axis whose position turns pair j (pairs that
+ *             rotary_fraction leaves unrotated are not looked at)
+ *   inv_freq  HOST [head_dim / 2] or NULL: the frequency of pair j, 0 .. 1, instead of
+ *             theta^(-2j / head_dim)
+ * Both are read during the call.
+ */
+typedef struct {
+  int32_t n_axes;
+  const uint8_t* axis;
+  const float* inv_freq;
+} g4_rope_axes;
+
+/*
+ * g4_kv_append_normrope with positions of several axes, apart from the cache's:
+ *   positions  [n_axes][B][T] RoPE positions (any value)
+ *   rows       [B][T] the position that a token takes in the cache (NULL on a
+ *              shared layer): as `positions` there, negative ones and, on a linear
+ *              cache, those >= max_len are not written
+ * Other arguments, and what is stored, as there: where all axes of a token agree
+ * with its row, the same bits.
+ */
+g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
+                                     int32_t layer, const g4_rope_axes* axes, const void* q_in, const void* k_in,
+                                     const void* v_in, const float* q_norm_w, const float* k_norm_w,
+                                     const int32_t* positions, const int32_t* rows, int32_t B, int32_t T, void* q_out,
+                                     void* stream);
+
+/*
+ * g4_attn_prefill with modified scores (mods NULL: none).  Arguments, caches, limits on
+ * launches in flight and errors as there, with these differences:
+ *   - q_start_pos is clamped into [0, 2^31 - 1 - T].
+ *   - Positions at or past the end of every interval of 128 queries in a row (those of a
+ *     tile) may hold anything, as may those before all of them: a padded
+ *     batch's unwritten rows need no values.
+ *   - On a ring, positions that it no longer holds count as absent; with key_begin
+ *     NULL the window has to fit as there.
+ */
+g4_status g4_attn_prefill_mods(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
+                               int32_t layer, const g4_score_mods* mods, const void* q, const int32_t* q_start_pos,
+                               int32_t B, int32_t T, void* out, void* stream);
+
+/* Workspace bytes g4_attn_decode_mods needs (0: none). */
+size_t g4_attn_decode_mods_workspace_size(const g4_layer_params* params, int32_t B, int32_t max_seq_len);
+
+/*
+ * g4_attn_decode with modified scores (mods NULL: none): the single-token form.
+ * Arguments and workspace as there, with these differences:
+ *   - seq_lens is clamped into [0, max_seq_len].
+ *   - mods->key_begin is [B]: sequence b sees the keys [max(key_begin[b], its window's
+ *     first), seq_lens[b]), which is what g4_attn_visible_ranges gives for T = 1.  The
+ *     new token is the last key: key_end must be NULL (G4_ERR_INVALID_ARG).
+ *   - A sequence that sees no key gets an output of zeros.
+ */
+g4_status g4_attn_decode_mods(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
+                              int32_t layer, const g4_score_mods* mods, const void* q, const int32_t* seq_lens,
+                              int32_t B, int32_t max_seq_len, void* out, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Thread-local message of the last non-OK status ("" if none). */
 const char* g4_last_error(void);
 
