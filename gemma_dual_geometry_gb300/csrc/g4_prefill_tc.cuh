@@ -26,7 +26,7 @@
 // after another from a global counter (the producer draws them and passes
 // them on through a 4-entry queue in shared memory), with its barriers, ring and TMEM
 // running on from item to item, so the next item's Q and first K parts load
-// while the current one finishes.  Warp roles (320 threads):
+// while the current one finishes.  Warp roles (320 threads, MODS 576):
 //   warp 0      TMA producer (converged; one elected lane issues): the Q
 //               tile, then K parts (128 keys x 64..256 dims) and V parts
 //               (64..128 keys x DV dims) as 5-D boxes, one request per
@@ -41,7 +41,7 @@
 //                                        TMEM, B = V_j MN-major)
 //               in the order QK_0, QK_1, PV_0, QK_2, PV_1, ... so the score
 //               MMA of the next tile overlaps the softmax of this one.
-//   warps 2-9   softmax: two warps per TMEM lane quarter (a warp may only
+//   warps 2-9   softmax (MODS: 2-17, quarters of a row instead of halves): two warps per TMEM lane quarter (a warp may only
 //               touch its quarter's 32 lanes), each thread half a query row
 //               (64 of the 128 score columns; TMEM lane = row): load the
 //               whole S row with tcgen05.ld (both threads of a row find the
@@ -84,7 +84,13 @@ constexpr int kCausal = 0, kBidir = 1, kMods = 2;
 constexpr int kBM = 128;       // query rows per CTA
 constexpr int kBN = 128;       // keys per tile
 constexpr int kChunkB = 16384;  // 128 rows x 64 bf16, one 128-byte-swizzled block
-constexpr int kThreads = 320;  // 10 warps
+// Softmax warps, beside the producer and the MMA issuer.  MODS: twice as many, each thread a quarter of a row, and a
+// warp that stores the output.
+template <int MODE>
+constexpr int kSoftWarps = MODE == kMods ? 16 : 8;
+template <int MODE>
+constexpr int kThreads = 64 + 32 * kSoftWarps<MODE> + (MODE == kMods ? 32 : 0);
+constexpr int kModsParts = kSoftWarps<kMods> / 4;  // parts of a row's columns
 constexpr int kMaxSlots = 12;
 constexpr int kSmemMax = 232448;  // opt-in shared memory per block
 // The exponent base of a row is raised only when a tile's maximum exceeds it
@@ -130,11 +136,16 @@ struct TcBars {
   uint64_t q_full;     // the current item's Q tile has landed (one phase per item)
   uint64_t q_free;     // every QK MMA of the current item is complete (Q may be replaced)
   uint64_t s_full[2];  // QK_j complete (tile parity)
-  uint64_t p_full[2];  // P_j written to TMEM by all 128 softmax threads
+  uint64_t p_full[2];  // P_j written to TMEM by all softmax threads
   uint64_t o_done[2];  // PV_j complete
   uint64_t drain;
   uint64_t sum_full[4];  // [lane quarter]: both row-sum shares written
-  uint64_t s_read[4];    // [lane quarter]: both warps have S_j in registers (P_j may overwrite it)
+  uint64_t s_read[4];    // [lane quarter]: its warps have S_j in registers (P_j may overwrite it)
+  // MODS:
+  uint64_t x_full[4];    // [lane quarter]: its warps have written their parts of an exchange
+  uint64_t x_free[4];    // [lane quarter]: and read those of all
+  uint64_t o_staged;     // the item's output is in its ring slots
+  uint64_t o_taken;      // the storing warp has seen that
   uint64_t full[kMaxSlots];
   uint64_t empty[kMaxSlots];
   uint64_t it_full[4];   // work-item queue entry written (by the producer)
@@ -143,9 +154,8 @@ struct TcBars {
   int kbeg[4], kend[4];  // MODS: the keys that some row of the item sees, [kbeg, kend)
   uint32_t tmem_base;
   int abort;
-  // [0][column half][row]: row-sum shares.  MODS: [tile parity][column half][row] maxima of the half's scores, the
-  // row-sum shares at the end in those of the parity that the last tile has not used.
-  float red[2][2][kBM];
+  alignas(16) int raise[2][4][kModsParts];  // MODS: [tile parity][lane quarter][part]: number of the tile whose maximum it wants raised
+  float red[kModsParts][kBM];   // [part of the columns][row]: row-sum shares; MODS: row maxima too
 };
 static_assert(sizeof(TcBars) <= 3072, "barrier block");
 
@@ -162,25 +172,6 @@ __device__ __forceinline__ bool softmax_sync_any(int flag) {
       : "r"(flag)
       : "memory");
   return any != 0;
-}
-
-// MODS: N raw scores q.k of the keys from k0 on become scores in log2 units, capped (CAP: c tanh(s / c) with
-// tanh(y) = 1 - 2 / (1 + e^2y), off by about 2^-22) and biased (BIAS) as asked.
-template <int N, bool CAP, bool BIAS>
-__device__ __forceinline__ void modify_scores(float (&s)[N], const ModsTcArgs& a, float slope, int qpos, int k0) {
-  [[maybe_unused]] const float apart = static_cast<float>(qpos - k0);
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    if constexpr (CAP) {
-      const float u = ex2_approx(s[n] * a.cap_in);  // (infinite: the reciprocal is 0 and the tanh 1)
-      float rcp;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(1.0f + u));
-      s[n] = fmaf(-2.0f * a.cap_log2, rcp, a.cap_log2);
-    } else {
-      s[n] *= a.scale_log2;
-    }
-    if constexpr (BIAS) s[n] = fmaf(-slope, fabsf(apart - static_cast<float>(n)), s[n]);
-  }
 }
 
 template <int MODE>
@@ -260,9 +251,341 @@ __device__ __forceinline__ TcItem tc_item(const Args& a, int it, int nqt) {
   return w;
 }
 
+// ---------------------------------------------------------------- MODS: softmax and output
+
+// Arrives for the warp once all of its lanes have come here.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+
+__device__ __forceinline__ int4 ld_shared_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.volatile.shared.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// The smaller one; NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Raw scores q.k of N keys become c tanh(s / c) in log2 units, with tanh(y) = 1 - 2 / (1 + e^2y), off by about 2^-22.
+// Four reciprocals are one of their product: a reciprocal takes the special-function unit as long as two exponentials
+// (capping costs a tile of 128 keys 970 cycles, 1430 with a reciprocal each).  e^2y is cut off at 2^30, where the tanh
+// is 1 in float32, so that the product stays finite; a NaN makes its neighbours NaN, which are the same row's.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&s)[N], float cap_in, float cap_log2) {
+  const float2 in2 = make_float2(cap_in, cap_in), one = make_float2(1.0f, 1.0f), cap2 = make_float2(cap_log2, cap_log2);
+  const float2 twice = make_float2(-2.0f * cap_log2, -2.0f * cap_log2);
+#pragma unroll
+  for (int n = 0; n < N; n += 4) {
+    const float2 x = __fmul2_rn(make_float2(s[n], s[n + 1]), in2), y = __fmul2_rn(make_float2(s[n + 2], s[n + 3]), in2);
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(min_nan(x.x, 30.0f)), ex2_approx(min_nan(x.y, 30.0f))), one);
+    const float2 e = __fadd2_rn(make_float2(ex2_approx(min_nan(y.x, 30.0f)), ex2_approx(min_nan(y.y, 30.0f))), one);
+    const float de = d.x * d.y, ee = e.x * e.y;
+    const float r = rcp_approx(de * ee);
+    const float rd = r * ee, re = r * de;  // 1 / (d.x d.y), 1 / (e.x e.y)
+    const float2 a = __ffma2_rn(__fmul2_rn(make_float2(rd, rd), make_float2(d.y, d.x)), twice, cap2);
+    const float2 b = __ffma2_rn(__fmul2_rn(make_float2(re, re), make_float2(e.y, e.x)), twice, cap2);
+    s[n] = a.x;
+    s[n + 1] = a.y;
+    s[n + 2] = b.x;
+    s[n + 3] = b.y;
+  }
+}
+
+// The softmax warps' work (16 warps; lane r of a quarter holds a row, four warps a quarter of its columns each).
+//   Item by item and tile by tile as in the causal kernel, from the last key tile to the first: a distance bias falls
+// from the diagonal on, so that the first tile's maximum is the largest and O need not be rescaled
+// (2 x 4096 tokens of head_dim 128 took 15 % longer in ascending order).
+//   A row's exponent base only has to be common to its parts and within 2^64 of the running maximum, so parts that
+// find their own maxima no further above the base go on without asking the others: the wish to raise the base
+// travels with the barrier that they need anyway, before P_j overwrites S_j, and only then do they exchange maxima.
+template <int HD, bool CAP, bool BIAS>
+__device__ __forceinline__ void softmax_mods(const ModsTcArgs& a, TcBars* bars, uint32_t tmem, uint32_t sRing, int nqt) {
+  using C = TcCfg<HD>;
+  constexpr int N = kBN / kModsParts;           // score columns per thread
+  constexpr int kDVP = C::DV / kModsParts;      // O columns per thread
+  constexpr int kCW = kDVP < 32 ? kDVP : 32;    // of which so many are loaded at once
+  constexpr int kParts = C::KPARTS + C::VPARTS;  // ring parts per key tile
+  static_assert(N == 32, "a part of S is one load");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3;       // TMEM lane quarter this warp may access
+  const int part = (warp - 2) >> 2;   // which quarter of the columns
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t tmem_O = tmem + 256 + lane_off + part * kDVP;
+  volatile int* abort = &bars->abort;
+
+  // All four parts of a row learn each other's number.
+  int xc = 0;
+  auto exchange = [&](float v, float (&all)[kModsParts]) -> bool {
+    if (xc > 0 && !warp_wait(smem_u32(&bars->x_free[quarter]), (xc - 1) & 1, a.err, abort)) return false;
+    bars->red[part][r] = v;
+    warp_arrive(&bars->x_full[quarter]);
+    if (!warp_wait(smem_u32(&bars->x_full[quarter]), xc & 1, a.err, abort)) return false;
+#pragma unroll
+    for (int i = 0; i < kModsParts; ++i) all[i] = bars->red[i][r];
+    warp_arrive(&bars->x_free[quarter]);
+    ++xc;
+    return true;
+  };
+
+  // Item n of the queue, with this row's keys and slope; false: none is left, or a wait gave up.
+  struct Next {
+    int qpos;             // the row's position
+    int kt_last, ntiles;  // the last key tile and how many there are
+    int2 keys;
+    float slope;
+    int it;
+  };
+  auto fetch = [&](int n, Next& x) -> bool {
+    const int e = n & 3;
+    if (!warp_wait(smem_u32(&bars->it_full[e]), (n >> 2) & 1, a.err, abort)) return false;
+    const int it = *reinterpret_cast<volatile int*>(&bars->items[e]);
+    const int kbeg = *reinterpret_cast<volatile int*>(&bars->kbeg[e]);
+    const int kend = *reinterpret_cast<volatile int*>(&bars->kend[e]);
+    warp_arrive(&bars->it_empty[e]);
+    if (it < 0) return false;
+    TcItem w = tc_item<C::NDH, kMods>(a, it, nqt);
+    tc_set_keys(w, kbeg, kend);
+    x.qpos = w.qpos_first + r;
+    x.kt_last = w.kt_begin + w.ntiles - 1;
+    x.ntiles = w.ntiles;
+    x.keys = tc_row_keys(a, w, r);
+    x.slope = BIAS ? a.slopes[w.h] * 1.4426950408889634f : 0.0f;
+    x.it = it;
+    return true;
+  };
+
+  int J = 0;      // tiles of earlier items
+  int nq = 0;     // items done that had any
+  int parts = 0;  // ring parts of earlier items
+  Next cur;
+  bool ok = fetch(0, cur);
+  for (int n = 0; ok; ++n) {
+    const int ntiles = cur.ntiles;
+    if (ntiles == 0) {
+      // no row sees a key
+      const TcItem w = tc_item<C::NDH, kMods>(a, cur.it, nqt);
+      if (r < w.valid_rows) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                             (((static_cast<size_t>(w.b) * a.T + w.q0 + r) * a.H + w.h) * HD + w.dh * C::DV + part * kDVP);
+#pragma unroll
+        for (int i = 0; i < kDVP / 8; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+      }
+      ok = fetch(n + 1, cur);
+      continue;
+    }
+    float m = -INFINITY;  // exponent base in log2 units
+    float l = 0.0f;       // this part's share of the row sum
+    for (int j = 0; j < ntiles; ++j) {
+      const int sb = (J + j) & 1;
+      if (!warp_wait(smem_u32(&bars->s_full[sb]), ((J + j) >> 1) & 1, a.err, abort)) { ok = false; break; }
+      tc_fence_after();
+      float s[N];
+      {
+        uint32_t raw[N];
+        tmem_ld32(tmem + lane_off + sb * kBN + part * N, raw);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = __uint_as_float(raw[i]);
+      }
+      const int k0 = (cur.kt_last - j) * kBN + part * N;  // this part's first key
+      const int lo = max(cur.keys.x - k0, 0), hi = min(cur.keys.y - k0, N);
+      const bool masked = lo > 0 || hi < N;
+      // bit i: key k0 + i is seen
+      const uint32_t seen = lo < hi ? (0xffffffffu << lo) & (0xffffffffu >> (N - hi)) : 0u;
+      if constexpr (CAP) {
+        if (masked) {  // (what nobody sees may be NaN)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (!(seen >> i & 1)) s[i] = 0.0f;
+        }
+        cap_scores(s, a.cap_in, a.cap_log2);
+      }
+      const float c2 = CAP ? 1.0f : a.scale_log2;
+      if constexpr (BIAS) {
+        const float slope = cur.slope, apart = static_cast<float>(cur.qpos - k0);
+        if (cur.qpos - k0 >= N - 1) {
+          // all keys at or before the query: c2 s - slope apart + slope i
+          const float2 c22 = make_float2(c2, c2), off = make_float2(-slope * apart, -slope * apart);
+          const float2 sl2 = make_float2(slope, slope);
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            float2 t = __ffma2_rn(make_float2(s[i], s[i + 1]), c22, off);
+            t = __ffma2_rn(sl2, make_float2(static_cast<float>(i), static_cast<float>(i + 1)), t);
+            s[i] = t.x;
+            s[i + 1] = t.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) s[i] = fmaf(-slope, fabsf(apart - static_cast<float>(i)), s[i] * c2);
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (!(seen >> i & 1)) s[i] = -INFINITY;
+      }
+      const float c3 = BIAS ? 1.0f : c2;  // what the scores are still multiplied by
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < N; i += 2) mx[i / 2 & 3] = fmaxf(mx[i / 2 & 3], fmaxf(s[i], s[i + 1]));
+      const float mp = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c3;
+      // (no base yet: any key raises it)
+      const bool raise = mp > (m == -INFINITY ? -INFINITY : m + kRescaleLog2);
+      if (__any_sync(0xffffffffu, raise) && lane == 0) bars->raise[sb][quarter][part] = J + j + 1;
+      warp_arrive(&bars->s_read[quarter]);
+
+      if (!warp_wait(smem_u32(&bars->s_read[quarter]), (J + j) & 1, a.err, abort)) { ok = false; break; }
+      static_assert(kModsParts == 4, "one load");
+      const int4 want = ld_shared_int4(smem_u32(bars->raise[sb][quarter]));
+      const int now = J + j + 1;
+      const bool raised = want.x == now || want.y == now || want.z == now || want.w == now;
+      if (raised) {  // (the same for all four warps)
+        float all[kModsParts];
+        if (!exchange(mp, all)) { ok = false; break; }
+        const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+        float alpha = 1.0f;
+        if (m == -INFINITY) {
+          m = mt;  // nothing accumulated yet (O's row is zero or unwritten)
+        } else if (mt - m > kRescaleLog2) {
+          alpha = ex2_approx(m - mt);
+          m = mt;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+          // A base is raised after a tile with a key (so j > 0): PV_{j-1} must be complete before O's rows are
+          // scaled; PV_j is not issued until P_j below is published.
+          if (!warp_wait(smem_u32(&bars->o_done[(J + j - 1) & 1]), ((J + j - 1) >> 1) & 1, a.err, abort)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < kDVP / kCW; ++cc) {
+            uint32_t o[kCW];
+            tmem_ld<kCW>(tmem_O + cc * kCW, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < kCW; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st<kCW>(tmem_O + cc * kCW, o);
+          }
+          tc_wait_st();
+        }
+        l *= alpha;
+      }
+      const float nb = m == -INFINITY ? 0.0f : -m;
+      const float2 c32 = make_float2(c3, c3), nb2 = make_float2(nb, nb);
+      uint32_t p[N / 2];
+      float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float2 t = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), c32, nb2);
+        p[i] = pack_bf16x2(ex2_approx(t.x), ex2_approx(t.y));
+        sum2[i & 1] = __fadd2_rn(sum2[i & 1], make_float2(bf16_lo(p[i]), bf16_hi(p[i])));
+      }
+      tmem_st16(tmem + lane_off + sb * kBN + part * (N / 2), p);
+      l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      tc_wait_st();
+      tc_fence_before();
+      warp_arrive(&bars->p_full[sb]);
+    }
+    if (!ok) break;
+    // The next item's keys are on their way while this one's output is finished.  (The producer has drawn it by now, or
+    // does without waiting for any of this item's weights.)
+    const bool more = fetch(n + 1, cur);
+    float all[kModsParts];
+    if (!exchange(l, all)) break;
+    l = (all[0] + all[1]) + (all[2] + all[3]);
+    // O / l as bf16, in the chunk-major 128-byte-swizzled layout of the output tensor map, into the ring slots of the
+    // item's last V parts (free once the last PV has completed).  Rows past T fall outside the map and are not written.
+    const int last_part = parts + ntiles * kParts - 1;  // ring sequence number
+    auto oslot = [&](int k) { return (last_part - (C::OSLOTS - 1) + k) % C::NSLOT; };
+    const int jl = J + ntiles - 1;
+    if (!warp_wait(smem_u32(&bars->o_done[jl & 1]), (jl >> 1) & 1, a.err, abort)) break;
+    tc_fence_after();
+    const float inv_l = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // (NaN stays)
+    constexpr int NCC = kDVP / kCW;
+    uint32_t o[NCC][kCW];
+#pragma unroll
+    for (int cc = 0; cc < NCC; ++cc) tmem_ld<kCW>(tmem_O + cc * kCW, o[cc]);
+    tc_wait_ld();
+#pragma unroll
+    for (int cc = 0; cc < NCC; ++cc) {
+      // kCW columns, half of a 64-column chunk or less: pieces (16 bytes) from p0 on
+      const int col = part * kDVP + cc * kCW;
+      const int ch = col / 64;
+      const uint32_t row_addr = sRing + oslot(ch / C::CPS) * C::SLOTB + (ch % C::CPS) * kChunkB + r * 128;
+      const int p0 = (col % 64) / 8;
+#pragma unroll
+      for (int i = 0; i < kCW / 8; ++i) {
+        uint32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = pack_bf16x2(__uint_as_float(o[cc][8 * i + 2 * k]) * inv_l, __uint_as_float(o[cc][8 * i + 2 * k + 1]) * inv_l);
+        const uint32_t addr = row_addr + (((p0 + i) ^ (r & 7)) * 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
+      }
+    }
+    fence_proxy_async_smem();
+    // (the storing warp has seen the item before: no phase is passed over)
+    if (nq > 0 && !warp_wait(smem_u32(&bars->o_taken), (nq - 1) & 1, a.err, abort)) break;
+    warp_arrive(&bars->o_staged);
+    J += ntiles;
+    parts += ntiles * kParts;
+    ++nq;
+    ok = more;
+  }
+}
+
+// The storing warp: the items' outputs go out from their ring slots, which are then free.
+template <int HD>
+__device__ __forceinline__ void store_mods(const ModsTcArgs& a, TcBars* bars, uint32_t sRing, int nqt, const CUtensorMap* tm_o) {
+  using C = TcCfg<HD>;
+  constexpr int kParts = C::KPARTS + C::VPARTS;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort = &bars->abort;
+  int nq = 0, parts = 0;
+  for (int n = 0;; ++n) {
+    const int e = n & 3;
+    if (!warp_wait(smem_u32(&bars->it_full[e]), (n >> 2) & 1, a.err, abort)) break;
+    const int it = *reinterpret_cast<volatile int*>(&bars->items[e]);
+    const int kbeg = *reinterpret_cast<volatile int*>(&bars->kbeg[e]);
+    const int kend = *reinterpret_cast<volatile int*>(&bars->kend[e]);
+    warp_arrive(&bars->it_empty[e]);
+    if (it < 0) break;
+    TcItem w = tc_item<C::NDH, kMods>(a, it, nqt);
+    tc_set_keys(w, kbeg, kend);
+    if (w.ntiles == 0) continue;
+    if (!warp_wait(smem_u32(&bars->o_staged), nq & 1, a.err, abort)) break;
+    const int last_part = parts + w.ntiles * kParts - 1;
+    auto oslot = [&](int k) { return (last_part - (C::OSLOTS - 1) + k) % C::NSLOT; };
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&bars->o_taken));
+#pragma unroll
+      for (int k = 0; k < C::OSLOTS; ++k)
+        tma_store_5d(tm_o, sRing + oslot(k) * C::SLOTB, 0, w.q0, w.dh * (C::DV / 64) + k * C::CPS, w.h, w.b);
+      bulk_commit_group();
+      bulk_wait_read_all();  // the slots must not be refilled before the stores have read them
+#pragma unroll
+      for (int k = 0; k < C::OSLOTS; ++k) mbar_arrive(smem_u32(&bars->empty[oslot(k)]));
+    }
+    __syncwarp();
+    parts += w.ntiles * kParts;
+    ++nq;
+  }
+}
+
 // (CAP and BIAS: with MODS, whether scores are capped and biased)
 template <int HD, int MODE, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<MODE>, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                       const __grid_constant__ TcArgsOf<MODE> a) {
@@ -296,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  pdl_wait();
+  if constexpr (!MODS) pdl_wait();  // (MODS: once the barriers are set up)
   pdl_trigger();
 
   const int nqt = (a.T + kBM - 1) / kBM;
@@ -307,21 +630,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&bars->q_free), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
-      mbar_init(smem_u32(&bars->p_full[i]), 256);
+      mbar_init(smem_u32(&bars->p_full[i]), MODS ? kSoftWarps<MODE> : 256);
       mbar_init(smem_u32(&bars->o_done[i]), 1);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     for (int qq = 0; qq < 4; ++qq) mbar_init(smem_u32(&bars->sum_full[qq]), 64);
-    for (int qq = 0; qq < 4; ++qq) mbar_init(smem_u32(&bars->s_read[qq]), 64);
+    for (int qq = 0; qq < 4; ++qq) mbar_init(smem_u32(&bars->s_read[qq]), MODS ? kModsParts : 64);
+    if constexpr (MODS) {
+      // (warps are counted, whose lane 0 arrives for them)
+      for (int qq = 0; qq < 4; ++qq) {
+        mbar_init(smem_u32(&bars->x_full[qq]), kModsParts);
+        mbar_init(smem_u32(&bars->x_free[qq]), kModsParts);
+      }
+      mbar_init(smem_u32(&bars->o_staged), kSoftWarps<MODE>);
+      mbar_init(smem_u32(&bars->o_taken), 1);
+      for (int i = 0; i < 2 * 4 * kModsParts; ++i) (&bars->raise[0][0][0])[i] = 0;
+    }
     for (int i = 0; i < C::NSLOT; ++i) mbar_init(smem_u32(&bars->full[i]), 1);
     for (int i = 0; i < C::NSLOT; ++i) mbar_init(smem_u32(&bars->empty[i]), 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->it_full[i]), 1);
-      mbar_init(smem_u32(&bars->it_empty[i]), 2);
+      mbar_init(smem_u32(&bars->it_empty[i]), MODS ? 2 + kSoftWarps<MODE> : 2);  // its readers
     }
     bars->abort = 0;
     fence_mbar_init();
   }
+  // (after the wait: TMEM taken while the launch before has yet to take its own could leave both waiting)
+  if constexpr (MODS) pdl_wait();
   if (warp == 1) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
@@ -363,9 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // next work item into queue entry n % 4 (once both readers are done with its last use)
         const int e = n & 3;
         if (n >= 4 && !warp_wait(smem_u32(&bars->it_empty[e]), ((n >> 2) - 1) & 1, a.err, abort)) break;
-        unsigned got = 0;
-        if (lane == 0) got = atomicAdd(a.item_ctr, 1u);
-        got = __shfl_sync(0xffffffffu, got, 0);
+        unsigned got = blockIdx.x;
+        if (!MODS || n > 0) {  // (MODS: a CTA's first item is its own, the counter gives out the others)
+          if (lane == 0) got = atomicAdd(a.item_ctr, 1u) + (MODS ? gridDim.x : 0u);
+          got = __shfl_sync(0xffffffffu, got, 0);
+        }
         const int it = got < static_cast<unsigned>(nitems) ? static_cast<int>(got) : -1;
         TcItem w;
         if constexpr (MODS) {
@@ -441,10 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             advance();
           }
         };
-        load_k(w.kt_begin);
+        auto tile = [&](int j) { return MODS ? w.kt_begin + w.ntiles - 1 - j : w.kt_begin + j; };
+        load_k(tile(0));
         for (int j = 0; j < w.ntiles && ok; ++j) {
-          if (j + 1 < w.ntiles) load_k(w.kt_begin + j + 1);
-          load_v(w.kt_begin + j);
+          if (j + 1 < w.ntiles) load_k(tile(j + 1));
+          load_v(tile(j));
         }
       }
       // Copies still in flight must land before the CTA may exit.
@@ -469,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K step only moves the start address (16-byte units in the low bits,
       // which stay below 2^14 for any shared-memory address).  Building them
       // per instruction costs the issue loop more cycles than the MMA.
+      const uint32_t lead = elect_one();  // (asked once: an elect per MMA costs the issue loop 1-3 %)
       const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(sRing, 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(sRing, C::VKP * 128, 1024);
@@ -524,10 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t bd = dk0 + soff;
 #pragma unroll
             for (int c = 0; c < C::CPP; ++c) {
-              tc_mma_ss_elect(dS, ad, bd, idesc_qk, (p2 > 0 || c > 0) ? 1u : 0u);
-              tc_mma_ss_elect(dS, ad + 2, bd + 2, idesc_qk, 1u);
-              tc_mma_ss_elect(dS, ad + 4, bd + 4, idesc_qk, 1u);
-              tc_mma_ss_elect(dS, ad + 6, bd + 6, idesc_qk, 1u);
+              tc_mma_ss_lead(lead, dS, ad, bd, idesc_qk, (p2 > 0 || c > 0) ? 1u : 0u);
+              tc_mma_ss_lead(lead, dS, ad + 2, bd + 2, idesc_qk, 1u);
+              tc_mma_ss_lead(lead, dS, ad + 4, bd + 4, idesc_qk, 1u);
+              tc_mma_ss_lead(lead, dS, ad + 6, bd + 6, idesc_qk, 1u);
               ad += kChunkB >> 4;
               bd += kChunkB >> 4;
             }
@@ -541,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sb = (J + j) & 1;
           if (!warp_wait(smem_u32(&bars->p_full[sb]), ((J + j) >> 1) & 1, a.err, abort)) { ok = false; return; }
           tc_fence_after();
-          const int kt = w.kt_begin + j;
+          const int kt = MODS ? w.kt_begin + w.ntiles - 1 - j : w.kt_begin + j;
           uint32_t ta = tmem + sb * kBN;  // P_j: 128 keys as 64 packed columns
           const bool last = j == w.ntiles - 1;
 #pragma unroll 1
@@ -551,38 +890,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (even NaN, and 0 * NaN = NaN); zero them before they meet P
             // (only in the part holding the end of the keys).
             const int key0 = kt * kBN + p2 * C::VKP;
-            if (key0 + C::VKP > w.Lk) {
-              const int nvalid = max(0, w.Lk - key0);
-              uint8_t* slot_ptr = smem + C::RING_OFF + slot * C::SLOTB;
-              const int nbad = C::VKP - nvalid;
-              for (int i = lane; i < (C::DV / 64) * nbad * 8; i += 32) {
-                const int dc = i / (nbad * 8);
-                const int rr = (i / 8) % nbad + nvalid;
-                const int pc = i % 8;
-                *reinterpret_cast<uint4*>(slot_ptr + dc * C::VKP * 128 + rr * 128 + pc * 16) = make_uint4(0, 0, 0, 0);
-              }
+            // A 64-column chunk of a part is 128 bytes per key, key after key (the swizzle stays within a key's).
+            auto zero_keys = [&](int first, int count) {
+              uint8_t* from = smem + C::RING_OFF + slot * C::SLOTB + first * 128;
+#pragma unroll
+              for (int dc = 0; dc < C::DV / 64; ++dc)
+                for (int i = lane * 16; i < count * 128; i += 512)
+                  *reinterpret_cast<uint4*>(from + dc * C::VKP * 128 + i) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
               __syncwarp();
+            };
+            if (key0 + C::VKP > w.Lk) {
+              const int nvalid = max(0, w.Lk - key0);
+              zero_keys(nvalid, C::VKP - nvalid);
             }
             if constexpr (MODS) {
               // and so may those before the first key that a row sees
-              if (key0 < w.kbeg) {
-                uint8_t* slot_ptr = smem + C::RING_OFF + slot * C::SLOTB;
-                const int nbad = min(C::VKP, w.kbeg - key0);
-                for (int i = lane; i < (C::DV / 64) * nbad * 8; i += 32) {
-                  const int dc = i / (nbad * 8);
-                  *reinterpret_cast<uint4*>(slot_ptr + dc * C::VKP * 128 + (i / 8) % nbad * 128 + i % 8 * 16) =
-                      make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
+              if (key0 < w.kbeg) zero_keys(0, min(C::VKP, w.kbeg - key0));
             }
             tc_fence_after();
             const uint64_t bd = dv0 + soff;
 #pragma unroll
             for (int kk = 0; kk < C::VKP / 16; ++kk)
-              tc_mma_ts_elect(tmem_O, ta + kk * 8, bd + static_cast<uint64_t>(kk * 128), idesc_pv,
+              tc_mma_ts_lead(lead, tmem_O, ta + kk * 8, bd + static_cast<uint64_t>(kk * 128), idesc_pv,
                         (j > 0 || p2 > 0 || kk > 0) ? 1u : 0u);
             ta += C::VKP / 2;
             // The item's last OSLOTS V parts stay held: the epilogue stages
@@ -606,13 +936,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_wait(smem_u32(&bars->drain), 0, nullptr);
     }
     __syncwarp();
+  } else if constexpr (MODS) {
+    if (warp < 2 + kSoftWarps<MODE>)
+      softmax_mods<HD, CAP, BIAS>(a, bars, tmem, sRing, nqt);
+    else
+      store_mods<HD>(a, bars, sRing, nqt, &tm_o);
   } else {
     // ------------------------------------------------------------ softmax
     const int quarter = warp & 3;  // TMEM lane quarter this warp may access
     const int half = (warp - 2) >> 2;  // which 64 of the 128 score columns
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    [[maybe_unused]] const float c2 = a.scale_log2;  // > 0 (checked on the host)
+    const float c2 = a.scale_log2;  // > 0 (checked on the host)
     constexpr int kHB = kBN / 2;    // score columns per thread
     constexpr int kDVH = C::DV / 2; // O columns per thread
     constexpr int kParts = C::KPARTS + C::VPARTS;  // ring parts per key tile
@@ -630,12 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_sync_any(1);
         break;
       }
-      TcItem w = tc_item<C::NDH, MODE>(a, it, nqt);
-      [[maybe_unused]] int2 keys = make_int2(0, 0);  // MODS: what this row sees
-      if constexpr (MODS) {
-        tc_set_keys(w, *reinterpret_cast<volatile int*>(&bars->kbeg[e]), *reinterpret_cast<volatile int*>(&bars->kend[e]));
-        keys = tc_row_keys(a, w, r);
-      }
+      const TcItem w = tc_item<C::NDH, MODE>(a, it, nqt);
       const int ntiles = w.ntiles;
       if (ntiles == 0) {
         // No visible key (only reachable with out-of-contract positions).
@@ -652,9 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int qpos = w.qpos_first + r;
-      [[maybe_unused]] const bool row_valid = r < w.valid_rows;
-      [[maybe_unused]] float slope = 0.0f;
-      if constexpr (BIAS) slope = a.slopes[w.h] * 1.4426950408889634f;
+      const bool row_valid = r < w.valid_rows;
       float m = -INFINITY;  // exponent base in log2 units: a stale running maximum
       float l = 0.0f;       // this half's share of the row sum
       bool ok = true;
@@ -664,36 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float s[kHB];
         float mt;
-        if constexpr (MODS) {
-          uint32_t r0[32], r1[32];
-          const uint32_t tS = tmem + lane_off + sb * kBN + half * kHB;
-          tmem_ld32(tS, r0);
-          tmem_ld32(tS + 32, r1);
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            s[i] = __uint_as_float(r0[i]);
-            s[32 + i] = __uint_as_float(r1[i]);
-          }
-          const int k0 = (w.kt_begin + j) * kBN + half * kHB;  // this half's first key
-          modify_scores<kHB, CAP, BIAS>(s, a, slope, qpos, k0);
-          const int lo = keys.x - k0, hi = keys.y - k0;
-          if (lo > 0 || hi < kHB) {
-            const unsigned span = static_cast<unsigned>(max(0, keys.y - keys.x));
-#pragma unroll
-            for (int n = 0; n < kHB; ++n)
-              if (static_cast<unsigned>(n - lo) >= span) s[n] = -INFINITY;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int n = 0; n < kHB; ++n) mx[n & 3] = fmaxf(mx[n & 3], s[n]);
-          const float mh = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // The halves' maxima meet in shared memory, by tile parity; the same barrier tells that both warps have read S_j.
-          bars->red[sb][half][r] = mh;
-          mbar_arrive(smem_u32(&bars->s_read[quarter]));
-          if (!warp_wait(smem_u32(&bars->s_read[quarter]), (J + j) & 1, a.err, abort)) { ok = false; break; }
-          mt = fmaxf(mh, bars->red[sb][1 - half][r]);
-        } else {
+        {
           // the whole row: both threads of a row take the same maximum
           uint32_t r0[32], r1[32], o0[32], o1[32];
           const uint32_t tS = tmem + lane_off + sb * kBN;
@@ -786,14 +1085,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          // (MODS: s is in log2 units by now)
-          const uint32_t pw = MODS ? pack_bf16x2(ex2_approx(s[2 * i] + nb), ex2_approx(s[2 * i + 1] + nb))
-                                   : pack_bf16x2(ex2_approx(fmaf(s[2 * i], c2, nb)), ex2_approx(fmaf(s[2 * i + 1], c2, nb)));
+          const uint32_t pw = pack_bf16x2(ex2_approx(fmaf(s[2 * i], c2, nb)), ex2_approx(fmaf(s[2 * i + 1], c2, nb)));
           p[i] = pw;
           sa[(2 * i) & 3] += bf16_lo(pw);
           sa[(2 * i + 1) & 3] += bf16_hi(pw);
         }
-        if (!MODS && !warp_wait(smem_u32(&bars->s_read[quarter]), (J + j) & 1, a.err, abort)) {
+        if (!warp_wait(smem_u32(&bars->s_read[quarter]), (J + j) & 1, a.err, abort)) {
           ok = false;
           break;
         }
@@ -806,12 +1103,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) {
         // the full row sum: both halves' shares
-        // (MODS: where the maxima of the tile before the last one were, which both have read)
-        auto& sums = bars->red[MODS ? (J + ntiles) & 1 : 0];
-        sums[half][r] = l;
+        bars->red[half][r] = l;
         mbar_arrive(smem_u32(&bars->sum_full[quarter]));
         ok = warp_wait(smem_u32(&bars->sum_full[quarter]), nq & 1, a.err, abort);
-        l = sums[0][r] + sums[1][r];
+        l = bars->red[0][r] + bars->red[1][r];
       }
       // Epilogue: O / l as bf16, in the chunk-major 128-byte-swizzled layout of
       // the output tensor map, into the ring slots of the item's last V parts
@@ -957,7 +1252,7 @@ cudaError_t launch_hd(const TcArgsOf<MODE>& a, cudaStream_t s) {
   const long long nblk = nitems < sm_count() ? nitems : sm_count();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(nblk));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<MODE>);
   cfg.dynamicSmemBytes = C::SMEM_B;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
