@@ -1200,13 +1200,13 @@ g4_status g4_attn_prefill_mods(const g4_layer_params* params, const g4_kv_cache*
   a.slopes = m.slopes;
   a.key_begin = m.key_begin;
   a.key_end = m.key_end;
-  return cuda_status(g4::launch_attn_simt_mods(a, params->dtype, s), "float32 prefill launch");
+  return cuda_status(g4::launch_attn_simt_mods(a, s), "float32 prefill launch");
 }
 
 size_t g4_attn_decode_mods_workspace_size(const g4_layer_params* params, int32_t B, int32_t max_seq_len) {
   if (check_params(params) != G4_OK || B < 1 || max_seq_len < 1) return 0;
-  return g4::decode_plan(params->dtype, params->layer_type == G4_SLIDING, params->window, params->head_dim,
-                         params->n_heads, params->n_kv_heads, B, max_seq_len, /*split_only=*/true)
+  return g4::mods_decode_plan(params->dtype, params->layer_type == G4_SLIDING ? params->window : 0, params->head_dim,
+                              params->n_heads, params->n_kv_heads, B, max_seq_len)
       .ws_bytes;
 }
 
@@ -1231,47 +1231,73 @@ g4_status g4_attn_decode_mods(const g4_layer_params* params, const g4_kv_cache* 
   if (max_seq_len < 1 || (!c->ring && max_seq_len > c->max_len))
     return fail(G4_ERR_CAPACITY, "max_seq_len %d outside [1, cache length %d]", max_seq_len, c->max_len);
   if (B == 0) return ok();
-  const g4::DecodePlan plan = g4::decode_plan(params->dtype, params->layer_type == G4_SLIDING, params->window,
-                                              params->head_dim, params->n_heads, params->n_kv_heads, B, max_seq_len,
-                                              /*split_only=*/true);
+  const int window = params->layer_type == G4_SLIDING ? params->window : 0;
+  const g4::ModsDecodePlan plan = g4::mods_decode_plan(params->dtype, window, params->head_dim, params->n_heads,
+                                                       params->n_kv_heads, B, max_seq_len);
   if (workspace_bytes < plan.ws_bytes)
     return fail(G4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, plan.ws_bytes);
   if (plan.ws_bytes > 0 && (workspace == nullptr || !aligned16(workspace)))
     return fail(G4_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
   int* err = device_error_ptr();
   if (err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
-  g4::ModsSimtArgs a;
+  const float scale_log2 = params->attn_scale * 1.4426950408889634f;
+  const float cap_log2 = m.softcap * 1.4426950408889634f;
+  if (plan.win) {
+    g4::ModsWinArgs w;
+    memset(&w, 0, sizeof(w));
+    w.q = q;
+    w.ck = c->k;
+    w.cv = c->v;
+    w.out = out;
+    w.base = seq_lens;
+    w.err = err;
+    w.B = B;
+    w.T = 1;
+    w.H = params->n_heads;
+    w.Hkv = params->n_kv_heads;
+    w.hd = params->head_dim;
+    w.max_len = c->max_len;
+    w.ring = c->ring;
+    w.sliding = window > 0;
+    w.window = window;
+    w.len_cap = max_seq_len;
+    w.chunk = 64;
+    w.nsplit = g4::decode_win_splits(window > 0 && window < max_seq_len ? window : max_seq_len);
+    w.scale_log2 = scale_log2;
+    w.cap_log2 = cap_log2;
+    w.slopes = m.slopes;
+    w.key_begin = m.key_begin;
+    return cuda_status(g4::launch_decode_win_mods(w, static_cast<cudaStream_t>(stream)), "windowed decode launch");
+  }
+  g4::ModsDecodeArgs a;
   memset(&a, 0, sizeof(a));
   a.q = q;
   a.ck = c->k;
   a.cv = c->v;
   a.out = out;
-  a.base = seq_lens;
+  a.lens = seq_lens;
+  a.key_begin = m.key_begin;
+  a.slopes = m.slopes;
   a.err = err;
   a.B = B;
-  a.T = 1;
   a.H = params->n_heads;
   a.Hkv = params->n_kv_heads;
   a.hd = params->head_dim;
   a.max_len = c->max_len;
   a.ring = c->ring;
-  a.sliding = params->layer_type == G4_SLIDING;
-  a.window = params->window;
+  a.window = window;
   a.len_cap = max_seq_len;
-  a.chunk = plan.chunk;
-  a.nsplit = plan.nsplit;
-  a.scale_log2 = params->attn_scale * 1.4426950408889634f;
-  a.cap_log2 = m.softcap * 1.4426950408889634f;
-  a.slopes = m.slopes;
-  a.key_begin = m.key_begin;
-  if (plan.nsplit > 1) {
+  a.nctas = plan.nctas;
+  a.scale_log2 = scale_log2;
+  a.cap_log2 = cap_log2;
+  if (plan.ws_bytes > 0) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.ws_o = reinterpret_cast<float*>(ws);
-    a.ws_m = reinterpret_cast<float*>(ws + plan.o_bytes);
-    a.ws_l = reinterpret_cast<float*>(ws + plan.o_bytes + plan.m_bytes);
-    a.tickets = reinterpret_cast<unsigned*>(ws + plan.o_bytes + 2 * plan.m_bytes);
+    a.tickets = reinterpret_cast<unsigned*>(ws);
+    a.ws_ml = reinterpret_cast<float2*>(ws + plan.t_bytes);
+    a.ws_o = reinterpret_cast<float*>(ws + plan.t_bytes + plan.ml_bytes);
   }
-  return cuda_status(g4::launch_attn_simt_mods(a, params->dtype, static_cast<cudaStream_t>(stream)), "decode launch");
+  return cuda_status(g4::launch_decode_mods(a, params->dtype, plan.warps, static_cast<cudaStream_t>(stream)),
+                     "decode launch");
 }
 
 const char* g4_last_error(void) { return g_last_error.c_str(); }

@@ -26,11 +26,10 @@ int sm_count() {
   return cached[dev];
 }
 
-DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len,
-                       bool split_only) {
+DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len) {
   DecodePlan p;
   const int span = sliding ? (max_seq_len < window ? max_seq_len : window) : max_seq_len;
-  if (!split_only && decode_win_eligible(dtype, hd, H / Hkv, span, B * Hkv)) {
+  if (decode_win_eligible(dtype, hd, H / Hkv, span, B * Hkv)) {
     p.win = 1;
     p.chunk = 64;
     p.nsplit = decode_win_splits(span);

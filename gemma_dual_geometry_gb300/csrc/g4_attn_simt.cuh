@@ -42,9 +42,9 @@
 // L-1, and uses them as its last key -- the append and the attention of one
 // decode step in a single launch.
 //
-// The MODS variant (g4_attn_prefill_mods in float32, g4_attn_decode_mods;
-// compiled in g4_attn_mods.cu) caps and biases a score in the lane that holds it
-// after the reduce-scatter, and streams a query's own interval of keys.
+// The MODS variant (g4_attn_prefill_mods in float32; compiled in g4_attn_mods.cu)
+// caps and biases a score in the lane that holds it after the reduce-scatter, and
+// streams a query's own interval of keys.
 #pragma once
 
 #include <math.h>
@@ -143,6 +143,87 @@ struct SimtCfg {
   static_assert(SMEM_B <= 232448, "shared memory budget");
 };
 
+// The n <= SK keys of a stage (K rows sk, V rows sv) into a warp's state: the heads' outputs o2 and, in the lanes
+// that hold head hh, its running maximum and sum.  modify(s, key) is what becomes of a score.
+template <typename C, typename T, int HD, int G, typename Modify>
+__device__ __forceinline__ void simt_stage(const T* sk, const T* sv, int n, const float2 (&q2)[G][C::EL / 2],
+                                           float2 (&o2)[G][C::EL / 2], float& m_l, float& l_l, float* sc, float* sa,
+                                           int lane, Modify modify) {
+  constexpr int EL2 = C::EL / 2;
+  constexpr int kSh = 5 - ilog2(C::NP);
+  const int hh = (lane >> kSh) & (G - 1);
+#pragma unroll 1
+  for (int nb = 0; nb < C::NB; ++nb) {
+    const int kb0 = nb * C::KB;
+    if (kb0 >= n) break;
+    // Partial dot products: part[key * G + h].
+    float part[C::NP];
+#pragma unroll
+    for (int key = 0; key < C::KB; ++key) {
+      float2 kx[EL2];
+      load_row_f2<T, C::NPC, C::PE>(sk + (kb0 + key) * HD, lane, kx);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < EL2; ++i) acc = fma2(q2[h][i], kx[i], acc);
+        part[key * G + h] = acc.x + acc.y;
+      }
+    }
+    // Softmax of this batch: each lane exponentiates its own entry; batch
+    // max and sum per head run over the lanes of the same head (key bits).
+    const int key_l = (lane >> kSh) / G;
+    const float s = modify(reduce_scatter<C::NP>(part, lane), kb0 + key_l);
+    const float s_me = (kb0 + key_l < n) ? s : -INFINITY;
+    float mb = s_me;
+#pragma unroll
+    for (int o = 1 << (kSh + ilog2(G)); o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    const float m_new = fmaxf(m_l, mb);
+    const float alpha = (m_l == -INFINITY) ? 0.0f : ex2(m_l - m_new);
+    const float p_l = ex2(s_me - m_new);
+    float ps = p_l;
+#pragma unroll
+    for (int o = 1 << (kSh + ilog2(G)); o < 32; o <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+    l_l = l_l * alpha + ps;
+    m_l = m_new;
+    if ((lane & ((1 << kSh) - 1)) == 0) {
+      sc[lane >> kSh] = p_l;
+      if (key_l == 0) sa[hh] = alpha;
+    }
+    __syncwarp();
+    float p[C::KB][G];
+#pragma unroll
+    for (int i = 0; i < C::NP; ++i) p[i / G][i % G] = sc[i];
+    float al[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) al[h] = sa[h];
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      if (al[h] != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < EL2; ++i) {
+          o2[h][i].x *= al[h];
+          o2[h][i].y *= al[h];
+        }
+      }
+    }
+    // o += p . v
+#pragma unroll
+    for (int key = 0; key < C::KB; ++key) {
+      if (kb0 + key < n) {
+        float2 vx[EL2];
+        load_row_f2<T, C::NPC, C::PE>(sv + (kb0 + key) * HD, lane, vx);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float2 pp = make_float2(p[key][h], p[key][h]);
+#pragma unroll
+          for (int i = 0; i < EL2; ++i) o2[h][i] = fma2(pp, vx[i], o2[h][i]);
+        }
+      }
+    }
+  }}
+
 template <bool MODS>
 using SimtArgsOf = std::conditional_t<MODS, ModsSimtArgs, AttnSimtArgs>;
 
@@ -188,19 +269,12 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
   int L, kbeg;
   [[maybe_unused]] int qpos = 0;  // MODS: the query's own position
   if constexpr (MODS) {
-    if (a.mode == 0) {
-      L = min(max(a.base[b], 0), a.len_cap);
-      qpos = L - 1;
-      kbeg = a.sliding ? max(0, L - a.window) : 0;
-      if (a.key_begin != nullptr) kbeg = max(kbeg, a.key_begin[b]);
-    } else {
-      const int start = min(max(a.base[b], 0), 0x7fffffff - a.T);
-      const int held = a.ring ? start + a.T : min(start + a.T, a.max_len);
-      qpos = start + t;
-      L = min(a.key_end != nullptr ? a.key_end[bt] : qpos + 1, held);
-      kbeg = a.key_begin != nullptr ? a.key_begin[bt] : a.sliding ? qpos - a.window + 1 : 0;
-      kbeg = max(kbeg, a.ring ? max(0, held - a.max_len) : 0);
-    }
+    const int start = min(max(a.base[b], 0), 0x7fffffff - a.T);
+    const int held = a.ring ? start + a.T : min(start + a.T, a.max_len);
+    qpos = start + t;
+    L = min(a.key_end != nullptr ? a.key_end[bt] : qpos + 1, held);
+    kbeg = a.key_begin != nullptr ? a.key_begin[bt] : a.sliding ? qpos - a.window + 1 : 0;
+    kbeg = max(kbeg, a.ring ? max(0, held - a.max_len) : 0);
     L = max(L, 0);
     kbeg = min(kbeg, L);
   } else if (!FUSED && a.mode == 2) {
@@ -218,10 +292,9 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
     }
     kbeg = a.sliding ? max(0, L - a.window) : 0;
   }
-  // (MODS: an interval may begin anywhere up to L, so the sums are made in 64 bits)
-  const int k0 = MODS ? static_cast<int>(min(static_cast<long long>(L), kbeg + static_cast<long long>(split) * a.chunk))
-                      : kbeg + split * a.chunk;
-  const int k1 = MODS ? (L - k0 < a.chunk ? L : k0 + a.chunk) : min(L, k0 + a.chunk);
+  // (MODS: one split, whose interval may begin anywhere up to L)
+  const int k0 = MODS ? kbeg : kbeg + split * a.chunk;
+  const int k1 = MODS ? L : min(L, k0 + a.chunk);
   // FUSED: the CTA holding position L-1 computes that key itself.
   const bool new_key = FUSED && a.k_raw != nullptr && (L - 1 >= k0) && (L - 1 < k1);
   const int k1c = new_key ? L - 1 : k1;  // keys streamed from the cache
@@ -422,81 +495,13 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
     const T* sk = reinterpret_cast<const T*>(ring + buf * 2 * C::STAGE_B);
     const T* sv = reinterpret_cast<const T*>(ring + buf * 2 * C::STAGE_B + C::STAGE_B);
 
-#pragma unroll 1
-    for (int nb = 0; nb < C::NB; ++nb) {
-      const int kb0 = nb * C::KB;
-      if (kb0 >= n) break;
-      // Partial dot products: part[key * G + h].
-      float part[C::NP];
-#pragma unroll
-      for (int key = 0; key < C::KB; ++key) {
-        float2 kx[EL2];
-        load_row_f2<T, C::NPC, C::PE>(sk + (kb0 + key) * HD, lane, kx);
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          float2 acc = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < EL2; ++i) acc = fma2(q2[h][i], kx[i], acc);
-          part[key * G + h] = acc.x + acc.y;
-        }
-      }
-      // Softmax of this batch: each lane exponentiates its own entry; batch
-      // max and sum per head run over the lanes of the same head (key bits).
-      float s = reduce_scatter<C::NP>(part, lane);
-      const int key_l = (lane >> kSh) / G;
+    simt_stage<C, T, HD, G>(sk, sv, n, q2, o2, m_l, l_l, sc, sa, lane, [&](float s, int key) {
       if constexpr (MODS) {
         if (a.cap_log2 > 0.0f) s = a.cap_log2 * tanhf(s * inv_cap);
-        if (a.slopes != nullptr) s = fmaf(-slope, fabsf(static_cast<float>(qpos - (k0 + st_idx * C::SK + kb0 + key_l))), s);
+        if (a.slopes != nullptr) s = fmaf(-slope, fabsf(static_cast<float>(qpos - (k0 + st_idx * C::SK + key))), s);
       }
-      const float s_me = (kb0 + key_l < n) ? s : -INFINITY;
-      float mb = s_me;
-#pragma unroll
-      for (int o = 1 << (kSh + ilog2(G)); o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-      const float m_new = fmaxf(m_l, mb);
-      const float alpha = (m_l == -INFINITY) ? 0.0f : ex2(m_l - m_new);
-      const float p_l = ex2(s_me - m_new);
-      float ps = p_l;
-#pragma unroll
-      for (int o = 1 << (kSh + ilog2(G)); o < 32; o <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-      l_l = l_l * alpha + ps;
-      m_l = m_new;
-      if ((lane & ((1 << kSh) - 1)) == 0) {
-        sc[lane >> kSh] = p_l;
-        if (key_l == 0) sa[hh] = alpha;
-      }
-      __syncwarp();
-      float p[C::KB][G];
-#pragma unroll
-      for (int i = 0; i < C::NP; ++i) p[i / G][i % G] = sc[i];
-      float al[G];
-#pragma unroll
-      for (int h = 0; h < G; ++h) al[h] = sa[h];
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        if (al[h] != 1.0f) {
-#pragma unroll
-          for (int i = 0; i < EL2; ++i) {
-            o2[h][i].x *= al[h];
-            o2[h][i].y *= al[h];
-          }
-        }
-      }
-      // o += p . v
-#pragma unroll
-      for (int key = 0; key < C::KB; ++key) {
-        if (kb0 + key < n) {
-          float2 vx[EL2];
-          load_row_f2<T, C::NPC, C::PE>(sv + (kb0 + key) * HD, lane, vx);
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float2 pp = make_float2(p[key][h], p[key][h]);
-#pragma unroll
-            for (int i = 0; i < EL2; ++i) o2[h][i] = fma2(pp, vx[i], o2[h][i]);
-          }
-        }
-      }
-    }
+      return s;
+    });
     __syncwarp();
     consumed = it + 1;
     const int next = st_idx + C::NST * NW;

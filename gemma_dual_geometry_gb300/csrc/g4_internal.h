@@ -151,14 +151,45 @@ struct AttnSimtArgs {
 };
 cudaError_t launch_attn_simt(const AttnSimtArgs& a, int dtype, cudaStream_t s);
 
-// The same with modified scores, modes 0 and 1, not fused (include/g4attn.h, g4_score_mods).
+// The same with modified scores, mode 1, not fused, one split (include/g4attn.h, g4_score_mods).
 struct ModsSimtArgs : AttnSimtArgs {
   float cap_log2;   // softcap * log2(e), 0: no cap
   const float* slopes;
   const int32_t* key_begin;  // [B][T]
   const int32_t* key_end;
 };
-cudaError_t launch_attn_simt_mods(const ModsSimtArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_mods(const ModsSimtArgs& a, cudaStream_t s);  // float32
+
+// Decode with modified scores: one query per sequence against keys [max(key_begin[b],
+// len - window), len), the keys of all sequences dealt out to the CTAs in equal shares.
+struct ModsDecodeArgs {
+  const void* q;      // [B][H][hd]
+  const void* ck;     // [B][Hkv][max_len][hd]
+  const void* cv;
+  void* out;          // [B][H][hd]
+  const int32_t* lens;
+  const int32_t* key_begin;  // [B] or null
+  const float* slopes;       // [H] or null
+  unsigned* tickets;  // arrival counters of merges (zero between calls)
+  float2* ws_ml;      // [2 nctas][G] running maximum and sum of a part
+  float* ws_o;        // [2 nctas][G][hd] its output, not normalised
+  int* err;
+  int B, H, Hkv, hd, max_len, ring;
+  int window;         // 0: full
+  int len_cap;        // lengths are clamped to [0, len_cap]
+  int nctas;
+  float scale_log2, cap_log2;
+};
+// How many CTAs a decode takes, and its workspace: tickets, ws_ml, ws_o in turn, each 256-byte aligned.
+// win = 1: the windowed cluster kernel (launch_decode_win_mods), no workspace.
+struct ModsDecodePlan {
+  int win;
+  int nctas;
+  int warps;  // per CTA
+  size_t t_bytes, ml_bytes, o_bytes, ws_bytes;
+};
+ModsDecodePlan mods_decode_plan(int dtype, int window, int hd, int H, int Hkv, int B, int max_seq_len);
+cudaError_t launch_decode_mods(const ModsDecodeArgs& a, int dtype, int warps, cudaStream_t s);
 
 // Step a5 (bf16): tcgen05 flash prefill.
 struct PrefillTcArgs {
@@ -200,6 +231,13 @@ constexpr int kMaxWinSplits = 8;
 bool decode_win_eligible(int dtype, int hd, int group, int span, int units);
 int decode_win_splits(int span);
 cudaError_t launch_decode_win(const AttnSimtArgs& a, cudaStream_t s);
+// The same with modified scores, not fused; lengths are clamped to [0, len_cap].
+struct ModsWinArgs : AttnSimtArgs {
+  float cap_log2;
+  const float* slopes;
+  const int32_t* key_begin;  // [B] or null
+};
+cudaError_t launch_decode_win_mods(const ModsWinArgs& a, cudaStream_t s);
 
 // The projections around the path on the tcgen05 tensor cores: a bf16 GEMM
 // out[M][N] = A[M][K] . Bw[N][K]^T (both operands K-major) whose epilogue is
@@ -243,9 +281,7 @@ struct DecodePlan {
   size_t o_bytes, m_bytes, t_bytes;  // sizes of the four regions (ws_m and ws_l share m_bytes)
   size_t ws_bytes;
 };
-// split_only: never win.
-DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len,
-                       bool split_only = false);
+DecodePlan decode_plan(int dtype, int sliding, int window, int hd, int H, int Hkv, int B, int max_seq_len);
 int sm_count();  // SMs of the current device
 
 }  // namespace g4
