@@ -1096,6 +1096,8 @@ g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_
     }
   }
   if (tokens == 0) return ok();
+  a.err = device_error_ptr();
+  if (a.err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
   a.n_axes = axes->n_axes;
   a.q_in = q_in;
   a.q_w = q_norm_w;
@@ -1107,11 +1109,10 @@ g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_
   a.Hkv = params->n_kv_heads;
   a.hd = params->head_dim;
   a.eps = params->eps;
-  // Tokens and rows per CTA as in g4_kv4_append_normrope.
+  // A warp takes a token's rows as long as that makes 16 warps for each SM, fewer of them otherwise.
   const int nrows = a.H + (shared ? 0 : 2 * a.Hkv);
-  a.tok_per_cta = T >= 16 ? (B < g4::kAppendMaxTokens ? B : g4::kAppendMaxTokens) : 1;
-  const long long ctas = static_cast<long long>(T) * ((B + a.tok_per_cta - 1) / a.tok_per_cta);
-  a.rows_per_cta = ctas >= 1024 ? nrows : 4;
+  const long long rows_each = tokens * nrows / (16LL * g4::sm_count());
+  a.rows_per_unit = static_cast<int>(rows_each < 1 ? 1 : rows_each > nrows ? nrows : rows_each);
   return cuda_status(g4::launch_append_axes(a, params->dtype, static_cast<cudaStream_t>(stream)), "append launch");
 }
 

@@ -34,10 +34,6 @@
 // append: 179 and 114), 59 us of which are bytes; with the stores left out 2 %
 // less.
 //
-// The append with several position axes (AXES) turns pair j by the position of
-// its axis and takes the cache row from an array of its own.  Its cos/sin tables
-// are the 4-bit append's: one per token whose positions differ from its neighbour's, all built at once.
-//
 // Lane l of a warp owns elements [l*E, l*E + E) of the lower half and the
 // same offsets of the upper half (E = head_dim / 64), so each rotate_half
 // pair (j, j + head_dim/2) sits in one lane.  Each warp loads its next row
@@ -264,16 +260,11 @@ __device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t*
   }
 }
 
-// Where rows go and what turns them: the bf16 / float32 cache, the 4-bit pool, the cache with several position axes.
-constexpr int kToCache = 0, kToKv4 = 1, kToCacheAxes = 2;
-template <int FORM>
-using ArgsOf = std::conditional_t<FORM == kToKv4, Kv4AppendArgs, std::conditional_t<FORM == kToCacheAxes, AxesAppendArgs, AppendArgs>>;
+template <bool KV4>
+using ArgsOf = std::conditional_t<KV4, Kv4AppendArgs, AppendArgs>;
 
-template <typename T, int HD, int FORM>
-__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ ArgsOf<FORM> a) {
-  constexpr bool KV4 = FORM == kToKv4;
-  constexpr bool AXES = FORM == kToCacheAxes;
-  constexpr bool TABS = KV4 || AXES;  // the tokens' tables are all built at once
+template <typename T, int HD, bool KV4>
+__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ ArgsOf<KV4> a) {
   constexpr int HALF = HD / 2;
   constexpr int E = HD / 64;
   constexpr bool kBF16 = sizeof(T) == 2;
@@ -281,19 +272,14 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
   constexpr float kErrAB = normrope_err_pair(kDFTrigErrUnits);
   constexpr float kErrO = normrope_err_out<2 * E>();
   constexpr float kErrR = normrope_err_r<2 * E>();
-  constexpr int kTabs = TABS ? kAppendMaxTokens : 1;  // tables held at once
+  constexpr int kTabs = KV4 ? kAppendMaxTokens : 1;  // tables held at once
   __shared__ DF s_cos_all[kTabs * HALF];
   __shared__ DF s_sin_all[kTabs * HALF];
-  [[maybe_unused]] int tok_pos[kAppendMaxTokens], tok_tab[kAppendMaxTokens];  // position and table of each token (TABS)
+  [[maybe_unused]] int tok_pos[kAppendMaxTokens], tok_tab[kAppendMaxTokens];  // KV4: position and table of each token
   int tab = 0;  // where the current token's table begins
-  auto cos_of = [&](int j) -> DF { return s_cos_all[(TABS ? tab : 0) + j]; };
-  auto sin_of = [&](int j) -> DF { return s_sin_all[(TABS ? tab : 0) + j]; };
-  // bf16 q rows whose place is where they come from are finished in shared memory too: a value left open is decided
-  // from the inputs again after the others have been stored.
-  constexpr bool STAGES = AXES && kBF16;
-  [[maybe_unused]] const bool in_place = STAGES && a.q_in == a.q_out;
-  // KV4, STAGES: a finished row per warp
-  __shared__ __align__(16) T s_row[KV4 ? 4 * kv4_row_at(HD) : STAGES ? 4 * HD : 1];
+  auto cos_of = [&](int j) -> DF { return s_cos_all[(KV4 ? tab : 0) + j]; };
+  auto sin_of = [&](int j) -> DF { return s_sin_all[(KV4 ? tab : 0) + j]; };
+  __shared__ __align__(16) T s_row[KV4 ? 4 * kv4_row_at(HD) : 1];  // KV4: a finished row per warp
 
   pdl_wait();
   pdl_trigger();
@@ -335,7 +321,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       sr[i] = s_sin_all[lane * E + i].h;
     }
   };
-  // TABS: token b's table becomes the current one.
+  // KV4: token b's table becomes the current one.
   auto use_table = [&](int b) {
     tab = 0;
 #pragma unroll
@@ -355,24 +341,23 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     const float* w;
     bool rope;
     bool valid;
-    bool is_q;
     uint8_t* rec;  // KV4: the record of a k or v row (null: a q row, whose place is dst) and its position there
     int m;
   };
   // Where element d of a row goes: its place, or (KV4) the warp's row in shared memory.
-  T* const row_buf = s_row + (KV4 ? warp * kv4_row_at(HD) : STAGES ? warp * HD : 0);
+  T* const row_buf = s_row + (KV4 ? warp * kv4_row_at(HD) : 0);
   auto at = [&](const RowRef& rr, int d) -> T* {
-    if constexpr (KV4) return row_buf + kv4_row_at(d);
-    if constexpr (STAGES) return (in_place && rr.is_q ? row_buf : rr.dst) + d;
-    return rr.dst + d;
+    if constexpr (KV4)
+      return row_buf + kv4_row_at(d);
+    else
+      return rr.dst + d;
   };
-  // (KV4: pos is the token's slot; AXES: its row)
+  // (KV4: pos is the token's slot)
   auto row_ref = [&](int b, int row, int pos) -> RowRef {
     const int tok = b * a.T + t;
     RowRef rr;
     rr.rec = nullptr;
     rr.m = 0;
-    rr.is_q = row < a.H;
     if (row < a.H) {  // q head
       const size_t off = (static_cast<size_t>(tok) * a.H + row) * HD;
       rr.src = static_cast<const T*>(a.q_in) + off;
@@ -547,36 +532,15 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       }
       __syncwarp();
     }
-    if constexpr (STAGES) {
-      if (in_place && rr.is_q) {
-        __syncwarp();
-        constexpr int C = HD >= 256 ? 8 : HD / 32;
-        using V = std::conditional_t<C == 8, uint4, std::conditional_t<C == 4, uint2, uint32_t>>;
-#pragma unroll
-        for (int d = lane * C; d < HD; d += 32 * C)
-          *reinterpret_cast<V*>(rr.dst + d) = *reinterpret_cast<const V*>(row_buf + d);
-        __syncwarp();
-      }
-    }
-  };
-
-  // Where token (b, t)'s k and v go (TABS): its slot, or its row's position.
-  [[maybe_unused]] auto place_of = [&](int b) -> int {
-    if constexpr (KV4)
-      return a.slots[b * a.T + t];
-    else if constexpr (AXES)
-      return a.rows[b * a.T + t];
-    else
-      return 0;
   };
 
   // Rows of tokens [bA, bB) (all at position pos), flattened in (b, row)
-  // order; warp w takes items w, w + 4, ... (TABS with four tokens: those of
+  // order; warp w takes items w, w + 4, ... (KV4 with four tokens: those of
   // token w).  The next item's loads are issued before the current one is computed.
   // `then` runs after the first item's loads have been issued.
   auto run = [&](int bA, int bB, int pos, auto then) {
     int b = bA, row = row0 + warp, stride = 4;
-    if (TABS && bB - bA == 4) {  // a token per warp: its cos / sin are loaded once
+    if (KV4 && bB - bA == 4) {  // a token per warp: its cos / sin are loaded once
       b = bA + warp;
       bB = b + 1;
       row = row0;
@@ -586,8 +550,8 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     RowRef rr = {};
     HalfBits<T, E> lo, hi;
     [[maybe_unused]] int b_tab = -1;
-    if constexpr (TABS) {
-      if (b < bB && owns) pos = place_of(b);
+    if constexpr (KV4) {
+      if (b < bB && owns) pos = a.slots[b * a.T + t];
     }
     if (b < bB) {
       rr = row_ref(b, row, pos);
@@ -601,13 +565,13 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       HalfBits<T, E> lon, hin;
       [[maybe_unused]] int pos_n = pos;
       if (bn < bB) {
-        if constexpr (TABS) {
-          if (bn != b && owns) pos_n = place_of(bn);
+        if constexpr (KV4) {
+          if (bn != b && owns) pos_n = a.slots[bn * a.T + t];
         }
         rrn = row_ref(bn, rn, pos_n);
         load_row(rrn, lon, hin);
       }
-      if constexpr (TABS) {
+      if constexpr (KV4) {
         if (b != b_tab) use_table(b_tab = b);
         rr = row_ref(b, row, pos);  // (again, rather than kept from the load: its registers)
       }
@@ -617,7 +581,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
         do_row(rr, lo, hi, std::false_type());
       b = bn;
       row = rn;
-      if constexpr (TABS)
+      if constexpr (KV4)
         pos = pos_n;
       else
         rr = rrn;
@@ -626,38 +590,23 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     }
   };
 
-  if constexpr (TABS) {
+  if constexpr (KV4) {
     // A table per distinct position (neighbours that agree share one), all of
     // them built at once while the first rows are on their way, so that rows of
     // all tokens follow each other.
-    [[maybe_unused]] auto pos_of = [&](int axis, int i) -> int {
-      return a.positions[(static_cast<size_t>(axis) * a.B + min(b0 + i, b1 - 1)) * a.T + t];
-    };
 #pragma unroll
     for (int i = 0; i < kAppendMaxTokens; ++i) {
-      tok_pos[i] = pos_of(0, i);
-      bool differs = i > 0 && tok_pos[i] != tok_pos[max(i, 1) - 1];
-      if constexpr (AXES) {
-        for (int x = 1; x < a.n_axes && i > 0; ++x) differs = differs || pos_of(x, i) != pos_of(x, i - 1);
-      }
-      tok_tab[i] = i == 0 ? 0 : tok_tab[i - 1] + differs;
+      tok_pos[i] = a.positions[min(b0 + i, b1 - 1) * a.T + t];
+      tok_tab[i] = i == 0 ? 0 : tok_tab[i - 1] + (tok_pos[i] != tok_pos[i - 1]);
     }
     run(b0, b1, 0, [&] {
       const int ntab = tok_tab[kAppendMaxTokens - 1] + 1;
       for (int idx = threadIdx.x; idx < ntab * HD; idx += blockDim.x) {
         const int j = (idx >> 1) % HALF, part = idx & 1, tb = idx / HD, at = tb * HALF + j;
         int pos = tok_pos[0];
-        if constexpr (AXES) {
-          int tok = 0;
 #pragma unroll
-          for (int i = 1; i < kAppendMaxTokens; ++i)
-            if (tok_tab[i] == tb) tok = i;
-          if (j < a.n_rot) pos = pos_of(a.axis[j], tok);
-        } else {
-#pragma unroll
-          for (int i = 1; i < kAppendMaxTokens; ++i)
-            if (tok_tab[i] == tb) pos = tok_pos[i];
-        }
+        for (int i = 1; i < kAppendMaxTokens; ++i)
+          if (tok_tab[i] == tb) pos = tok_pos[i];
         if (j < a.n_rot) {
           bool to_cos;
           const DF v = sincos_df_part(pos, a.inv_freq[j], part, to_cos);
@@ -704,15 +653,15 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, cudaStream_t s, const Args& a) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename T, int FORM>
-cudaError_t launch_t(const ArgsOf<FORM>& a, cudaStream_t s) {
+template <typename T, bool KV4>
+cudaError_t launch_t(const ArgsOf<KV4>& a, cudaStream_t s) {
   const int nrows = a.H + (a.k_in ? 2 * a.Hkv : 0);
   dim3 grid(a.T * ((a.B + a.tok_per_cta - 1) / a.tok_per_cta), (nrows + a.rows_per_cta - 1) / a.rows_per_cta);
   switch (a.hd) {
-    case 64: return launch_pdl(append_normrope_kernel<T, 64, FORM>, grid, s, a);
-    case 128: return launch_pdl(append_normrope_kernel<T, 128, FORM>, grid, s, a);
-    case 256: return launch_pdl(append_normrope_kernel<T, 256, FORM>, grid, s, a);
-    case 512: return launch_pdl(append_normrope_kernel<T, 512, FORM>, grid, s, a);
+    case 64: return launch_pdl(append_normrope_kernel<T, 64, KV4>, grid, s, a);
+    case 128: return launch_pdl(append_normrope_kernel<T, 128, KV4>, grid, s, a);
+    case 256: return launch_pdl(append_normrope_kernel<T, 256, KV4>, grid, s, a);
+    case 512: return launch_pdl(append_normrope_kernel<T, 512, KV4>, grid, s, a);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -720,13 +669,9 @@ cudaError_t launch_t(const ArgsOf<FORM>& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-  return dtype == 1 ? launch_t<__nv_bfloat16, kToCache>(a, s) : launch_t<float, kToCache>(a, s);
+  return dtype == 1 ? launch_t<__nv_bfloat16, false>(a, s) : launch_t<float, false>(a, s);
 }
 
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) { return launch_t<__nv_bfloat16, kToKv4>(a, s); }
-
-cudaError_t launch_append_axes(const AxesAppendArgs& a, int dtype, cudaStream_t s) {
-  return dtype == 1 ? launch_t<__nv_bfloat16, kToCacheAxes>(a, s) : launch_t<float, kToCacheAxes>(a, s);
-}
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) { return launch_t<__nv_bfloat16, true>(a, s); }
 
 }  // namespace g4

@@ -87,11 +87,12 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s);
 
-// The same with positions of several axes, apart from the cache's rows; tok_per_cta at most
-// kAppendMaxTokens (g4_kv4_internal.h).
+// The same with positions of several axes, apart from the cache's rows (rows_per_cta and tok_per_cta unused).
 struct AxesAppendArgs : AppendArgs {
   const int32_t* rows;   // [B*T] position in the cache (positions: [n_axes][B*T]); null on a shared layer
+  int* err;
   int n_axes;
+  int rows_per_unit;     // head rows that a warp takes of a token
   uint8_t axis[kMaxHalf];  // axis of pair j
 };
 cudaError_t launch_append_axes(const AxesAppendArgs& a, int dtype, cudaStream_t s);
