@@ -39,19 +39,25 @@ namespace {
 constexpr int kWarps = 4;
 constexpr float kTrigUnits = 1.5f;  // bound on the error of sincos_f32 in units of 2^-24
 
-// (a call of its own: positions so far are rare, and the code long)
-static __device__ __noinline__ float2 sincos_far(int p, float f) {
+// sincos_df as a call of its own, {cos, sin}: rarely needed, and long.
+static __device__ __noinline__ float4 sincos_exact(int p, float f) {
   DF c, s;
   sincos_df(p, f, c, s);
-  return make_float2(c.h, s.h);
+  return make_float4(c.h, c.l, s.h, s.l);
 }
 
 // cos and sin of p * f: the exact product less the nearest multiple k of pi/2 (three floats), Taylor polynomials.
+__device__ __forceinline__ bool angle_is_near(int p, float f) {
+  return fabsf(static_cast<float>(p) * f) < 0x1.0p20f && p < (1 << 24) && p > -(1 << 24);
+}
 __device__ __forceinline__ float2 sincos_f32(int p, float f) {
   const float pf = static_cast<float>(p);
   const float th = pf * f, tl = fmaf(pf, f, -th);
   // (k no longer the nearest, or p not exact)
-  if (fabsf(th) >= 0x1.0p20f || p >= (1 << 24) || p <= -(1 << 24)) return sincos_far(p, f);
+  if (!angle_is_near(p, f)) {
+    const float4 v = sincos_exact(p, f);
+    return make_float2(v.x, v.z);
+  }
   const float k = rintf(th * 0x1.45f306p-1f);  // 2 / pi
   constexpr float P1 = 0x1.921fb6p+0f, P2 = -0x1.777a5cp-25f, P3 = -0x1.ee59dap-50f;  // pi / 2
   const float ah = k * P1, al = fmaf(k, P1, -ah);
@@ -69,6 +75,28 @@ __device__ __forceinline__ float2 sincos_f32(int p, float f) {
   const int q = static_cast<int>(k) & 3;
   const float c = q & 1 ? sn : cs, s = q & 1 ? cs : sn;
   return make_float2(q == 1 || q == 2 ? -c : c, q >= 2 ? -s : s);
+}
+
+// The same with two floats each, off by at most 0.32 x 2^-24: the reduced angle in double-float, the heads of both
+// series exact, their tails in float32.  A third of sincos_df's instructions.
+constexpr float kMidErr = 0x1.0p-24f;  // (three times that)
+__device__ __forceinline__ void sincos_mid(int p, float f, DF& c, DF& s) {
+  int q;
+  const DF r = reduce_angle_df(p, f, q);
+  const float z = r.h * r.h, zl = fmaf(2.0f * r.h, r.l, fmaf(r.h, r.h, -z));
+  float ps = fmaf(z, 0x1.71de3ap-19f, -0x1.a01a02p-13f);
+  ps = fmaf(z, ps, 0x1.111112p-7f);
+  ps = fmaf(z, ps, -0x1.555556p-3f);
+  const DF sn = fast_two_sum(r.h, fmaf(r.h * z, ps, r.l * fmaf(z, -0.5f, 1.0f)));
+  float pc = fmaf(z, -0x1.27e4fcp-22f, 0x1.a01a02p-16f);
+  pc = fmaf(z, pc, -0x1.6c16c2p-10f);
+  pc = fmaf(z, pc, 0x1.555556p-5f);
+  DF cs = fast_two_sum(1.0f, -0.5f * z);
+  cs = fast_two_sum(cs.h, cs.l + fmaf(z * z, pc, -0.5f * zl));
+  c = q & 1 ? sn : cs;
+  s = q & 1 ? cs : sn;
+  if (q == 1 || q == 2) c = df_neg(c);
+  if (q >= 2) s = df_neg(s);
 }
 
 template <typename T, int HD>
@@ -431,14 +459,28 @@ __global__ void __launch_bounds__(kWarps * 32, AxCfg<T, HD>::RESIDENT) append_ax
               const bool lower = k < 16;
               const int j = e / CW * C::SPAN + lane * CW + e % CW;
               const int self = lower ? j : HALF + j, other = lower ? HALF + j : j;
-              DF inner = two_prod(static_cast<float>(in[self]), rope ? w[self] : 1.0f);
+              const DF own = two_prod(static_cast<float>(in[self]), rope ? w[self] : 1.0f);
+              DF v = df_mul(own, rd);
               if (rope && j < n_rot) {
                 const DF po = two_prod(static_cast<float>(in[other]), w[other]);
-                DF cj, sj;
-                sincos_df(position(s_axis[j]), s_freq[j], cj, sj);
-                inner = df_add(df_mul(inner, cj), df_mul(po, lower ? df_neg(sj) : sj));
+                auto turned = [&](DF cj, DF sj) {
+                  return df_mul(df_add(df_mul(own, cj), df_mul(po, lower ? df_neg(sj) : sj)), rd);
+                };
+                const int at = position(s_axis[j]);
+                const float f = s_freq[j];
+                bool decided = angle_is_near(at, f);
+                if (decided) {
+                  DF cj, sj;
+                  sincos_mid(at, f, cj, sj);
+                  v = turned(cj, sj);
+                  decided = fabsf((v.h - bf16_midpoint(v.h)) + v.l) > kMidErr * rd.h * (fabsf(own.h) + fabsf(po.h));
+                }
+                if (!decided) {
+                  const float4 t = sincos_exact(at, f);
+                  v = turned(DF{t.x, t.y}, DF{t.z, t.w});
+                }
               }
-              dst[self] = static_cast<T>(df_round_bf16(df_mul(inner, rd)));
+              dst[self] = static_cast<T>(df_round_bf16(v));
             }
           }
         }
