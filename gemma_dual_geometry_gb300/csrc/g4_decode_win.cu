@@ -206,15 +206,17 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<HD, G>::MINB))
       return min(max(a.base[b], 1), a.len_cap);
     }
   };
-  auto first_key = [&](int Lx) {
+  auto first_of_seq = [&](int Lx) {
     const int from = a.sliding ? max(0, Lx - a.window) : 0;
-    return (MODS ? min(max(from, begin), Lx) : from) + split * kWinKeys;
+    return MODS ? min(max(from, begin), Lx) : from;
   };
   auto n_keys = [&](int Lx) {
     // (MODS: positions may end at 2^31 - 1, so nothing is added to them)
-    if constexpr (MODS) return max(0, min(kWinKeys, Lx - (first_key(Lx) - split * kWinKeys) - split * kWinKeys));
-    return max(0, min(Lx, first_key(Lx) + kWinKeys) - first_key(Lx));
+    if constexpr (MODS) return max(0, min(kWinKeys, Lx - first_of_seq(Lx) - split * kWinKeys));
+    const int from = first_of_seq(Lx) + split * kWinKeys;
+    return max(0, min(Lx, from + kWinKeys) - from);
   };
+  auto first_key = [&](int Lx) { return MODS && n_keys(Lx) == 0 ? 0 : first_of_seq(Lx) + split * kWinKeys; };
   // cos / sin of position p (all threads; the pairs past n_rot are the identity)
   auto build_table = [&](int p) {
     for (int idx = threadIdx.x; idx < HD; idx += kWinThreads) {

@@ -106,6 +106,7 @@ struct RangesArgs {
   int32_t* begin;       // [B][T]
   int32_t* end;
   int B, T, max_len, window;
+  int aligned_ids, aligned_out;  // rows may be read, or written, four at a time (set by the launcher)
 };
 cudaError_t launch_ranges(const RangesArgs& a, cudaStream_t s);
 

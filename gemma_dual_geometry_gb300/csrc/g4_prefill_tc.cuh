@@ -357,7 +357,7 @@ __device__ __forceinline__ void softmax_mods(const ModsTcArgs& a, TcBars* bars, 
     if (it < 0) return false;
     TcItem w = tc_item<C::NDH, kMods>(a, it, nqt);
     tc_set_keys(w, kbeg, kend);
-    x.qpos = w.qpos_first + r;
+    x.qpos = w.qpos_first + min(r, w.valid_rows - 1);
     x.kt_last = w.kt_begin + w.ntiles - 1;
     x.ntiles = w.ntiles;
     x.keys = tc_row_keys(a, w, r);

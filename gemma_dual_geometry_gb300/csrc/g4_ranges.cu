@@ -12,7 +12,10 @@
 // the others through distributed shared memory, and then scans its tiles with
 // what came before and comes after.  A CTA of one tile keeps the ids in registers
 // between the two passes.
-//   Bound by latency: load, reduction, cluster barrier, scan, store.
+//   Bound by latency: load, reduction, cluster barrier, scan, store: 8 rows of 32768
+// positions (3.7 MB) 5.8 us, one of 1000 3.0 us, one of 131072 12 us.  (CTAs that find what
+// they need of the rest of the row by themselves, looking back for the beginning of their
+// run, took 18, 3.7 and 68 us.)
 #include <cooperative_groups.h>
 
 #include "g4_device.cuh"
@@ -23,15 +26,14 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kRangesThreads = 1024;
-constexpr int kPer = 4;                          // consecutive positions per thread
-constexpr int kTile = kRangesThreads * kPer;
-constexpr int kRangesMaxCtas = 8;                // clusters of up to 8 CTAs are always allowed
+// (1024 threads of 4 positions: 6.4 us against 5.8 at 8 rows of 32768; 256 of 16: 6.2)
+constexpr int kRangesThreads = 512;
+constexpr int kRangesMaxCtas = 16;
 constexpr int kRangesMaxTiles = 512;             // tiles per CTA: 2^24 positions over 8 CTAs
 constexpr int kNone = 0x7fffffff;
-static_assert(kTile * kRangesMaxTiles * static_cast<long long>(kRangesMaxCtas) >= 1 << 24, "longest rows");
 
-// One tile's ids of this thread, and what is a cut.
+// One tile's ids of this thread (kPer consecutive positions), and what is a cut.
+template <int kPer>
 struct Ids {
   int doc[kPer], span[kPer];
   uint32_t doc_cut, span_cut;  // bit i: position i of the thread's is a cut
@@ -47,10 +49,14 @@ __device__ __forceinline__ Cuts join(Cuts a, Cuts b) {
   return {max(a.doc, b.doc), max(a.span, b.span), min(a.first, b.first)};
 }
 
+template <int kPer>
 __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_constant__ RangesArgs a) {
   __shared__ Cuts s_tile[kRangesMaxTiles];  // of this CTA's tiles
   __shared__ Cuts s_cta;                    // of all of them
-  __shared__ Cuts s_warp[32];
+  constexpr int NW = kRangesThreads / 32;
+  constexpr int kTile = kRangesThreads * kPer;
+  static_assert(kPer == 4 || 8LL * kTile * kRangesMaxTiles >= 1 << 24, "longest rows");
+  __shared__ Cuts s_warp[NW];
   cg::cluster_group cluster = cg::this_cluster();
   const int nctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int b = blockIdx.x / nctas;
@@ -69,7 +75,7 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
 
   // Ids of the thread's positions of a tile; those from len on take no part.
   auto load = [&](int tile) {
-    Ids d;
+    Ids<kPer> d;
     const int p0 = tile * kTile + tid * kPer;
     d.doc_cut = d.span_cut = 0;
     int before_doc = 0, before_span = -1;
@@ -77,11 +83,21 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
       if (doc != nullptr) before_doc = __ldg(doc + p0 - 1);
       if (span != nullptr) before_span = __ldg(span + p0 - 1);
     }
+    if (a.aligned_ids && p0 + kPer <= len) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int p = p0 + i;
-      d.doc[i] = doc != nullptr && p < len ? __ldg(doc + p) : 0;
-      d.span[i] = span != nullptr && p < len ? __ldg(span + p) : -1;
+      for (int i = 0; i < kPer; i += 4) {
+        const int4 x = doc != nullptr ? __ldg(reinterpret_cast<const int4*>(doc + p0 + i)) : make_int4(0, 0, 0, 0);
+        const int4 y = span != nullptr ? __ldg(reinterpret_cast<const int4*>(span + p0 + i)) : make_int4(-1, -1, -1, -1);
+        d.doc[i] = x.x; d.doc[i + 1] = x.y; d.doc[i + 2] = x.z; d.doc[i + 3] = x.w;
+        d.span[i] = y.x; d.span[i + 1] = y.y; d.span[i + 2] = y.z; d.span[i + 3] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int p = p0 + i;
+        d.doc[i] = doc != nullptr && p < len ? __ldg(doc + p) : 0;
+        d.span[i] = span != nullptr && p < len ? __ldg(span + p) : -1;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -94,7 +110,7 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
     }
     return d;
   };
-  auto of_thread = [&](const Ids& d, int tile) {
+  auto of_thread = [&](const Ids<kPer>& d, int tile) {
     const int p0 = tile * kTile + tid * kPer;
     Cuts c = no_cuts();
     if (d.doc_cut) c.doc = p0 + 31 - __clz(d.doc_cut);
@@ -109,14 +125,14 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
   };
 
   // First pass: the cuts of each tile of this CTA.
-  Ids ids = {};
+  Ids<kPer> ids = {};
   for (int tile = t0; tile < t1; ++tile) {
     ids = load(tile);
     const Cuts c = of_warp(of_thread(ids, tile));
     if (lane == 0) s_warp[warp] = c;
     __syncthreads();
     if (warp == 0) {
-      const Cuts all = of_warp(s_warp[lane]);
+      const Cuts all = of_warp(lane < NW ? s_warp[lane] : no_cuts());
       if (lane == 0) s_tile[tile - t0] = all;
     }
     __syncthreads();
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
       }
       if (lane == 0) s_warp[warp].first = scan.first;
       __syncthreads();
-      const Cuts others = s_warp[lane];
+      const Cuts others = lane < NW ? s_warp[lane] : no_cuts();
       const Cuts w_before = of_warp(lane < warp ? others : no_cuts());
       const Cuts w_after = of_warp(lane > warp ? others : no_cuts());
       int d = __shfl_up_sync(kAll, scan.doc, 1), s = __shfl_up_sync(kAll, scan.span, 1);
@@ -183,29 +199,45 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
         ends[i] = e;
         if (ids.span_cut >> i & 1) e = tile_begin + tid * kPer + i;
       }
+      int first[kPer], last[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int p = tile_begin + tid * kPer + i;
         if (ids.doc_cut >> i & 1) d = p;
         if (ids.span_cut >> i & 1) s = p;
-        const int t = p - start;
-        if (p >= len || t < 0 || t >= a.T) continue;
-        int begin = a.window > 0 ? max(d, p - a.window + 1) : d, end = p + 1;
+        first[i] = a.window > 0 ? max(d, p - a.window + 1) : d;
+        last[i] = p + 1;
         if (ids.span[i] >= 0) {
-          begin = min(begin, s);
-          end = ends[i];
+          first[i] = min(first[i], s);
+          last[i] = ends[i];
         }
-        if (ids.doc[i] < 0) begin = end = 0;
-        const size_t at = static_cast<size_t>(b) * a.T + t;
-        a.begin[at] = begin;
-        a.end[at] = end;
+        if (ids.doc[i] < 0) first[i] = last[i] = 0;
+      }
+      const int p0 = tile_begin + tid * kPer;
+      const long long t = static_cast<long long>(p0) - start;  // the first one's token
+      int* const to_begin = a.begin + static_cast<size_t>(b) * a.T + t;
+      int* const to_end = a.end + static_cast<size_t>(b) * a.T + t;
+      if (t >= 0 && t + kPer <= a.T && p0 + kPer <= len && a.aligned_out && (start & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) {
+          *reinterpret_cast<int4*>(to_begin + i) = make_int4(first[i], first[i + 1], first[i + 2], first[i + 3]);
+          *reinterpret_cast<int4*>(to_end + i) = make_int4(last[i], last[i + 1], last[i + 2], last[i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (p0 + i < len && t + i >= 0 && t + i < a.T) {
+            to_begin[i] = first[i];
+            to_end[i] = last[i];
+          }
+        }
       }
     }
     before = join(before, s_tile[tile - t0]);
   }
   // tokens that are no position held
-  for (int t = rank * kRangesThreads + tid; t < a.T; t += nctas * kRangesThreads) {
-    const int p = start + t;
+  for (long long t = rank * kRangesThreads + tid; t < a.T; t += nctas * kRangesThreads) {
+    const int p = start + static_cast<int>(t);
     if (p < 0 || p >= len) {
       const size_t at = static_cast<size_t>(b) * a.T + t;
       a.begin[at] = 0;
@@ -215,12 +247,8 @@ __global__ void __launch_bounds__(kRangesThreads) ranges_kernel(const __grid_con
   if (nctas > 1) cluster.barrier_wait();
 }
 
-}  // namespace
-
-cudaError_t launch_ranges(const RangesArgs& a, cudaStream_t s) {
-  // A CTA per tile of the longest row, up to a cluster of 8.
-  int nctas = 1;
-  while (nctas < kRangesMaxCtas && nctas * kTile < a.max_len) nctas *= 2;
+template <int kPer>
+cudaError_t launch_per(const RangesArgs& a, unsigned nctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * nctas);
   cfg.blockDim = dim3(kRangesThreads);
@@ -234,7 +262,23 @@ cudaError_t launch_ranges(const RangesArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ranges_kernel, a);
+  return cudaLaunchKernelEx(&cfg, ranges_kernel<kPer>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_ranges(const RangesArgs& a_in, cudaStream_t s) {
+  RangesArgs a = a_in;
+  auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  a.aligned_ids = a.max_len % 4 == 0 && aligned(a.doc) && aligned(a.span);
+  a.aligned_out = a.T % 4 == 0 && aligned(a.begin) && aligned(a.end);
+  // A CTA per tile of the longest row, up to a cluster of 16 where that may be had.  Rows of one tile of 2048 take that one
+  // (1000 positions 3.0 us against 3.6 with a tile of 4096).
+  if (a.max_len <= 4 * kRangesThreads) return launch_per<4>(a, 1, s);
+  unsigned nctas = 1;
+  const unsigned most = a.max_len > 8 * 8 * kRangesThreads ? cluster_limit_once<ranges_kernel<8>>(kRangesThreads, 0) : 8;
+  while (nctas < most && static_cast<long long>(nctas) * 8 * kRangesThreads < a.max_len) nctas *= 2;
+  return launch_per<8>(a, nctas, s);
 }
 
 }  // namespace g4
