@@ -561,9 +561,14 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
         }
       }
     }
+    if constexpr (MODS) {  // (scores that are all NaN leave no maximum behind)
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        if (ls[w * G + h] != ls[w * G + h]) Ls = ls[w * G + h];
+    }
     const int head = kvh * G + h;
     if (a.nsplit == 1) {
-      const float val = (Ls > 0.0f) ? O / Ls : 0.0f;
+      const float val = (MODS ? Ls != 0.0f : Ls > 0.0f) ? O / Ls : 0.0f;  // (MODS: a NaN stays one)
       T* dst = static_cast<T*>(a.out) + (static_cast<size_t>(bt) * a.H + head) * HD + d;
       store_elems<1>(dst, &val);
     } else {

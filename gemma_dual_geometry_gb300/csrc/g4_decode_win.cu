@@ -442,8 +442,9 @@ __global__ void __launch_bounds__(kWinThreads, (WinCfg<HD, G>::MINB))
     float m = fmaxf(v0, v1);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float p0 = m == -INFINITY ? 0.0f : ex2_approx(v0 - m);
-    const float p1 = m == -INFINITY ? 0.0f : ex2_approx(v1 - m);
+    // (MODS: scores that are all NaN have no maximum, and stay NaN)
+    const float p0 = m == -INFINITY && !(MODS && v0 != v0) ? 0.0f : ex2_approx(v0 - m);
+    const float p1 = m == -INFINITY && !(MODS && v1 != v1) ? 0.0f : ex2_approx(v1 - m);
     const float l = warp_sum(p0 + p1);
     s_p[lane * G + h] = p0;
     s_p[(lane + 32) * G + h] = p1;

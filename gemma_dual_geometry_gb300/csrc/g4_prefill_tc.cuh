@@ -302,6 +302,62 @@ __device__ __forceinline__ void cap_scores(float (&s)[N], float cap_in, float ca
   }
 }
 
+// One row's output in NC columns again, without the tensor cores, where a key that the row does not see holds a NaN or
+// an infinity (its weight is zero, but zero times that is a NaN in the product): the warp forms the weights of the keys
+// that it does see, eight at a time, with the row's own base m, and adds their values up, two columns per lane.
+// inv_l: 1 / row sum.  Done once all columns are NaN: the row sees one itself.
+//   A warp has up to 32 such rows, and the others' bounded waits go on meanwhile, so rows of more than kAgainKeys keys
+// are left as they are.
+constexpr int kAgainKeys = 1 << 16;
+
+template <int HD, int NC>
+__device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int tok, int2 keys, int qpos, float slope,
+                                         float m, float inv_l, int col0) {
+  constexpr int KB = 8;
+  const int lane = threadIdx.x & 31;
+  const int kvh = h / (a.H / a.Hkv);
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<size_t>(b) * a.T + tok) * a.H + h) * HD;
+  const size_t head = (static_cast<size_t>(b) * a.Hkv + kvh) * a.max_len;
+  float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+  for (int j0 = keys.x; j0 < keys.y; j0 += KB) {
+    size_t row[KB];
+    float s[KB];
+    uint32_t v[KB];
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      const int j = min(j0 + i, keys.y - 1);
+      row[i] = (head + (a.ring ? j % a.max_len : j)) * HD;
+      s[i] = 0.0f;
+      v[i] = lane * 2 < NC ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.cv) + row[i] + col0 + lane * 2) : 0u;
+    }
+#pragma unroll 1
+    for (int d = lane * 2; d < HD; d += 64) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d);
+      uint32_t y[KB];
+#pragma unroll
+      for (int i = 0; i < KB; ++i) y[i] = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.ck) + row[i] + d);
+#pragma unroll
+      for (int i = 0; i < KB; ++i) s[i] = fmaf(bf16_lo(x), bf16_lo(y[i]), fmaf(bf16_hi(x), bf16_hi(y[i]), s[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) s[i] = warp_sum(s[i]);
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      float t = a.cap_log2 > 0.0f ? fmaf(-2.0f * a.cap_log2, rcp_approx(1.0f + ex2_approx(min_nan(s[i] * a.cap_in, 30.0f))), a.cap_log2)
+                                  : s[i] * a.scale_log2;
+      t = fmaf(-slope, fabsf(static_cast<float>(qpos - (j0 + i))), t);
+      const float p = bf16_lo(pack_bf16x2(ex2_approx(t - m), 0.0f));
+      if (j0 + i < keys.y) {
+        o.x = fmaf(p, bf16_lo(v[i]), o.x);
+        o.y = fmaf(p, bf16_hi(v[i]), o.y);
+      }
+    }
+    if (__all_sync(0xffffffffu, lane * 2 >= NC || (o.x != o.x && o.y != o.y))) break;
+  }
+  return make_float2(o.x * inv_l, o.y * inv_l);
+}
+
 // The softmax warps' work (16 warps; lane r of a quarter holds a row, four warps a quarter of its columns each).
 //   Item by item and tile by tile as in the causal kernel, from the last key tile to the first: a distance bias falls
 // from the diagonal on, so that the first tile's maximum is the largest and O need not be rescaled
@@ -497,6 +553,7 @@ __device__ __forceinline__ void softmax_mods(const ModsTcArgs& a, TcBars* bars, 
       warp_arrive(&bars->p_full[sb]);
     }
     if (!ok) break;
+    const Next done = cur;
     // The next item's keys are on their way while this one's output is finished.  (The producer has drawn it by now, or
     // does without waiting for any of this item's weights.)
     const bool more = fetch(n + 1, cur);
@@ -516,6 +573,7 @@ __device__ __forceinline__ void softmax_mods(const ModsTcArgs& a, TcBars* bars, 
 #pragma unroll
     for (int cc = 0; cc < NCC; ++cc) tmem_ld<kCW>(tmem_O + cc * kCW, o[cc]);
     tc_wait_ld();
+    uint32_t top = 0;  // largest magnitudes, as bits of bf16 pairs
 #pragma unroll
     for (int cc = 0; cc < NCC; ++cc) {
       // kCW columns, half of a 64-column chunk or less: pieces (16 bytes) from p0 on
@@ -527,11 +585,34 @@ __device__ __forceinline__ void softmax_mods(const ModsTcArgs& a, TcBars* bars, 
       for (int i = 0; i < kCW / 8; ++i) {
         uint32_t v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
           v[k] = pack_bf16x2(__uint_as_float(o[cc][8 * i + 2 * k]) * inv_l, __uint_as_float(o[cc][8 * i + 2 * k + 1]) * inv_l);
+          top = __vmaxu2(top, v[k] & 0x7fff7fffu);
+        }
         const uint32_t addr = row_addr + (((p0 + i) ^ (r & 7)) * 16);
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                      : "memory");
+      }
+    }
+    // Rows with a NaN or an infinity, if only from keys that they do not see.
+    // (Those whose sum is one have it from a key that they do.)
+    const bool odd = max(top & 0xffffu, top >> 16) >= 0x7f80u && inv_l == inv_l && done.keys.x < done.keys.y &&
+                     done.keys.y - done.keys.x <= kAgainKeys;
+    for (unsigned todo = __ballot_sync(0xffffffffu, odd); todo != 0; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const TcItem w = tc_item<C::NDH, kMods>(a, done.it, nqt);
+      const int2 keys = make_int2(__shfl_sync(0xffffffffu, done.keys.x, src), __shfl_sync(0xffffffffu, done.keys.y, src));
+      const int row = quarter * 32 + src;
+      const float2 v = row_again<HD, kDVP>(a, w.b, w.h, w.q0 + row, keys, __shfl_sync(0xffffffffu, done.qpos, src), done.slope,
+                                           __shfl_sync(0xffffffffu, m == -INFINITY ? 0.0f : m, src),
+                                           __shfl_sync(0xffffffffu, inv_l, src),
+                                           w.dh * C::DV + part * kDVP);
+      __syncwarp();  // (the row's first values are in place)
+      if (lane * 2 < kDVP) {
+        const int col = part * kDVP + lane * 2, ch = col / 64;
+        const uint32_t addr = sRing + oslot(ch / C::CPS) * C::SLOTB + (ch % C::CPS) * kChunkB + row * 128 +
+                              ((col % 64 / 8) ^ (row & 7)) * 16 + col % 8 * 2;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(pack_bf16x2(v.x, v.y)) : "memory");
       }
     }
     fence_proxy_async_smem();

@@ -28,7 +28,6 @@ namespace cg = cooperative_groups;
 
 // (1024 threads of 4 positions: 6.4 us against 5.8 at 8 rows of 32768; 256 of 16: 6.2)
 constexpr int kRangesThreads = 512;
-constexpr int kRangesMaxCtas = 16;
 constexpr int kRangesMaxTiles = 512;             // tiles per CTA: 2^24 positions over 8 CTAs
 constexpr int kNone = 0x7fffffff;
 

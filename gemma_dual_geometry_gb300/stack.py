@@ -3,7 +3,8 @@
 Owns the device buffers of a stack (one KV cache per layer that owns one,
 q_out scratch per head width, decode workspaces) and sequences the per-layer
 calls: g4_kv_append_normrope then g4_attn_prefill / g4_attn_decode (or
-g4_attn_encoder).  Sliding caches may be rings of one window.  Shared-KV
+g4_attn_encoder), with modified scores and positions of several axes where asked.
+Sliding caches may be rings of one window.  Shared-KV
 tail layers get no cache and read their source layer's
 (cortiq-engine g4e.rs `g4e_forward`: `src = kv_share_src.unwrap_or(li)`).
 ``PagedAttnStack`` is the same over the paged 4-bit cache: g4_kv4_assign_blocks
@@ -37,7 +38,8 @@ def _layers(cfg):
 
 
 class AttnStack:
-    def __init__(self, cfg, Lmax, device="cuda", B=None):
+    def __init__(self, cfg, Lmax, device="cuda", B=None, mods=False):
+        """``mods``: there will be decodes with modified scores (one more workspace)."""
         self.cfg = cfg
         self.B = cfg["B"] if B is None else B
         self.Lmax = Lmax
@@ -61,6 +63,10 @@ class AttnStack:
         for l, p in enumerate(self.params):
             nb = G.g4_attn_decode_workspace_size(p, self.B, Lmax)
             self.ws[l] = (torch.zeros(max(nb, 16), dtype=torch.uint8, device=self.device), nb)
+        self.mods_ws = None
+        if mods:  # serves all layers in turn
+            nb = max(G.g4_attn_decode_mods_workspace_size(p, self.B, Lmax) for p in self.params)
+            self.mods_ws = torch.zeros(max(nb, 16), dtype=torch.uint8, device=self.device)
 
     def owns(self, l):
         return self.src[l] < 0
@@ -68,18 +74,39 @@ class AttnStack:
     def cache_bytes(self):
         return sum(k.numel() * k.element_size() * 2 for k, _ in self.caches.values())
 
+    def visible_ranges(self, layer_type, q_start, seq_lens, doc_ids, span_ids, T, key_begin, key_end, stream=None):
+        """The intervals of keys of T tokens per sequence, for all layers of one type (ids are [B][Lmax])."""
+        window = next(g["window"] for g in self.geo if g["layer_type"] == layer_type) if layer_type == W.SLIDING else 0
+        G.g4_attn_visible_ranges(window, q_start, seq_lens, doc_ids, span_ids, self.Lmax, self.B, T, key_begin, key_end,
+                                 stream=stream)
+
+    def append_axes(self, l, axes, q, k, v, qw, kw, positions, rows, T, q_out, stream=None):
+        """append() with positions of several axes [n_axes][B][T], apart from the cache's rows [B][T]."""
+        G.g4_kv_append_normrope_axes(self.params[l], self.table, l, axes, q, k, v, qw, kw, positions,
+                                     rows if self.owns(l) else None, self.B, T, q_out, stream=stream)
+
     def append(self, l, q, k, v, qw, kw, positions, T, q_out, stream=None):
         G.g4_kv_append_normrope(self.params[l], self.table, l, q, k, v, qw, kw, positions, self.B, T, q_out,
                                 stream=stream)
 
-    def prefill_attn(self, l, q_out, q_start, T, out, stream=None):
+    def prefill_attn(self, l, q_out, q_start, T, out, stream=None, mods=None):
+        """``mods``: G.score_mods(), for modified scores."""
+        if mods is not None:
+            G.g4_attn_prefill_mods(self.params[l], self.table, l, mods, q_out, q_start, self.B, T, out, stream=stream)
+            return
         G.g4_attn_prefill(self.params[l], self.table, l, q_out, q_start, self.B, T, out, stream=stream)
 
     def encoder_attn(self, l, q_out, T, out, stream=None):
         """Bidirectional attention over the T tokens appended at positions 0..T-1."""
         G.g4_attn_encoder(self.params[l], self.table, l, q_out, self.B, T, out, stream=stream)
 
-    def decode_attn(self, l, q_out, seq_lens, max_seq_len, out, stream=None):
+    def decode_attn(self, l, q_out, seq_lens, max_seq_len, out, stream=None, mods=None):
+        if mods is not None:
+            if self.mods_ws is None:
+                raise ValueError("the stack was made without mods")
+            G.g4_attn_decode_mods(self.params[l], self.table, l, mods, q_out, seq_lens, self.B, max_seq_len, out,
+                                  self.mods_ws, self.mods_ws.numel(), stream=stream)
+            return
         ws, nb = self.ws[l]
         G.g4_attn_decode(self.params[l], self.table, l, q_out, seq_lens, self.B, max_seq_len, out, ws, nb,
                          stream=stream)

@@ -630,9 +630,11 @@ g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_
  * g4_attn_prefill with modified scores (mods NULL: none).  Arguments, caches, limits on
  * launches in flight and errors as there, with these differences:
  *   - q_start_pos is clamped into [0, 2^31 - 1 - T].
- *   - Positions at or past the end of every interval of 128 queries in a row (those of a
- *     tile) may hold anything, as may those before all of them: a padded
- *     batch's unwritten rows need no values.
+ *   - A position reaches the queries that see it and no others, whatever it holds: a
+ *     padded batch's unwritten rows need no values, and a NaN or an infinity in one
+ *     document stays there.  (bf16 rows of up to 65536 keys: those that share a tile with
+ *     one that they do not see are formed again on CUDA cores, which takes long.
+ *     Longer rows become NaN.)
  *   - On a ring, positions that it no longer holds count as absent; with key_begin
  *     NULL the window has to fit as there.
  */
