@@ -41,8 +41,8 @@
 //                                        TMEM, B = V_j MN-major)
 //               in the order QK_0, QK_1, PV_0, QK_2, PV_1, ... so the score
 //               MMA of the next tile overlaps the softmax of this one.
-//   warps 2-9   softmax (MODS: 2-17, quarters of a row instead of halves): two warps per TMEM lane quarter (a warp may only
-//               touch its quarter's 32 lanes), each thread half a query row
+//   warps 2-9   softmax (MODS: 2-17, quarters of a row instead of halves):
+//               two warps per TMEM lane quarter (a warp may only touch its quarter's 32 lanes), each thread half a query row
 //               (64 of the 128 score columns; TMEM lane = row): load the
 //               whole S row with tcgen05.ld (both threads of a row find the
 //               same maximum), mask (one visible key interval per row:
@@ -154,7 +154,8 @@ struct TcBars {
   int kbeg[4], kend[4];  // MODS: the keys that some row of the item sees, [kbeg, kend)
   uint32_t tmem_base;
   int abort;
-  alignas(16) int raise[2][4][kModsParts];  // MODS: [tile parity][lane quarter][part]: number of the tile whose maximum it wants raised
+  // MODS: [tile parity][lane quarter][part]: number of the tile whose maximum it wants raised
+  alignas(16) int raise[2][4][kModsParts];
   float red[kModsParts][kBM];   // [part of the columns][row]: row-sum shares; MODS: row maxima too
 };
 static_assert(sizeof(TcBars) <= 3072, "barrier block");
@@ -317,6 +318,8 @@ __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int 
   const int lane = threadIdx.x & 31;
   const int kvh = h / (a.H / a.Hkv);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<size_t>(b) * a.T + tok) * a.H + h) * HD;
+  const __nv_bfloat16* ck = static_cast<const __nv_bfloat16*>(a.ck);
+  const __nv_bfloat16* cv = static_cast<const __nv_bfloat16*>(a.cv) + col0;
   const size_t head = (static_cast<size_t>(b) * a.Hkv + kvh) * a.max_len;
   float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll 1
@@ -329,14 +332,14 @@ __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int 
       const int j = min(j0 + i, keys.y - 1);
       row[i] = (head + (a.ring ? j % a.max_len : j)) * HD;
       s[i] = 0.0f;
-      v[i] = lane * 2 < NC ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.cv) + row[i] + col0 + lane * 2) : 0u;
+      v[i] = lane * 2 < NC ? *reinterpret_cast<const uint32_t*>(cv + row[i] + lane * 2) : 0u;
     }
 #pragma unroll 1
     for (int d = lane * 2; d < HD; d += 64) {
       const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d);
       uint32_t y[KB];
 #pragma unroll
-      for (int i = 0; i < KB; ++i) y[i] = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.ck) + row[i] + d);
+      for (int i = 0; i < KB; ++i) y[i] = *reinterpret_cast<const uint32_t*>(ck + row[i] + d);
 #pragma unroll
       for (int i = 0; i < KB; ++i) s[i] = fmaf(bf16_lo(x), bf16_lo(y[i]), fmaf(bf16_hi(x), bf16_hi(y[i]), s[i]));
     }
@@ -344,8 +347,9 @@ __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int 
     for (int i = 0; i < KB; ++i) s[i] = warp_sum(s[i]);
 #pragma unroll
     for (int i = 0; i < KB; ++i) {
-      float t = a.cap_log2 > 0.0f ? fmaf(-2.0f * a.cap_log2, rcp_approx(1.0f + ex2_approx(min_nan(s[i] * a.cap_in, 30.0f))), a.cap_log2)
-                                  : s[i] * a.scale_log2;
+      float t = s[i] * a.scale_log2;
+      if (a.cap_log2 > 0.0f)
+        t = fmaf(-2.0f * a.cap_log2, rcp_approx(1.0f + ex2_approx(min_nan(s[i] * a.cap_in, 30.0f))), a.cap_log2);
       t = fmaf(-slope, fabsf(static_cast<float>(qpos - (j0 + i))), t);
       const float p = bf16_lo(pack_bf16x2(ex2_approx(t - m), 0.0f));
       if (j0 + i < keys.y) {
