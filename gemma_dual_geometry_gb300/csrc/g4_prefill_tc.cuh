@@ -188,7 +188,7 @@ struct TcItem {
   int kbeg;  // MODS only: the first key that some row sees (Lk: one past the last one)
 };
 
-// MODS: the interval of keys that row r of the item sees (empty: lo >= hi).
+// MODS: the interval of keys that row r of the item sees (empty: 0, 0).
 __device__ __forceinline__ int2 tc_row_keys(const ModsTcArgs& a, const TcItem& w, int r) {
   if (r >= w.valid_rows) return make_int2(0, 0);
   const int q_start = min(max(a.q_start[w.b], 0), 0x7fffffff - a.T);
@@ -198,7 +198,9 @@ __device__ __forceinline__ int2 tc_row_keys(const ModsTcArgs& a, const TcItem& w
   int lo = a.sliding ? pos - a.window + 1 : 0, hi = pos + 1;
   if (a.key_begin != nullptr) lo = a.key_begin[tok];
   if (a.key_end != nullptr) hi = a.key_end[tok];
-  return make_int2(max(lo, a.ring ? max(0, held - a.max_len) : 0), min(hi, held));
+  lo = max(lo, a.ring ? max(0, held - a.max_len) : 0);
+  hi = min(hi, held);
+  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);  // (ends from -2^31 on do not come into any difference)
 }
 
 // MODS: the keys of an item, known to the producer that drew it.
@@ -305,22 +307,36 @@ __device__ __forceinline__ void cap_scores(float (&s)[N], float cap_in, float ca
 
 // One row's output in NC columns again, without the tensor cores, where a key that the row does not see holds a NaN or
 // an infinity (its weight is zero, but zero times that is a NaN in the product): the warp forms the weights of the keys
-// that it does see, eight at a time, with the row's own base m, and adds their values up, two columns per lane.
+// that it does see, several at a time, with the row's own base m, and adds their values up, two columns per lane.
 // inv_l: 1 / row sum.  Done once all columns are NaN: the row sees one itself.
-//   A warp has up to 32 such rows, and the others' bounded waits go on meanwhile, so rows of more than kAgainKeys keys
-// are left as they are.
-constexpr int kAgainKeys = 1 << 16;
+//   A warp has up to 32 such rows (of 16384 keys 307 ms at head_dim 512, 158 at 128), and the others' bounded waits go on
+// meanwhile, so rows of more than kAgainKeys keys are left as they are.
+constexpr int kAgainKeys = 1 << 15;
 
 template <int HD, int NC>
 __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int tok, int2 keys, int qpos, float slope,
                                          float m, float inv_l, int col0) {
-  constexpr int KB = 8;
+  constexpr int KB = HD < 256 ? 8 : 4;  // keys at a time
+  constexpr int W = HD / 64 < 4 ? HD / 64 : 4;  // 32-bit words of a row that a lane loads at once
+  constexpr int NW = HD / 64 / W;
   const int lane = threadIdx.x & 31;
   const int kvh = h / (a.H / a.Hkv);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<size_t>(b) * a.T + tok) * a.H + h) * HD;
   const __nv_bfloat16* ck = static_cast<const __nv_bfloat16*>(a.ck);
   const __nv_bfloat16* cv = static_cast<const __nv_bfloat16*>(a.cv) + col0;
   const size_t head = (static_cast<size_t>(b) * a.Hkv + kvh) * a.max_len;
+  auto load = [&](const __nv_bfloat16* row, int n, uint32_t (&x)[W]) {
+    const __nv_bfloat16* from = row + (n * 32 + lane) * 2 * W;
+    if constexpr (W == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(from);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else if constexpr (W == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      x[0] = v.x; x[1] = v.y;
+    } else {
+      x[0] = *reinterpret_cast<const uint32_t*>(from);
+    }
+  };
   float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll 1
   for (int j0 = keys.x; j0 < keys.y; j0 += KB) {
@@ -335,13 +351,15 @@ __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int 
       v[i] = lane * 2 < NC ? *reinterpret_cast<const uint32_t*>(cv + row[i] + lane * 2) : 0u;
     }
 #pragma unroll 1
-    for (int d = lane * 2; d < HD; d += 64) {
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d);
-      uint32_t y[KB];
+    for (int n = 0; n < NW; ++n) {
+      uint32_t x[W], y[KB][W];
+      load(q, n, x);
 #pragma unroll
-      for (int i = 0; i < KB; ++i) y[i] = *reinterpret_cast<const uint32_t*>(ck + row[i] + d);
+      for (int i = 0; i < KB; ++i) load(ck + row[i], n, y[i]);
 #pragma unroll
-      for (int i = 0; i < KB; ++i) s[i] = fmaf(bf16_lo(x), bf16_lo(y[i]), fmaf(bf16_hi(x), bf16_hi(y[i]), s[i]));
+      for (int i = 0; i < KB; ++i)
+#pragma unroll
+        for (int w = 0; w < W; ++w) s[i] = fmaf(bf16_lo(x[w]), bf16_lo(y[i][w]), fmaf(bf16_hi(x[w]), bf16_hi(y[i][w]), s[i]));
     }
 #pragma unroll
     for (int i = 0; i < KB; ++i) s[i] = warp_sum(s[i]);
@@ -600,8 +618,7 @@ __device__ __forceinline__ void softmax_mods(const ModsTcArgs& a, TcBars* bars, 
     }
     // Rows with a NaN or an infinity, if only from keys that they do not see.
     // (Those whose sum is one have it from a key that they do.)
-    const bool odd = max(top & 0xffffu, top >> 16) >= 0x7f80u && inv_l == inv_l && done.keys.x < done.keys.y &&
-                     done.keys.y - done.keys.x <= kAgainKeys;
+    const bool odd = max(top & 0xffffu, top >> 16) >= 0x7f80u && inv_l == inv_l && done.keys.y - done.keys.x <= kAgainKeys;
     for (unsigned todo = __ballot_sync(0xffffffffu, odd); todo != 0; todo &= todo - 1) {
       const int src = __ffs(todo) - 1;
       const TcItem w = tc_item<C::NDH, kMods>(a, done.it, nqt);

@@ -632,7 +632,7 @@ g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_
  *   - q_start_pos is clamped into [0, 2^31 - 1 - T].
  *   - A position reaches the queries that see it and no others, whatever it holds: a
  *     padded batch's unwritten rows need no values, and a NaN or an infinity in one
- *     document stays there.  (bf16 rows of up to 65536 keys: those that share a tile with
+ *     document stays there.  (bf16 rows of up to 32768 keys: those that share a tile with
  *     one that they do not see are formed again on CUDA cores, which takes long.
  *     Longer rows become NaN.)
  *   - On a ring, positions that it no longer holds count as absent; with key_begin

@@ -88,6 +88,48 @@ def test_prefill_rows_formed_again_are_right(geo, cap, bias):
     assert np.isnan(f64(out)[:, ~clean]).all()
 
 
+@pytest.mark.parametrize("geo", GEOS)
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+def test_prefill_rows_that_see_nothing_are_zero(geo, dtype):
+    """Empty intervals (of all kinds) among rows that see NaN and infinities, of queries that are NaN themselves."""
+    T = 140
+    c = Case(geo, [T], T, dtype, 4)
+    c.dv[0, :, 10] = float("nan")
+    c.dv[0, :, 20] = float("-inf")
+    c.dk[0, :, 30] = float("inf")
+    q = unit((1, T, geo[2], geo[1]), 2, dtype).to(DEV)
+    begin, end = np.zeros((1, T), int), np.full((1, T), 60)
+    empty = np.arange(T) % 3 == 0
+    begin[0, empty] = np.resize([0, 60, 500, 2 ** 31 - 1, 50, -3, 0, -2 ** 31, 2 ** 31 - 1], empty.sum())
+    end[0, empty] = np.resize([0, 60, 3, -2 ** 31, 40, -3, -2 ** 31, -2 ** 31 + 1, 2 ** 31 - 1], empty.sum())
+    q[0, 3] = float("nan")
+    out = torch.empty_like(q)
+    G.g4_attn_prefill_mods(c.params, c.table, 0, G.score_mods(0.0, None, i32(begin), i32(end)), q, i32([0]), 1, T, out)
+    assert (f64(out)[0, empty] == 0).all() and np.isnan(f64(out)[0, ~empty]).all()
+
+
+@pytest.mark.parametrize("n", [32768, 32769])
+def test_prefill_rows_too_long_to_form_again(n):
+    """Rows of up to 2^15 keys are formed again, longer ones are NaN, as documented; other tiles are as they were."""
+    geo, T = (W.FULL, 64, 2, 1, 0), 256
+    c = Case(geo, [n + 200], n + 200, W.BF16, 7)
+    c.dv[:, :, n + 1] = float("nan")
+    q = unit((1, T, 2, 64), 8, W.BF16)
+    begin, end = np.full((1, T), 1), np.full((1, T), n + 1)
+    end[0, :100] = n + 2   # (the first tile's only)
+    begin[0, :100] = n + 1
+    out = torch.empty_like(q, device=DEV)
+    mods = G.score_mods(0.0, None, i32(begin), i32(end))
+    G.g4_attn_prefill_mods(c.params, c.table, 0, mods, q.to(DEV), i32([n - 100]), 1, T, out)
+    got = f64(out)
+    assert np.isnan(got[0, :100]).all() and np.isnan(got[0, 100:128]).all() == (n > 32768)
+    some = [100, 127, 128, 255] if n <= 32768 else [128, 255]
+    c.v[:, :, n + 1] = 0.0
+    at = (n - 100 + np.arange(T))[None, some]
+    want, mass, size = c.reference(f64(q)[:, some], at, begin[:, some], end[:, some], [n + 200], 0.0, None)
+    check(got[:, some], want, mass, size, c.g, n, 0.0, True, n)
+
+
 @pytest.mark.parametrize("geo,lens", [(GEOS[0], [100, 300]), (GEOS[1], [300, 90]), (GEOS[2], [700, 260]),
                                       (GEOS[3], [30, 200])])
 @pytest.mark.parametrize("dtype", [W.BF16, W.F32])
@@ -365,3 +407,65 @@ def test_no_mods_are_the_plain_calls_within_their_rounding():
     G.g4_attn_decode_mods(c.params, c.table, 0, None, q[:, -1].contiguous().to(DEV), i32([300, 200]), 2, 300, d, ws, n)
     want, mass, size = c.reference(f64(q)[:, -1:], at[:, -1:], lo[:, -1:], hi[:, -1:], [300, 200], 0.0, None)
     check(f64(d)[:, None], want, mass, size, c.g, 300, 0.0, False, "none")
+
+
+def test_intervals_straight_into_the_attention():
+    """Each call right behind the one that writes its intervals, with the documents changed in between: as with a
+    synchronisation."""
+    geo, B, T, L = GEOS[1], 3, 40, 900
+    c = Case(geo, [L] * B, L, W.BF16, 3)
+    rng = np.random.default_rng(2)
+    q = unit((B, T, geo[2], geo[1]), 5, W.BF16).to(DEV)
+    size = G.g4_attn_decode_mods_workspace_size(c.params, B, L)
+    ws = torch.zeros(max(16, size), dtype=torch.uint8, device=DEV)
+    doc, lens, start = i32(np.zeros((B, L))), i32([0] * B), i32([0] * B)
+    begin, end, last = i32(np.zeros((B, T))), i32(np.zeros((B, T))), i32([0] * B)
+    one, one_end = i32(np.zeros((B, 1))), i32(np.zeros((B, 1)))
+    for _ in range(12):
+        n = rng.integers(T, L + 1, B)
+        doc.copy_(i32(np.cumsum(rng.random((B, L)) < 0.01, 1)))
+        lens.copy_(i32(n))
+        start.copy_(i32(n - T))
+        last.copy_(i32(n - 1))
+        outs = []
+        for wait in (False, True):
+            outs.append([torch.empty_like(q), torch.empty_like(q[:, 0])])
+            begin.zero_(), end.zero_(), one.zero_()
+            torch.cuda.synchronize()
+            G.g4_attn_visible_ranges(0, start, lens, doc, None, L, B, T, begin, end)
+            if wait:
+                torch.cuda.synchronize()
+            G.g4_attn_prefill_mods(c.params, c.table, 0, G.score_mods(0.0, None, begin, end), q, start, B, T, outs[-1][0])
+            G.g4_attn_visible_ranges(0, last, lens, doc, None, L, B, 1, one, one_end)
+            if wait:
+                torch.cuda.synchronize()
+            G.g4_attn_decode_mods(c.params, c.table, 0, G.score_mods(0.0, None, one.view(B)), q[:, -1].contiguous(), lens, B,
+                                  L, outs[-1][1], ws, size)
+            torch.cuda.synchronize()
+        for a, b in zip(*outs):
+            assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
+def test_two_streams_at_once():
+    """Prefills and decodes (a workspace each) on two streams at a time give what they give alone."""
+    geo, T, L = GEOS[4], 700, 900
+    c = Case(geo, [L, L], L, W.BF16, 3)
+    size = G.g4_attn_decode_mods_workspace_size(c.params, 2, L)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    qs = [unit((2, T, geo[2], geo[1]), 5 + i, W.BF16).to(DEV) for i in range(2)]
+    last = [q[:, -1].contiguous() for q in qs]
+    starts, lens = [i32([200, 100]), i32([0, 150])], [i32([900, 800]), i32([300, 5])]
+    mods = [G.score_mods(30.0), G.score_mods(0.0, torch.tensor(SLOPES(geo[2]), dtype=torch.float32, device=DEV))]
+    spaces = [torch.zeros(max(16, size), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [[(torch.empty_like(q), torch.empty_like(x)) for q, x in zip(qs, last)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for turn, pair in enumerate(outs):
+        for i, (o, d) in enumerate(pair):
+            G.g4_attn_prefill_mods(c.params, c.table, 0, mods[i], qs[i], starts[i], 2, T, o, stream=streams[i])
+            G.g4_attn_decode_mods(c.params, c.table, 0, mods[i], last[i], lens[i], 2, L, d, spaces[i], size, stream=streams[i])
+            if turn == 0:
+                torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    for pair in outs[1:]:
+        for (o, d), (o0, d0) in zip(pair, outs[0]):
+            assert torch.equal(o, o0) and torch.equal(d, d0)
