@@ -105,7 +105,8 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[NP], int lane) {
   return r;
 }
 
-template <typename T, int HD, int G, int NW_>
+// NPM: partial scores per reduce-scatter batch, at most.
+template <typename T, int HD, int G, int NW_, int NPM = kNPMax>
 struct SimtCfg {
   static constexpr int NW = NW_;                     // warps per CTA
   static constexpr int ES = sizeof(T);
@@ -114,8 +115,8 @@ struct SimtCfg {
   static constexpr int PE = EL < CHE ? EL : CHE;     // elements per piece a lane reads
   static constexpr int NPC = EL / PE;                // pieces per lane per row
   static constexpr int ROWB = HD * ES;               // bytes per cache row
-  static constexpr int KB_G = kNPMax / G;
-  static constexpr int KB_B = kStageMaxB / ROWB;
+  static constexpr int KB_G = NPM / G;
+  static constexpr int KB_B = (NPM > kNPMax && ROWB <= 256 ? 2048 : kStageMaxB) / ROWB;
   static constexpr int KB = KB_G < KB_B ? KB_G : KB_B;  // keys per reduce batch
   static constexpr int NP = KB * G;                  // partial scores per batch (2..16)
   static constexpr int NB = (KB * ROWB >= 2048) ? 1 : 2048 / (KB * ROWB);  // batches per stage
@@ -139,7 +140,7 @@ struct SimtCfg {
   static constexpr int QN_OFF = FLAG_OFF + 16;  // normed q of the G heads (fused step)
   static constexpr int KN_OFF = QN_OFF + G * HD * ES;  // normed new k and v (fused step)
   static constexpr int SMEM_B = KN_OFF + 2 * HD * ES;
-  static_assert(NP >= 2 && NP <= 16 && (NP & (NP - 1)) == 0, "reduce batch");
+  static_assert(NP >= 2 && NP <= NPM && (NP & (NP - 1)) == 0, "reduce batch");
   static_assert(SMEM_B <= 232448, "shared memory budget");
 };
 

@@ -19,10 +19,13 @@
 // Measured (device time; copy rate 6.78 TB/s): head_dim 512, 8 heads on 2, 64 sequences
 // of 1024 to 8192 keys, capped 196 us, 6.2 TB/s (237 with equal splits of the longest length); 4 of
 // 131072 with a bias that begin anywhere 250 us, 5.8 TB/s (311); 8 of 4097 36 us, 3.7 TB/s.
-//   What bounds it: at head_dim 512 the bytes; at 128 and below instruction issue (each
-// key's partial products are reduced over the warp); with few keys the start (lengths,
+// 64 sequences of 1024 to 8192 keys of 256 101 us, 6.0 TB/s; of 128 63 us, 4.8 TB/s.
+//   What bounds it: at head_dim 512 and 256 with up to 4 heads per kv head, and with one or two at any, the bytes; otherwise
+// instruction issue (each key's partial products are reduced over the warp); with few keys the start (lengths,
 // scans, first copies) and the merges, some 10 us.
 #include <math.h>
+
+#include <algorithm>
 
 #include "g4_attn_simt.cuh"
 
@@ -44,6 +47,20 @@ constexpr int kCutShift = 3;
 // The slot of a unit's part i, left by CTA c_first + i: the second of its two
 // where the unit begins, else the first.
 __device__ __forceinline__ int part_slot(int c_first, int i) { return 2 * (c_first + i) + (i == 0 ? 1 : 0); }
+
+// CTAs per SM: two where q and O of the group take some 180 registers of a thread, three otherwise; four for rows of up to
+// 256 bytes, whose stages are short (64 x 1024 .. 8192 keys, four against three, with batches of 16: head_dim 128, 4 heads
+// 74 us against 81, head_dim 64 93 against 97; head_dim 256, 2 heads 219 against 184; five or six are slower throughout).
+constexpr int resident_ctas(int warps, int group_width, int row_bytes) {
+  return warps > 4 ? 1 : group_width >= 2048 ? 2 : group_width > 512 || row_bytes > 256 ? 3 : 4;
+}
+
+// Scores that a warp sums over its lanes at a time, for rows of ROWB bytes.  32 where they are short: every lane has a
+// score of its own, and twice the keys share a batch's fixed costs (64 x 1024 .. 8192 keys, 32 against 16: head_dim 128, 4
+// heads per kv head 63 us against 74, 8 heads 105 against 128; head_dim 256, 4 heads 101 against 119, 8 heads 185 against 229;
+// 256 windows of 512 keys of 256 57 against 65).  Rows of 1 KB would need stages of 8 KB, and so a CTA less per SM.
+template <int ROWB>
+constexpr int kBatch = ROWB <= 512 ? 32 : kNPMax;
 
 // The keys of one sequence.
 struct SeqKeys {
@@ -70,16 +87,16 @@ struct Tail {
   long long scan[NW];
   long long unit0;           // keys before the run's unit
   Run run;
-  float sc[NW][kNPMax];
+  float sc[NW][32];  // (kBatch, at most)
   float sa[NW][8];
   float ml[2][G];
   int last;
 };
 
 template <typename T, int HD, int G, int NW>
-__global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
+__global__ void __launch_bounds__(NW * 32, resident_ctas(NW, G * HD, HD * sizeof(T)))
     decode_mods_kernel(const __grid_constant__ ModsDecodeArgs a) {
-  using C = SimtCfg<T, HD, G, NW>;
+  using C = SimtCfg<T, HD, G, NW, kBatch<HD * sizeof(T)>>;
   constexpr int EL2 = C::EL / 2;
   constexpr int NT = NW * 32;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -446,7 +463,7 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
 
 template <typename T, int HD, int G, int NW>
 cudaError_t launch_w(const ModsDecodeArgs& a, cudaStream_t s) {
-  using C = SimtCfg<T, HD, G, NW>;
+  using C = SimtCfg<T, HD, G, NW, kBatch<HD * sizeof(T)>>;
   constexpr int smem = C::AREA_B + sizeof(Tail<NW, C::NST, G>);
   const cudaError_t e = set_smem_limit_once<decode_mods_kernel<T, HD, G, NW>>(smem);
   if (e != cudaSuccess) return e;
@@ -517,7 +534,8 @@ ModsDecodePlan mods_decode_plan(int dtype, int window, int hd, int H, int Hkv, i
   // .. 2000 of 512 62 against 64, 4 x 131072 of 512 250 against 263).
   const bool wide = hd * (dtype == 1 ? 2 : 4) >= 1024 && 2 * units <= sm_count() && units * span <= 4096LL * sm_count();
   p.warps = most <= sm_count() || wide ? 8 : 4;
-  const int resident = p.warps == 8 ? 1 : G * hd >= 2048 ? 2 : 3;  // per SM (SimtCfg::MINB)
+  // (few units have more parts to merge then: 1 x 30000 keys of head_dim 128 17.7 us with four CTAs per SM, 16.0 with three)
+  const int resident = std::min(units < 32 ? 3 : 4, resident_ctas(p.warps, G * hd, hd * (dtype == 1 ? 2 : 4)));
   const long long slots = static_cast<long long>(sm_count()) * resident;
   p.nctas = static_cast<int>(most < slots ? most : slots);
   if (p.nctas > kMaxCtas) p.nctas = kMaxCtas;
