@@ -151,8 +151,12 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(NW, G * HD, HD * sizeof
     }
     long long at = scan(sum, total) * a.Hkv;  // keys before this thread's sequences
     total *= a.Hkv;
-    share = max(static_cast<long long>(kMinShare), (total + nctas - 1) / nctas);
-    const long long cut = nctas > units ? max(static_cast<long long>(kMinShare), (total + nctas - units - 1) / (nctas - units)) : 0;
+    // (where there are units enough for all CTAs, starting them is the work)
+    share = max(units < nctas ? static_cast<long long>(kMinShare) : 1LL, (total + nctas - 1) / nctas);
+    // (with a CTA for every unit and none of more than kMinShare keys, 300 keys of 75 units were 5 shares: 42 us)
+    const long long cut = nctas > units ? max(static_cast<long long>(kMinShare), (total + nctas - units - 1) / (nctas - units))
+                          : nctas == units && (a.window > 0 ? min(a.window, a.len_cap) : a.len_cap) <= kMinShare ? kMinShare
+                                                                                                                 : 0;
     cut_units = cut > 0 && cut <= share + (share >> kCutShift);
     if (cut_units) {
       // parts of `cut` keys, the last of a unit fewer: at most total / cut + units <= nctas of them

@@ -469,3 +469,22 @@ def test_two_streams_at_once():
     for pair in outs[1:]:
         for (o, d), (o0, d0) in zip(pair, outs[0]):
             assert torch.equal(o, o0) and torch.equal(d, d0)
+
+
+@pytest.mark.parametrize("geo", [GEOS[1], GEOS[2], GEOS[3], (W.FULL, 256, 3, 3, 0)])
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+@pytest.mark.parametrize("B,most", [(70, 5), (70, 64), (70, 65), (610, 5), (610, 40)])
+def test_decode_of_many_short_sequences(geo, dtype, B, most):
+    """A CTA for every unit, or more units than CTAs; sequences of no, one and up to `most` keys."""
+    lens = [i % (most + 1) for i in range(B)]
+    c = Case(geo, [max(1, n) for n in lens], most, dtype, 12)
+    q = unit((B, geo[2], geo[1]), 3, dtype)
+    size = G.g4_attn_decode_mods_workspace_size(c.params, B, most)
+    ws = torch.zeros(max(16, size), dtype=torch.uint8, device=DEV)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device=DEV)
+    begin = [n // 3 for n in lens]
+    G.g4_attn_decode_mods(c.params, c.table, 0, G.score_mods(9.0, None, i32(begin)), q.to(DEV), i32(lens), B, most, out, ws, size)
+    at = np.asarray(lens)[:, None] - 1
+    lo, hi = M.default_intervals(at, geo[0], geo[4])
+    want, mass, mag = c.reference(f64(q)[:, None], at, np.maximum(lo, np.asarray(begin)[:, None]), hi, lens, 9.0, None)
+    check(f64(out)[:, None], want, mass, mag, c.g, most, 9.0, False, geo)
