@@ -119,7 +119,7 @@ struct TcCfg {
   static constexpr int OSLOTS = (DV / 64) / CPS;
   static constexpr int Q_OFF = 0;
   static constexpr int RING_OFF = Q_OFF + QCH * kChunkB;
-  static constexpr int BAR_B = 3072;
+  static constexpr int BAR_B = 3 * 1024;
   static constexpr int NSLOT_FIT = (kSmemMax - BAR_B - RING_OFF) / SLOTB;
   static constexpr int NSLOT = NSLOT_FIT < kMaxSlots ? NSLOT_FIT : kMaxSlots;
   static constexpr int BAR_OFF = RING_OFF + NSLOT * SLOTB;
@@ -158,7 +158,7 @@ struct TcBars {
   alignas(16) int raise[2][4][kModsParts];
   float red[kModsParts][kBM];   // [part of the columns][row]: row-sum shares; MODS: row maxima too
 };
-static_assert(sizeof(TcBars) <= 3072, "barrier block");
+static_assert(sizeof(TcBars) <= TcCfg<64>::BAR_B, "barrier block");
 
 // All 256 softmax threads meet (named barrier 1) and learn whether any of
 // them passed a nonzero flag.

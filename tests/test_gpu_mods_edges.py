@@ -292,7 +292,8 @@ def test_a_prompt_with_images_and_its_answer(dtype, side_stream):
             begin, end = M.visible_ranges(g["window"], now[:, 0], lens + s, doc, None, Lmax, 1)
             p = np.stack([now, now // 2, now % 7])
             want, mass, size = attend(l, append(l, s, p, now), now, begin, end, lens + s)
-            check(f64(step_outs[l, s])[:, None], want, mass * (1.0 if dtype == W.BF16 else 8.0), size, g, Lmax, cap, False, ("step", s, l))
+            check(f64(step_outs[l, s])[:, None], want, mass * (1.0 if dtype == W.BF16 else 8.0), size, g, Lmax,
+                  cap, False, ("step", s, l))
 
 
 # ---------------------------------------------------------------- graphs, streams, workspaces
