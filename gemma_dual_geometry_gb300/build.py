@@ -25,7 +25,7 @@ SOURCES = ["g4_api.cu", "g4_append.cu", "g4_append_axes.cu", "g4_attn_mods.cu", 
            "g4_decode_win.cu", "g4_gemm_tc.cu",
            "g4_kv4_cache.cu", "g4_kv4_decode.cu", "g4_prefill_mods.cu", "g4_prefill_tc.cu", "g4_ranges.cu"]
 HEADERS = ["g4_attn_simt.cuh", "g4_device.cuh", "g4_internal.h", "g4_kv4.cuh", "g4_kv4_internal.h", "g4_normrope.cuh",
-           "g4_prefill_tc.cuh"]
+           "g4_prefill_tc.cuh", "g4_tiles.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

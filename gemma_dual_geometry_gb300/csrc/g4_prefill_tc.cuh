@@ -74,6 +74,7 @@
 
 #include "g4_device.cuh"
 #include "g4_internal.h"
+#include "g4_tiles.h"
 
 namespace g4 {
 namespace {
@@ -208,7 +209,7 @@ __device__ __forceinline__ void tc_set_keys(TcItem& w, int kbeg, int kend) {
   w.kbeg = kbeg;
   w.Lk = kend;
   w.kt_begin = kbeg / kBN;
-  w.ntiles = kend > kbeg ? (kend + kBN - 1) / kBN - w.kt_begin : 0;
+  w.ntiles = kend > kbeg ? tiles_before(kend, kBN) - w.kt_begin : 0;
 }
 
 template <int NDH, int MODE, typename Args>
@@ -250,7 +251,7 @@ __device__ __forceinline__ TcItem tc_item(const Args& a, int it, int nqt) {
     kbeg = a.sliding ? max(0, w.qpos_first - a.window + 1) : 0;
   }
   w.kt_begin = kbeg / kBN;
-  w.ntiles = max(0, (kend + kBN - 1) / kBN - w.kt_begin);
+  w.ntiles = max(0, tiles_before(kend, kBN) - w.kt_begin);
   return w;
 }
 
@@ -1002,10 +1003,8 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
               fence_proxy_async_smem();
               __syncwarp();
             };
-            if (key0 + C::VKP > w.Lk) {
-              const int nvalid = max(0, w.Lk - key0);
-              zero_keys(nvalid, C::VKP - nvalid);
-            }
+            const int nvalid = keys_before(w.Lk, key0, C::VKP);
+            if (nvalid < C::VKP) zero_keys(nvalid, C::VKP - nvalid);
             if constexpr (MODS) {
               // and so may those before the first key that a row sees
               if (key0 < w.kbeg) zero_keys(0, min(C::VKP, w.kbeg - key0));
