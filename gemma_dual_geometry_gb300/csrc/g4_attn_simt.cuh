@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
     simt_stage<C, T, HD, G>(sk, sv, n, q2, o2, m_l, l_l, sc, sa, lane, [&](float s, int key) {
       if constexpr (MODS) {
         if (a.cap_log2 > 0.0f) s = a.cap_log2 * tanhf(s * inv_cap);
-        if (a.slopes != nullptr) s = fmaf(-slope, fabsf(static_cast<float>(qpos - (k0 + st_idx * C::SK + key))), s);
+        if (a.slopes != nullptr) s = fmaf(-slope, fabsf(static_cast<float>(qpos - k0 - st_idx * C::SK - key)), s);
       }
       return s;
     });

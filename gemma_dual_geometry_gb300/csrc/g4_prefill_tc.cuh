@@ -339,14 +339,16 @@ __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int 
     }
   };
   float2 o = make_float2(0.0f, 0.0f);
+  // (keys are counted from the row's first one: past the last one there may be no position)
+  const int nkeys = keys.y - keys.x;
 #pragma unroll 1
-  for (int j0 = keys.x; j0 < keys.y; j0 += KB) {
+  for (int j0 = 0; j0 < nkeys; j0 += KB) {
     size_t row[KB];
     float s[KB];
     uint32_t v[KB];
 #pragma unroll
     for (int i = 0; i < KB; ++i) {
-      const int j = min(j0 + i, keys.y - 1);
+      const int j = keys.x + min(j0 + i, nkeys - 1);
       row[i] = (head + (a.ring ? j % a.max_len : j)) * HD;
       s[i] = 0.0f;
       v[i] = lane * 2 < NC ? *reinterpret_cast<const uint32_t*>(cv + row[i] + lane * 2) : 0u;
@@ -369,9 +371,9 @@ __device__ __noinline__ float2 row_again(const ModsTcArgs& a, int b, int h, int 
       float t = s[i] * a.scale_log2;
       if (a.cap_log2 > 0.0f)
         t = fmaf(-2.0f * a.cap_log2, rcp_approx(1.0f + ex2_approx(min_nan(s[i] * a.cap_in, 30.0f))), a.cap_log2);
-      t = fmaf(-slope, fabsf(static_cast<float>(qpos - (j0 + i))), t);
+      t = fmaf(-slope, fabsf(static_cast<float>(qpos - keys.x - (j0 + i))), t);
       const float p = bf16_lo(pack_bf16x2(ex2_approx(t - m), 0.0f));
-      if (j0 + i < keys.y) {
+      if (j0 + i < nkeys) {
         o.x = fmaf(p, bf16_lo(v[i]), o.x);
         o.y = fmaf(p, bf16_hi(v[i]), o.y);
       }

@@ -75,3 +75,29 @@ def test_plain_chunks_at_the_last_positions(geo, T, rows):
     lo, hi = M.default_intervals(at, geo[0], geo[4])
     want, mass, size = c.reference(f64(q), at, lo, hi, starts + T, 0.0, None)
     check(f64(out), want, mass, size, c.g, rows, 0.0, True, (geo, T))
+
+
+@pytest.mark.parametrize("geo,T,rows", [n for n in NEAR if n[1] > 1])
+@pytest.mark.parametrize("start", ["last", 3000])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
+def test_rows_formed_again_on_a_ring(geo, T, rows, start, cap, bias):
+    """NaN and an infinity in the last keys' values, which some of a tile's queries see: the others' rows are right, up to
+    the last position (keys are counted in eights there), and where the ring wraps."""
+    start = LAST - T if start == "last" else start
+    c = ring(geo, 1, rows, W.BF16)
+    held = start + T
+    c.dv[0, :, (held - 1) % rows] = float("nan")
+    c.dv[0, :, (held - 20) % rows] = float("inf")
+    at = start + np.arange(T)
+    seen = np.where(np.arange(T) % 3 == 0, held, held - 1 - np.arange(T) % 3)[None]
+    seen = np.where((np.arange(T) % 5 == 0)[None], held - 20 - np.arange(T)[None] % 40, seen)
+    begin = np.where(np.arange(T) % 4 == 1, held - 19, held - np.minimum(rows, 60 + np.arange(T)))[None]
+    clean = ~((seen[0] == held) | ((begin[0] <= held - 20) & (seen[0] > held - 20)))
+    assert 0.2 < clean.mean() < 0.8
+    out, _, _ = run(c, [start], T, cap, bias, begin, seen, rows=np.flatnonzero(clean))
+    assert not np.isfinite(out[0, ~clean]).any()
+    # the causal form: the last token alone sees the last key
+    c.dv[0, :, (held - 20) % rows] = 1.0
+    c.v.copy_(c.dv)
+    out, _, _ = run(c, [start], T, cap, bias, rows=np.arange(T - 1))
+    assert np.isnan(out[0, T - 1]).all()
