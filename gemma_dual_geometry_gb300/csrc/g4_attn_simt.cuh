@@ -146,7 +146,9 @@ struct SimtCfg {
 
 // The n <= SK keys of a stage (K rows sk, V rows sv) into a warp's state: the heads' outputs o2 and, in the lanes
 // that hold head hh, its running maximum and sum.  modify(s, key) is what becomes of a score.
-template <typename C, typename T, int HD, int G, typename Modify>
+//   MODS: keys whose scores are all minus infinity weigh nothing, also where no other key has come yet (the exponential's
+// base is zero then, which leaves NaN as it is).
+template <typename C, typename T, int HD, int G, bool MODS, typename Modify>
 __device__ __forceinline__ void simt_stage(const T* sk, const T* sv, int n, const float2 (&q2)[G][C::EL / 2],
                                            float2 (&o2)[G][C::EL / 2], float& m_l, float& l_l, float* sc, float* sa,
                                            int lane, Modify modify) {
@@ -181,7 +183,7 @@ __device__ __forceinline__ void simt_stage(const T* sk, const T* sv, int n, cons
     for (int o = 1 << (kSh + ilog2(G)); o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     const float m_new = fmaxf(m_l, mb);
     const float alpha = (m_l == -INFINITY) ? 0.0f : ex2(m_l - m_new);
-    const float p_l = ex2(s_me - m_new);
+    const float p_l = ex2(s_me - (MODS && m_new == -INFINITY ? 0.0f : m_new));
     float ps = p_l;
 #pragma unroll
     for (int o = 1 << (kSh + ilog2(G)); o < 32; o <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(NW * 32, (SimtCfg<T, HD, G, NW>::MINB))
     const T* sk = reinterpret_cast<const T*>(ring + buf * 2 * C::STAGE_B);
     const T* sv = reinterpret_cast<const T*>(ring + buf * 2 * C::STAGE_B + C::STAGE_B);
 
-    simt_stage<C, T, HD, G>(sk, sv, n, q2, o2, m_l, l_l, sc, sa, lane, [&](float s, int key) {
+    simt_stage<C, T, HD, G, MODS>(sk, sv, n, q2, o2, m_l, l_l, sc, sa, lane, [&](float s, int key) {
       if constexpr (MODS) {
         if (a.cap_log2 > 0.0f) s = a.cap_log2 * tanhf(s * inv_cap);
         if (a.slopes != nullptr) s = fmaf(-slope, fabsf(static_cast<float>(qpos - k0 - st_idx * C::SK - key)), s);

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(NW, G * HD, HD * sizeof
       }
       const int kk0 = run.k0 + st_idx * C::SK;
       const T* sk = reinterpret_cast<const T*>(ring + buf * 2 * C::STAGE_B);
-      simt_stage<C, T, HD, G>(sk, sk + C::STAGE_B / C::ES, min(C::SK, run.k1 - kk0), q2, o2, m_l, l_l, sc, sa, lane,
+      simt_stage<C, T, HD, G, true>(sk, sk + C::STAGE_B / C::ES, min(C::SK, run.k1 - kk0), q2, o2, m_l, l_l, sc, sa, lane,
                               [&](float s, int key) {
                                 if (a.cap_log2 > 0.0f) s = a.cap_log2 * tanhf(s * inv_cap);
                                 if (a.slopes != nullptr) s = fmaf(-slope, static_cast<float>(run.L - 1 - kk0 - key), s);
