@@ -241,13 +241,16 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(NW, G * HD, HD * sizeof
   const int hh = (lane >> kSh) & (G - 1);
   const float inv_cap = a.cap_log2 > 0.0f ? 1.0f / a.cap_log2 : 0.0f;
   int used = 0;  // stages that this warp has taken in earlier runs
+  // After a wait that gave up (the error word is set) the CTA reads no further keys, but still takes its place in the
+  // merges of this run and of those that follow, so that the counters are zero again for the next call.
+  bool gave_up = false;
 
   while (true) {
     const Run run = sh.run;
     const size_t head_base = (static_cast<size_t>(run.b) * a.Hkv + run.kvh) * a.max_len;
     const T* gk = static_cast<const T*>(a.ck) + head_base * HD;
     const T* gv = static_cast<const T*>(a.cv) + head_base * HD;
-    const int nstages = (run.k1 - run.k0 + C::SK - 1) / C::SK;
+    const int nstages = gave_up ? 0 : (run.k1 - run.k0 + C::SK - 1) / C::SK;
     auto issue = [&](int st_idx, int buf) {
       const int kk0 = run.k0 + st_idx * C::SK;
       const int n = min(C::SK, run.k1 - kk0);
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(NW, G * HD, HD * sizeof
       for (int i = it; i < it + C::NST && warp + i * NW < nstages; ++i)
         warp_wait(smem_u32(&wbar[(used + i) % C::NST]), ((used + i) / C::NST) & 1, nullptr);
     used += it;
-    if (__syncthreads_or(aborted)) return;  // (the error word is set)
+    if (__syncthreads_or(aborted)) gave_up = true;
 
     // ---- the warps' (m, l, o) meet in shared memory (the rings are free now)
     float* ms = reinterpret_cast<float*>(smem);  // [NW][G]

@@ -651,7 +651,7 @@ size_t g4_attn_decode_mods_workspace_size(const g4_layer_params* params, int32_t
  *   - seq_lens is clamped into [0, max_seq_len].
  *   - The workspace, zero-filled once before its first use, is left ready for the next
  *     call of this function, whatever that call's layer, batch and lengths (size it
- *     for the largest).
+ *     for the largest), also by one that g4_take_device_error reports as given up.
  *   - mods->key_begin is [B]: sequence b sees the keys [max(key_begin[b], its window's
  *     first), seq_lens[b]), which is what g4_attn_visible_ranges gives for T = 1.  The
  *     new token is the last key: key_end must be NULL (G4_ERR_INVALID_ARG).
