@@ -653,8 +653,14 @@ size_t g4_attn_decode_mods_workspace_size(const g4_layer_params* params, int32_t
  *     call of this function, whatever that call's layer, batch and lengths (size it
  *     for the largest), also by one that g4_take_device_error reports as given up.
  *   - mods->key_begin is [B]: sequence b sees the keys [max(key_begin[b], its window's
- *     first), seq_lens[b]), which is what g4_attn_visible_ranges gives for T = 1.  The
- *     new token is the last key: key_end must be NULL (G4_ERR_INVALID_ARG).
+ *     first), seq_lens[b]).  The new token is the last key: key_end must be NULL
+ *     (G4_ERR_INVALID_ARG).  This is the interval that g4_attn_visible_ranges gives the
+ *     token for T = 1, but in two cases:
+ *       padding has the interval (0, 0), whose begin alone says "from 0": give such a
+ *       sequence seq_lens[b] = 0 (or a key_begin[b] >= seq_lens[b]);
+ *       a token in a span that begins before its layer's window sees the span's keys
+ *       within the window only.
+ *     g4_attn_prefill_mods with T = 1 takes the whole interval in both.
  *   - A sequence that sees no key gets an output of zeros.
  */
 g4_status g4_attn_decode_mods(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,
