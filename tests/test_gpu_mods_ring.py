@@ -101,3 +101,24 @@ def test_rows_formed_again_on_a_ring(geo, T, rows, start, cap, bias):
     c.v.copy_(c.dv)
     out, _, _ = run(c, [start], T, cap, bias, rows=np.arange(T - 1))
     assert np.isnan(out[0, T - 1]).all()
+
+
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+@pytest.mark.parametrize("geo,T,rows", [((W.SLIDING, 256, 4, 2, 200), 250, 256), ((W.SLIDING, 64, 8, 1, 100), 384, 384),
+                                        ((W.SLIDING, 512, 2, 2, 33), 129, 384), ((W.SLIDING, 128, 3, 3, 128), 1, 128)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (50.0, True)])
+def test_intervals_of_the_callers_own(geo, T, rows, dtype, cap, bias):
+    """Intervals that begin before what the ring still holds, that end past the query or past the last position, that are
+    empty; chunks that leave no room for the layer's window; rings that are not full, and that wrap inside a tile."""
+    starts = np.array([0, 3, 1000, 777, 2 * rows, 12345])
+    B, at = len(starts), starts[:, None] + np.arange(T)[None]
+    rng = np.random.default_rng(T + rows)
+    begin = at - rng.integers(0, 2 * rows, at.shape)
+    end = at + rng.integers(-rows // 2, rows, at.shape)
+    begin[:, T // 3], end[:, T // 3] = -2 ** 31, 2 ** 31 - 1      # all that is held
+    end[:, T // 2:T // 2 + 3] = (starts + T - rows)[:, None]      # nothing that is
+    out, lo, hi = run(ring(geo, B, rows, dtype), starts, T, cap, bias, begin, end)
+    held = (starts + T)[:, None]
+    empty = np.minimum(hi, held) <= np.maximum(lo, np.maximum(held - rows, 0))
+    assert empty.any() and (out[empty] == 0).all()
+    run(ring(geo, B, rows, dtype), starts, T, cap, bias, begin, None)
