@@ -319,13 +319,26 @@ def g4_kv4_attn_prefill(params, pools, layer, q, block_table, max_blocks, q_star
                                      _ptr(workspace), int(workspace_bytes), _stream(stream, q)))
 
 
+_ANY = 1 << 62  # entries of an array that is given by its address, or not at all
+
+
 def score_mods(softcap=0.0, slopes=None, key_begin=None, key_end=None):
-    """What is done to a layer's scores (g4_score_mods).  Holds on to the tensors that it is made of."""
+    """What is done to a layer's scores (g4_score_mods).  Holds on to the tensors that it is made of, which the calls
+    refuse where they are on another device than q or have fewer entries than heads or tokens."""
+    device, entries = None, []
     for t, dtype in ((slopes, "float32"), (key_begin, "int32"), (key_end, "int32")):
-        if t is not None and not isinstance(t, int) and (str(t.dtype) != "torch." + dtype or not t.is_contiguous()):
+        if t is None or isinstance(t, int):
+            entries.append(_ANY)
+            continue
+        if str(t.dtype) != "torch." + dtype or not t.is_contiguous():
             raise ValueError(f"expected a contiguous tensor of {dtype}, got one of {t.dtype}")
+        if device is not None and t.get_device() != device:
+            raise ValueError("slopes, key_begin and key_end are on different devices")
+        device = t.get_device()
+        entries.append(t.numel())
     m = G4ScoreMods(float(softcap), _ptr(slopes), _ptr(key_begin), _ptr(key_end))
     m.tensors = (slopes, key_begin, key_end)
+    m.device, m.entries = device, entries
     return m
 
 
@@ -357,14 +370,25 @@ def g4_kv_append_normrope_axes(params, caches, layer, axes, q_in, k_in, v_in, q_
                                             _ptr(positions), _ptr(rows), B, T, _ptr(q_out), _stream(stream, q_in)))
 
 
-def _mods(mods):
-    return None if mods is None else ctypes.byref(mods)
+def _mods(mods, q, heads, tokens):
+    """The address of a call's mods, whose tensors the kernels can read: of q's device, an entry for every head or token."""
+    if mods is None:
+        return None
+    device = getattr(mods, "device", None)  # (None: no tensors, or a structure of the caller's own)
+    if device is not None:
+        if device < 0 or (q is not None and not isinstance(q, int) and q.get_device() != device):
+            raise ValueError("slopes, key_begin and key_end must be on the device of q")
+        slopes, begin, end = mods.entries
+        if slopes < heads or begin < tokens or end < tokens:
+            raise ValueError(f"slopes need {heads} entries, key_begin and key_end {tokens}")
+    return ctypes.byref(mods)
 
 
 def g4_attn_prefill_mods(params, caches, layer, mods, q, q_start_pos, B, T, out, stream=None):
     """g4_attn_prefill with modified scores (score_mods(), or None)."""
-    _check(lib().g4_attn_prefill_mods(ctypes.byref(params), caches, len(caches), layer, _mods(mods), _ptr(q),
-                                      _ptr(q_start_pos), B, T, _ptr(out), _stream(stream, q)))
+    _check(lib().g4_attn_prefill_mods(ctypes.byref(params), caches, len(caches), layer,
+                                      _mods(mods, q, params.n_heads, B * T), _ptr(q), _ptr(q_start_pos), B, T,
+                                      _ptr(out), _stream(stream, q)))
 
 
 def g4_attn_decode_mods_workspace_size(params, B, max_seq_len):
@@ -374,9 +398,9 @@ def g4_attn_decode_mods_workspace_size(params, B, max_seq_len):
 def g4_attn_decode_mods(params, caches, layer, mods, q, seq_lens, B, max_seq_len, out, workspace=None,
                         workspace_bytes=0, stream=None):
     """g4_attn_decode with modified scores (score_mods(), or None)."""
-    _check(lib().g4_attn_decode_mods(ctypes.byref(params), caches, len(caches), layer, _mods(mods), _ptr(q),
-                                     _ptr(seq_lens), B, max_seq_len, _ptr(out), _ptr(workspace), int(workspace_bytes),
-                                     _stream(stream, q)))
+    _check(lib().g4_attn_decode_mods(ctypes.byref(params), caches, len(caches), layer,
+                                     _mods(mods, q, params.n_heads, B), _ptr(q), _ptr(seq_lens), B, max_seq_len,
+                                     _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream, q)))
 
 
 def g4_last_error():
