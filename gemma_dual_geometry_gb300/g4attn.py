@@ -344,15 +344,19 @@ def score_mods(softcap=0.0, slopes=None, key_begin=None, key_end=None):
 
 def rope_axes(n_axes, axis, head_dim, inv_freq=None):
     """Positions of several axes (g4_rope_axes): ``axis[j]`` turns pair j, ``inv_freq[j]`` is its frequency (None: the
-    layer's).  Both may stop at the last rotated pair."""
+    layer's).  Both may stop at the layer's last rotated pair, no earlier (the call refuses that)."""
     half = head_dim // 2
     for given in (axis, inv_freq):
         if given is not None and len(given) > half:
             raise ValueError(f"{len(given)} pairs in a head of {half}")
+    if not all(0 <= x < 256 and x == int(x) for x in axis):  # (an 8-bit table would take them modulo 256)
+        raise ValueError("axes are whole numbers from 0 on")
     table = (ctypes.c_uint8 * half)(*[int(x) for x in axis])
     freq = None if inv_freq is None else (ctypes.c_float * half)(*[float(x) for x in inv_freq])
-    return G4RopeAxes(int(n_axes), ctypes.cast(table, _P(ctypes.c_uint8)),
+    axes = G4RopeAxes(int(n_axes), ctypes.cast(table, _P(ctypes.c_uint8)),
                       None if freq is None else ctypes.cast(freq, _P(ctypes.c_float)))
+    axes.pairs = len(axis) if inv_freq is None else min(len(axis), len(inv_freq))
+    return axes
 
 
 def g4_attn_visible_ranges(window, q_start_pos, seq_lens, doc_ids, span_ids, max_len, B, T, key_begin, key_end,
@@ -365,6 +369,11 @@ def g4_attn_visible_ranges(window, q_start_pos, seq_lens, doc_ids, span_ids, max
 def g4_kv_append_normrope_axes(params, caches, layer, axes, q_in, k_in, v_in, q_norm_w, k_norm_w, positions, rows, B, T,
                                q_out, stream=None):
     """g4_kv_append_normrope with positions of several axes [n_axes][B][T], apart from the cache's rows [B][T]."""
+    pairs = getattr(axes, "pairs", _ANY)  # (a structure of the caller's own)
+    if pairs < params.head_dim // 2:
+        turned = int(params.head_dim * params.rotary_fraction / 2)
+        if pairs < turned:
+            raise ValueError(f"axes or frequencies of {pairs} pairs, but the layer turns {turned}")
     _check(lib().g4_kv_append_normrope_axes(ctypes.byref(params), caches, len(caches), layer, ctypes.byref(axes),
                                             _ptr(q_in), _ptr(k_in), _ptr(v_in), _ptr(q_norm_w), _ptr(k_norm_w),
                                             _ptr(positions), _ptr(rows), B, T, _ptr(q_out), _stream(stream, q_in)))

@@ -99,3 +99,31 @@ def test_fewer_entries_than_heads_or_tokens(one_device):
         with pytest.raises(ValueError if refused else G.G4Error):
             G.g4_attn_decode_mods(params(), table(), 0, G.score_mods(0.0, None, OnDevice(0, n)), OnDevice(0), FAKE, 4, 100,
                                   FAKE, FAKE, 0, 0)
+
+
+@pytest.mark.parametrize("axis", [[0, 256], [0, -1], [0, 0.5], [0, 300.0], [float("nan")]])
+def test_axes_that_a_byte_does_not_hold(axis):
+    """(256 became axis 0, -1 axis 255.)"""
+    with pytest.raises(ValueError, match="whole numbers"):
+        G.rope_axes(2, axis, 64)
+
+
+def test_tables_that_stop_short_of_the_rotated_pairs():
+    """(The rest were turned by axis 0, or by no angle at all; tables of a smaller head were read past their end.)"""
+    def call(axes, **kw):
+        p = params(**kw)
+        t = G.cache_table(1)
+        G.set_cache(t, 0, FAKE, FAKE, G.G4_FULL, p.head_dim, 2, 100, 4, G.G4_BF16)
+        G.g4_kv_append_normrope_axes(p, t, 0, axes, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, 5, FAKE, 0)
+
+    call(G.rope_axes(2, [0, 1] * 16, 64))
+    call(G.rope_axes(2, [0, 1] * 4, 64), rotary_fraction=0.25)
+    call(G.rope_axes(2, [0, 1] * 4, 64, [0.5] * 8), rotary_fraction=0.25)
+    call(G.rope_axes(2, [0, 1] * 16, 64), head_dim=128, rotary_fraction=0.5)
+    call(G.rope_axes(1, [], 64), rotary_fraction=0.0)
+    for axes, kw in ((G.rope_axes(2, [0, 1] * 15 + [0], 64), {}), (G.rope_axes(2, [0, 1] * 16, 64, [0.5] * 31), {}),
+                     (G.rope_axes(2, [0, 1] * 3, 64), dict(rotary_fraction=0.25)),
+                     (G.rope_axes(2, [0, 1] * 4, 64, [0.5] * 7), dict(rotary_fraction=0.25)),
+                     (G.rope_axes(2, [0, 1] * 16, 64), dict(head_dim=128)), (G.rope_axes(1, [], 64), {})):
+        with pytest.raises(ValueError, match="pairs"):
+            call(axes, **kw)
