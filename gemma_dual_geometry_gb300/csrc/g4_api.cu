@@ -33,6 +33,7 @@ g4_status ok() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool supported_hd(int hd) { return hd == 64 || hd == 128 || hd == 256 || hd == 512; }
 
@@ -1022,8 +1023,7 @@ g4_status check_mods(const g4_layer_params* p, const g4_score_mods* given, g4_sc
   *m = *given;
   if (m->softcap != 0.0f && !(m->softcap >= 0x1.0p-10f && m->softcap <= 0x1.0p10f))
     return fail(G4_ERR_UNSUPPORTED, "softcap %g is neither 0 nor in [2^-10, 2^10]", static_cast<double>(m->softcap));
-  if ((reinterpret_cast<uintptr_t>(m->slopes) | reinterpret_cast<uintptr_t>(m->key_begin) |
-       reinterpret_cast<uintptr_t>(m->key_end)) & 3u)
+  if (!aligned4(m->slopes) || !aligned4(m->key_begin) || !aligned4(m->key_end))
     return fail(G4_ERR_INVALID_ARG, "slopes, key_begin and key_end must be 4-byte aligned");
   if (m->softcap != 0.0f && !isfinite(p->attn_scale * 2.8853900817779268f / m->softcap))
     return fail(G4_ERR_UNSUPPORTED, "attn_scale %g is too large for softcap %g", static_cast<double>(p->attn_scale),
@@ -1045,6 +1045,9 @@ g4_status g4_attn_visible_ranges(int32_t window, const int32_t* q_start_pos, con
   if (static_cast<long long>(B) * T > 0x7fffffffLL) return fail(G4_ERR_INVALID_ARG, "B * T exceeds 2^31 - 1");
   if (q_start_pos == nullptr || seq_lens == nullptr || key_begin == nullptr || key_end == nullptr)
     return fail(G4_ERR_INVALID_ARG, "q_start_pos, seq_lens, key_begin and key_end must be non-NULL");
+  if (!aligned4(q_start_pos) || !aligned4(seq_lens) || !aligned4(doc_ids) || !aligned4(span_ids) || !aligned4(key_begin) ||
+      !aligned4(key_end))
+    return fail(G4_ERR_INVALID_ARG, "positions, lengths, ids and intervals must be 4-byte aligned");
   if (B == 0 || T == 0) return ok();
   g4::RangesArgs a;
   memset(&a, 0, sizeof(a));
@@ -1076,6 +1079,7 @@ g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_
     return fail(G4_ERR_INVALID_ARG, "q_in, q_out, q_norm_w and positions must be non-NULL");
   if (!aligned16(q_in) || !aligned16(q_out) || !aligned16(q_norm_w))
     return fail(G4_ERR_INVALID_ARG, "q_in, q_out and q_norm_w must be 16-byte aligned");
+  if (!aligned4(positions) || !aligned4(rows)) return fail(G4_ERR_INVALID_ARG, "positions and rows must be 4-byte aligned");
   const bool shared = params->kv_share_src >= 0;
   g4::AxesAppendArgs a;
   memset(&a, 0, sizeof(a));
@@ -1139,6 +1143,7 @@ g4_status g4_attn_prefill_mods(const g4_layer_params* params, const g4_kv_cache*
   if (q == nullptr || out == nullptr || q_start_pos == nullptr)
     return fail(G4_ERR_INVALID_ARG, "q, out and q_start_pos must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(G4_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (!aligned4(q_start_pos)) return fail(G4_ERR_INVALID_ARG, "q_start_pos must be 4-byte aligned");
   g4_score_mods m;
   st = check_mods(params, mods, &m);
   if (st != G4_OK) return st;
@@ -1235,6 +1240,7 @@ g4_status g4_attn_decode_mods(const g4_layer_params* params, const g4_kv_cache* 
   if (q == nullptr || out == nullptr || seq_lens == nullptr)
     return fail(G4_ERR_INVALID_ARG, "q, out and seq_lens must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(G4_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (!aligned4(seq_lens)) return fail(G4_ERR_INVALID_ARG, "seq_lens must be 4-byte aligned");
   g4_score_mods m;
   st = check_mods(params, mods, &m);
   if (st != G4_OK) return st;

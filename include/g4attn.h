@@ -544,7 +544,8 @@ g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* 
  *
  * What prompts with images, rows packed of documents, padded batches and models
  * with capped or distance-biased scores need of the calls above.  (The pages have
- * no counterpart: these are calls of this library.)
+ * no counterpart: these are calls of this library.)  Arrays of positions, lengths, ids,
+ * intervals and slopes must be 4-byte aligned (G4_ERR_INVALID_ARG).
  */
 
 /*

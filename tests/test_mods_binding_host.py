@@ -127,3 +127,28 @@ def test_tables_that_stop_short_of_the_rotated_pairs():
                      (G.rope_axes(2, [0, 1] * 16, 64), dict(head_dim=128)), (G.rope_axes(1, [], 64), {})):
         with pytest.raises(ValueError, match="pairs"):
             call(axes, **kw)
+
+
+def refused(fn, *args):
+    with pytest.raises(G.G4Error) as e:
+        fn(*args)
+    return e.value.status == G.G4_ERR_INVALID_ARG and "4-byte aligned" in str(e.value)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_arrays_that_are_not_aligned(off):
+    """Positions, lengths, ids and intervals are 32-bit numbers: at other addresses their loads fault."""
+    odd = FAKE + off
+    for i in (1, 2, 3, 4, 8, 9):
+        args = [0, FAKE, FAKE, FAKE, FAKE, 10, 1, 0, FAKE, FAKE, 0]
+        G.g4_attn_visible_ranges(*args)
+        args[i] = odd
+        assert refused(G.g4_attn_visible_ranges, *args), i
+    axes = G.rope_axes(1, [0] * 32, 64)
+    for i in (9, 10):
+        args = [params(), table(), 0, axes, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1, 0, FAKE, 0]
+        G.g4_kv_append_normrope_axes(*args)
+        args[i] = odd
+        assert refused(G.g4_kv_append_normrope_axes, *args), i
+    assert refused(G.g4_attn_prefill_mods, params(), table(), 0, None, FAKE, odd, 1, 0, FAKE, 0)
+    assert refused(G.g4_attn_decode_mods, params(), table(), 0, None, FAKE, odd, 0, 100, FAKE, FAKE, 1 << 30, 0)
