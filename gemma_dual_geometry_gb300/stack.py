@@ -39,7 +39,7 @@ def _layers(cfg):
 
 class AttnStack:
     def __init__(self, cfg, Lmax, device="cuda", B=None, mods=False):
-        """``mods``: there will be decodes with modified scores (one more workspace)."""
+        """``mods``: there will be decodes with modified scores (one more workspace per layer)."""
         self.cfg = cfg
         self.B = cfg["B"] if B is None else B
         self.Lmax = Lmax
@@ -63,10 +63,11 @@ class AttnStack:
         for l, p in enumerate(self.params):
             nb = G.g4_attn_decode_workspace_size(p, self.B, Lmax)
             self.ws[l] = (torch.zeros(max(nb, 16), dtype=torch.uint8, device=self.device), nb)
-        self.mods_ws = None
-        if mods:  # serves all layers in turn
-            nb = max(G.g4_attn_decode_mods_workspace_size(p, self.B, Lmax) for p in self.params)
-            self.mods_ws = torch.zeros(max(nb, 16), dtype=torch.uint8, device=self.device)
+        self.mods_ws = {}
+        if mods:
+            for l, p in enumerate(self.params):
+                nb = G.g4_attn_decode_mods_workspace_size(p, self.B, Lmax)
+                self.mods_ws[l] = torch.zeros(max(nb, 16), dtype=torch.uint8, device=self.device)
 
     def owns(self, l):
         return self.src[l] < 0
@@ -102,10 +103,11 @@ class AttnStack:
 
     def decode_attn(self, l, q_out, seq_lens, max_seq_len, out, stream=None, mods=None):
         if mods is not None:
-            if self.mods_ws is None:
+            if not self.mods_ws:
                 raise ValueError("the stack was made without mods")
+            ws = self.mods_ws[l]
             G.g4_attn_decode_mods(self.params[l], self.table, l, mods, q_out, seq_lens, self.B, max_seq_len, out,
-                                  self.mods_ws, self.mods_ws.numel(), stream=stream)
+                                  ws, ws.numel(), stream=stream)
             return
         ws, nb = self.ws[l]
         G.g4_attn_decode(self.params[l], self.table, l, q_out, seq_lens, self.B, max_seq_len, out, ws, nb,
