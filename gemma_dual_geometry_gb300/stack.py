@@ -68,6 +68,8 @@ class AttnStack:
             for l, p in enumerate(self.params):
                 nb = G.g4_attn_decode_mods_workspace_size(p, self.B, Lmax)
                 self.mods_ws[l] = torch.zeros(max(nb, 16), dtype=torch.uint8, device=self.device)
+        if self.device.type == "cuda":
+            torch.cuda.current_stream(self.device).synchronize()  # what was queued above is there for any stream
 
     def owns(self, l):
         return self.src[l] < 0
