@@ -79,14 +79,31 @@ class AttnStack:
 
     def visible_ranges(self, layer_type, q_start, seq_lens, doc_ids, span_ids, T, key_begin, key_end, stream=None):
         """The intervals of keys of T tokens per sequence, for all layers of one type (ids are [B][Lmax])."""
-        window = next(g["window"] for g in self.geo if g["layer_type"] == layer_type) if layer_type == W.SLIDING else 0
-        G.g4_attn_visible_ranges(window, q_start, seq_lens, doc_ids, span_ids, self.Lmax, self.B, T, key_begin, key_end,
-                                 stream=stream)
+        windows = [g["window"] for g in self.geo if g["layer_type"] == layer_type]
+        if not windows:
+            raise ValueError(f"the stack has no layers of type {layer_type}")
+        for what, x, n in (("q_start", q_start, 1), ("seq_lens", seq_lens, 1), ("doc_ids", doc_ids, self.Lmax),
+                           ("span_ids", span_ids, self.Lmax), ("key_begin", key_begin, T), ("key_end", key_end, T)):
+            self._check_i32(what, x, self.B * n)
+        G.g4_attn_visible_ranges(windows[0] if layer_type == W.SLIDING else 0, q_start, seq_lens, doc_ids, span_ids,
+                                 self.Lmax, self.B, T, key_begin, key_end, stream=stream)
 
     def append_axes(self, l, axes, q, k, v, qw, kw, positions, rows, T, q_out, stream=None):
         """append() with positions of several axes [n_axes][B][T], apart from the cache's rows [B][T]."""
-        G.g4_kv_append_normrope_axes(self.params[l], self.table, l, axes, q, k, v, qw, kw, positions,
-                                     rows if self.owns(l) else None, self.B, T, q_out, stream=stream)
+        rows = rows if self.owns(l) else None
+        self._check_i32("positions", positions, axes.n_axes * self.B * T)
+        self._check_i32("rows", rows, self.B * T)
+        G.g4_kv_append_normrope_axes(self.params[l], self.table, l, axes, q, k, v, qw, kw, positions, rows, self.B, T,
+                                     q_out, stream=stream)
+
+    @staticmethod
+    def _check_i32(what, x, n):
+        """Whether tensor ``x`` (not an address, nor None) is what the kernels read n 32-bit numbers of."""
+        if x is None or isinstance(x, int):
+            return
+        few = x.numel() < n if x.dim() == 1 else x.numel() != n   # (a flat buffer may be longer)
+        if x.dtype != torch.int32 or few or not x.is_contiguous():
+            raise ValueError(f"{what} must be {n} int32 numbers, contiguous")
 
     def append(self, l, q, k, v, qw, kw, positions, T, q_out, stream=None):
         G.g4_kv_append_normrope(self.params[l], self.table, l, q, k, v, qw, kw, positions, self.B, T, q_out,
