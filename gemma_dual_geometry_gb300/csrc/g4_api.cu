@@ -153,16 +153,6 @@ g4_status cuda_status(cudaError_t e, const char* what) {
   return fail(G4_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-g4_status launch_axes(g4::AxesAppendArgs& a, int dtype, void* stream) {
-  a.err = device_error_ptr();
-  if (a.err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
-  // A warp takes a token's rows as long as that makes 16 warps for each SM, fewer of them otherwise.
-  const int nrows = a.H + (a.k_in != nullptr ? 2 * a.Hkv : 0);
-  const long long rows_each = static_cast<long long>(a.B) * a.T * nrows / (16LL * g4::sm_count());
-  a.rows_per_unit = static_cast<int>(rows_each < 1 ? 1 : rows_each > nrows ? nrows : rows_each);
-  return cuda_status(g4::launch_append_axes(a, dtype, static_cast<cudaStream_t>(stream)), "append launch");
-}
-
 // Scratch for g4_attn_decode_noalloc: a fixed array in device global memory,
 // created when the library's device code is loaded on a GPU and held until the
 // process exits.  Host code must not hand `g_noalloc_scratch` itself to a
@@ -259,16 +249,6 @@ g4_status g4_kv_append_normrope(const g4_layer_params* params, const g4_kv_cache
   const long long ctas = static_cast<long long>(T) * ((B + a.tok_per_cta - 1) / a.tok_per_cta);
   a.rows_per_cta = ctas >= 1024 ? nrows : 4;
   rope_table(params, &a.n_rot, a.inv_freq);
-  if (q_in == q_out && params->dtype == G4_BF16) {
-    // In place: the kernel of one axis, which stores the same bits, keeps a row's inputs until the row is done with; the
-    // one below reads them again where float32 leaves a rounding open.
-    g4::AxesAppendArgs x;
-    memset(&x, 0, sizeof(x));
-    static_cast<g4::AppendArgs&>(x) = a;
-    x.rows = shared ? nullptr : positions;
-    x.n_axes = 1;
-    return launch_axes(x, params->dtype, stream);
-  }
   return cuda_status(g4::launch_append(a, params->dtype, static_cast<cudaStream_t>(stream)), "append launch");
 }
 
@@ -1131,7 +1111,13 @@ g4_status g4_kv_append_normrope_axes(const g4_layer_params* params, const g4_kv_
   a.Hkv = params->n_kv_heads;
   a.hd = params->head_dim;
   a.eps = params->eps;
-  return launch_axes(a, params->dtype, stream);
+  a.err = device_error_ptr();
+  if (a.err == nullptr) return fail(G4_ERR_CUDA, "cannot resolve the device error word");
+  // A warp takes a token's rows as long as that makes 16 warps for each SM, fewer of them otherwise.
+  const int nrows = a.H + (shared ? 0 : 2 * a.Hkv);
+  const long long rows_each = tokens * nrows / (16LL * g4::sm_count());
+  a.rows_per_unit = static_cast<int>(rows_each < 1 ? 1 : rows_each > nrows ? nrows : rows_each);
+  return cuda_status(g4::launch_append_axes(a, params->dtype, static_cast<cudaStream_t>(stream)), "append launch");
 }
 
 g4_status g4_attn_prefill_mods(const g4_layer_params* params, const g4_kv_cache* caches, int32_t n_layers,

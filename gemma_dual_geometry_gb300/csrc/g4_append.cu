@@ -38,6 +38,12 @@
 // same offsets of the upper half (E = head_dim / 64), so each rotate_half
 // pair (j, j + head_dim/2) sits in one lane.  Each warp loads its next row
 // before it computes the current one.
+//
+// q_out = q_in (IN_PLACE, bf16): stages 2 and 3 look at a row's elements again,
+// which stage 1 has overwritten by then, so lanes with open values keep theirs in
+// shared memory: 8 x 2048 tokens of 8 + 2 + 2 rows of 512 119 us (apart 111), of 256 75 (74), of 128 49
+// (52); with the kernel of several axes, 121, 102 and 69.  Four CTAs per SM at 512, since at five the next
+// row's elements are spilled, and so waited for, as soon as they are asked for: 285 us.
 #include <type_traits>
 
 #include "g4_device.cuh"
@@ -77,6 +83,19 @@ __device__ __forceinline__ void load_bits(const __nv_bfloat16* p, HalfBits<__nv_
     h.v[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
     h.v[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_bits(__nv_bfloat16* p, const HalfBits<__nv_bfloat16, E>& h) {
+  if constexpr (E == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(h.v[0], h.v[1], h.v[2], h.v[3]);
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(h.v[0], h.v[1]);
+  } else if constexpr (E == 2) {
+    *reinterpret_cast<uint32_t*>(p) = h.v[0];
+  } else {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(h.v[0]);
   }
 }
 
@@ -263,11 +282,12 @@ __device__ __forceinline__ void kv4_store_row(const __nv_bfloat16* row, uint8_t*
 template <bool KV4>
 using ArgsOf = std::conditional_t<KV4, Kv4AppendArgs, AppendArgs>;
 
-template <typename T, int HD, bool KV4>
-__global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel(const __grid_constant__ ArgsOf<KV4> a) {
+template <typename T, int HD, bool KV4, bool IN_PLACE>
+__global__ void __launch_bounds__(128, HD < 512 ? 8 : IN_PLACE ? 4 : 5) append_normrope_kernel(const __grid_constant__ ArgsOf<KV4> a) {
   constexpr int HALF = HD / 2;
   constexpr int E = HD / 64;
   constexpr bool kBF16 = sizeof(T) == 2;
+  static_assert(!IN_PLACE || (kBF16 && !KV4), "the others look at no element again after its store");
   constexpr float kErrY = normrope_err_y<2 * E>();
   constexpr float kErrAB = normrope_err_pair(kDFTrigErrUnits);
   constexpr float kErrO = normrope_err_out<2 * E>();
@@ -280,6 +300,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
   auto cos_of = [&](int j) -> DF { return s_cos_all[(KV4 ? tab : 0) + j]; };
   auto sin_of = [&](int j) -> DF { return s_sin_all[(KV4 ? tab : 0) + j]; };
   __shared__ __align__(16) T s_row[KV4 ? 4 * kv4_row_at(HD) : 1];  // KV4: a finished row per warp
+  __shared__ __align__(16) T s_raw[IN_PLACE ? 4 * HD : 1];  // IN_PLACE: open lanes' elements of a row per warp
 
   pdl_wait();
   pdl_trigger();
@@ -396,6 +417,14 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
     load_bits<E>(rr.src + HALF + lane * E, hi);
   };
 
+  // Where the elements of a row are looked at again (those of lanes with open values).
+  auto again = [&](const RowRef& rr) -> const T* {
+    if constexpr (IN_PLACE)
+      return s_raw + warp * HD;
+    else
+      return rr.src;
+  };
+
   // Values of row rr that the float32 evaluation could not decide (bit k of
   // need: element k of the lane's 2E, lower half first), evaluated again in
   // double-float from the row's inverse rms rd and stored over the fast ones.
@@ -408,10 +437,10 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       const bool lower = k < E;
       const int j = lane * E + (lower ? k : k - E);
       const int self = lower ? j : HALF + j, other = lower ? HALF + j : j;
-      const float xs = static_cast<float>(rr.src[self]);
+      const float xs = static_cast<float>(again(rr)[self]);
       float v;
       if (rr.rope) {
-        const float xo = static_cast<float>(rr.src[other]);
+        const float xo = static_cast<float>(again(rr)[other]);
         const float ws = rr.w != nullptr ? rr.w[self] : 1.0f, wo = rr.w != nullptr ? rr.w[other] : 1.0f;
         v = normrope_exact_bf16_inl(xs, ws, xo, wo, rd, j < a.n_rot, lower, cos_of(j), sin_of(j));
       } else {
@@ -435,7 +464,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       const bool lower = k < E;
       const int j = lane * E + (lower ? k : k - E);
       const int self = lower ? j : HALF + j, other = lower ? HALF + j : j;
-      const float xs = static_cast<float>(rr.src[self]);
+      const float xs = static_cast<float>(again(rr)[self]);
       DF inner = {xs, 0.0f};
       float mag = fabsf(xs);
       if (rr.rope) {
@@ -443,7 +472,7 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
         inner = two_prod(xs, ws);
         mag = fabsf(inner.h);
         if (j < a.n_rot) {
-          const float xo = static_cast<float>(rr.src[other]);
+          const float xo = static_cast<float>(again(rr)[other]);
           const float wo = rr.w != nullptr ? rr.w[other] : 1.0f;
           const DF po = two_prod(xo, wo);
           mag += fabsf(po.h);
@@ -508,6 +537,12 @@ __global__ void __launch_bounds__(128, HD >= 512 ? 5 : 8) append_normrope_kernel
       if constexpr (kBF16) {
 #pragma unroll
         for (int k = 0; k < 2 * E; ++k) need |= (bf16_decided(o[k], kErrY * fabsf(o[k])) ? 0u : 1u) << k;
+      }
+    }
+    if constexpr (IN_PLACE) {
+      if (need != 0) {
+        store_bits<E>(s_raw + warp * HD + lane * E, lo);
+        store_bits<E>(s_raw + warp * HD + HALF + lane * E, hi);
       }
     }
     store_elems<E>(at(rr, lane * E), o);
@@ -653,15 +688,15 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, cudaStream_t s, const Args& a) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename T, bool KV4>
+template <typename T, bool KV4, bool IN_PLACE>
 cudaError_t launch_t(const ArgsOf<KV4>& a, cudaStream_t s) {
   const int nrows = a.H + (a.k_in ? 2 * a.Hkv : 0);
   dim3 grid(a.T * ((a.B + a.tok_per_cta - 1) / a.tok_per_cta), (nrows + a.rows_per_cta - 1) / a.rows_per_cta);
   switch (a.hd) {
-    case 64: return launch_pdl(append_normrope_kernel<T, 64, KV4>, grid, s, a);
-    case 128: return launch_pdl(append_normrope_kernel<T, 128, KV4>, grid, s, a);
-    case 256: return launch_pdl(append_normrope_kernel<T, 256, KV4>, grid, s, a);
-    case 512: return launch_pdl(append_normrope_kernel<T, 512, KV4>, grid, s, a);
+    case 64: return launch_pdl(append_normrope_kernel<T, 64, KV4, IN_PLACE>, grid, s, a);
+    case 128: return launch_pdl(append_normrope_kernel<T, 128, KV4, IN_PLACE>, grid, s, a);
+    case 256: return launch_pdl(append_normrope_kernel<T, 256, KV4, IN_PLACE>, grid, s, a);
+    case 512: return launch_pdl(append_normrope_kernel<T, 512, KV4, IN_PLACE>, grid, s, a);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -669,9 +704,12 @@ cudaError_t launch_t(const ArgsOf<KV4>& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-  return dtype == 1 ? launch_t<__nv_bfloat16, false>(a, s) : launch_t<float, false>(a, s);
+  if (dtype != 1) return launch_t<float, false, false>(a, s);
+  return a.q_in == a.q_out ? launch_t<__nv_bfloat16, false, true>(a, s) : launch_t<__nv_bfloat16, false, false>(a, s);
 }
 
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) { return launch_t<__nv_bfloat16, true>(a, s); }
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s) {
+  return launch_t<__nv_bfloat16, true, false>(a, s);
+}
 
 }  // namespace g4
