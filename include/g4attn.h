@@ -553,8 +553,11 @@ g4_status g4_kv4_attn_prefill(const g4_layer_params* params, const g4_kv4_pool* 
  * order:
  *   softcap    > 0: s becomes softcap tanh(s / softcap).  0: no cap.  Otherwise 2^-10
  *              .. 2^10 (G4_ERR_UNSUPPORTED outside).
+ *              The bf16 prefill's scores are then off by up to 2^-20 of the cap: its weights
+ *              by 5e-5 at a cap of 50, by 1e-3 (their bf16 rounding: 2e-3) at 2^10.
  *   slopes     [n_heads] float32 device, or NULL: s -= slopes[h] |i - j| (a bias that
- *              falls with distance in either direction).
+ *              falls with distance in either direction).  Magnitudes up to 2^64; a key
+ *              whose score is minus infinity weighs nothing.
  *   key_begin, key_end  int32 device, or NULL: query t of sequence b sees the
  *              positions key_begin[b][t] <= j < key_end[b][t] that the cache holds,
  *              whatever the layer's type and window say; g4_attn_visible_ranges makes
@@ -598,7 +601,10 @@ g4_status g4_attn_visible_ranges(int32_t window, const int32_t* q_start_pos, con
                                  int32_t* key_begin, int32_t* key_end, void* stream);
 
 /*
- * Positions of several axes (time, height and width of images and video).
+ * Positions of several axes (time, height and width of images and video).  Pair j is
+ * dimensions j and j + head_dim / 2 of the whole head, as in g4_kv_append_normrope.  (Models
+ * that give each axis a part of the head with halves of its own need their q and k
+ * projections' rows, and norm weights, in that order: scores do not depend on it.)
  *   n_axes    1 .. 4
  *   axis      HOST [head_dim / 2]: the axis whose position turns pair j (pairs that
  *             rotary_fraction leaves unrotated are not looked at)

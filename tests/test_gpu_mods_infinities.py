@@ -1,4 +1,5 @@
-"""Keys that a query sees whose scores are minus infinity: they weigh nothing, wherever they lie among its keys."""
+"""Keys that a query sees whose scores are minus infinity: they weigh nothing, wherever they lie among its keys.  The
+steepest slopes, next to infinity."""
 
 import numpy as np
 import pytest
@@ -87,3 +88,30 @@ def test_nothing_but_such_keys(geo, dtype):
     one = torch.full((1, geo[2], geo[1]), float("nan"), dtype=q.dtype, device=DEV)
     G.g4_attn_decode_mods(c.params, c.table, 0, None, q[:, 0].contiguous(), i32([n]), 1, n, one, ws, size)
     assert (one == 0).all()
+
+
+@pytest.mark.parametrize("geo", WIDE)
+@pytest.mark.parametrize("dtype", [W.BF16, W.F32])
+@pytest.mark.parametrize("n,T", [(2, 1), (130, 130), (400, 150), (900, 40)])
+def test_the_steepest_slopes(geo, dtype, n, T):
+    """Slopes of 2^64 leave the query's own key, of -2^64 the farthest one that it sees, to the bit."""
+    c = Case(geo, [n], n, dtype, 8)
+    q = unit((1, T, geo[2], geo[1]), 3, dtype).to(DEV)
+    slopes = torch.tensor([2.0 ** 64 * (-1) ** h for h in range(geo[2])], device=DEV)
+    at = torch.arange(n - T, n, device=DEV)
+    group = geo[2] // geo[3]
+
+    def rows(p, h):
+        return c.dv[0, h // group, p]
+
+    out = torch.empty_like(q)
+    first = i32([[t % 7 for t in range(T)]]).clamp(max=n - T)
+    G.g4_attn_prefill_mods(c.params, c.table, 0, G.score_mods(0.0, slopes, first), q, i32([n - T]), 1, T, out)
+    for h in range(geo[2]):
+        assert torch.equal(out[0, :, h], rows(at if h % 2 == 0 else first[0].long(), h))
+    size = G.g4_attn_decode_mods_workspace_size(c.params, 1, n)
+    ws = torch.zeros(max(16, size), dtype=torch.uint8, device=DEV)
+    one = torch.empty((1, geo[2], geo[1]), dtype=q.dtype, device=DEV)
+    G.g4_attn_decode_mods(c.params, c.table, 0, G.score_mods(0.0, slopes), q[:, 0].contiguous(), i32([n]), 1, n, one, ws, size)
+    for h in range(geo[2]):
+        assert torch.equal(one[0, h], rows(n - 1 if h % 2 == 0 else 0, h))
