@@ -17,7 +17,7 @@
 // kv head sharing every row, a cap and a bias applied in the lane that holds a score.
 //
 // Measured (device time; copy rate 6.78 TB/s): head_dim 512, 8 heads on 2, 64 sequences
-// of 1024 to 8192 keys, capped 196 us, 6.2 TB/s (237 with equal splits of the longest length); 4 of
+// of 1024 to 8192 keys, capped 197 us, 6.1 TB/s (237 with equal splits of the longest length); 4 of
 // 131072 with a bias that begin anywhere 250 us, 5.8 TB/s (311); 8 of 4097 36 us, 3.7 TB/s.
 // 64 sequences of 1024 to 8192 keys of 256 101 us, 6.0 TB/s; of 128 63 us, 4.8 TB/s.
 //   What bounds it: at head_dim 512 and 256 with up to 4 heads per kv head, and with one or two at any, the bytes; otherwise

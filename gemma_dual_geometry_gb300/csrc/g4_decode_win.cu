@@ -3,7 +3,7 @@
 // a sequence -- with the splits of a (sequence, kv head) merged inside a
 // thread-block cluster.
 //
-// Semantics as in g4_attn_simt.cu (turbospark-runtime gemma4/attn.rs decode:
+// Semantics as in g4_attn_simt.cuh (turbospark-runtime gemma4/attn.rs decode:
 // keys [kv_start, seq_len) with kv_start = seq_len - sliding_window on sliding
 // layers, score scale attn_scale; query head h reads kv head h / (H / Hkv) as
 // in taconite-embeddinggemma2 `text_attention`), and the FUSED form appends

@@ -16,9 +16,9 @@
 //   * Rows of V outside of the item's keys are zeroed before they meet P, and rows of the output that a NaN or an
 //     infinity reached from keys that other rows of the tile see are formed again (row_again; the check costs 1-2 %).
 // Measured: a row of 8192 packed tokens (sliding, head_dim 256) 51 us, 61 with 8 warps and their exchange per tile;
-// 4 x 2048 tokens with images, capped (head_dim 512) 173 us against 188.
+// 4 x 2048 tokens with images, capped (head_dim 512) 174 us against 188; 2 x 4096 with a bias (head_dim 128) 75 against 87.
 //   Not taken: groups of softmax warps that take key tiles in turn, so that one computes while the other waits.  Two
-// groups of 8, two threads a row: 94 us for 2 x 4096 biased tokens of head_dim 128 against 77; of 4, a thread a row: 104.
+// groups of 8, two threads a row: 94 us for 2 x 4096 biased tokens of head_dim 128 against 75; of 4, a thread a row: 104.
 // A group then has half of the issue slots for its tile, and its next scores wait for its weights and two products.
 //   What bounds it: at head_dim 512 and 256 the tensor pipe and the issue of its instructions (half of the time, per tile
 // 3600 of 5000 cycles at 512), at 128 and below the softmax's chain of load, maximum, exponentials and store

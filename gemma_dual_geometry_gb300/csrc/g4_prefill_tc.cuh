@@ -1,6 +1,6 @@
 // Step a5 in bf16: causal GQA flash attention on the tcgen05 tensor cores.
 //
-// Semantics as in g4_attn_simt.cu (cortiq-engine g4e.rs `attend_all_heads`
+// Semantics as in g4_attn_simt.cuh (cortiq-engine g4e.rs `attend_all_heads`
 // with scale 1.0 and the sliding window, ferrox-models gemma4_engine.rs
 // `causal_gqa_attention[_windowed]`): o_i = sum_j softmax_j(scale q_i.k_j) v_j
 // over keys j <= i (and i - j < window on sliding layers), query head h
@@ -26,7 +26,7 @@
 // after another from a global counter (the producer draws them and passes
 // them on through a 4-entry queue in shared memory), with its barriers, ring and TMEM
 // running on from item to item, so the next item's Q and first K parts load
-// while the current one finishes.  Warp roles (320 threads, MODS 576):
+// while the current one finishes.  Warp roles (320 threads, MODS 608):
 //   warp 0      TMA producer (converged; one elected lane issues): the Q
 //               tile, then K parts (128 keys x 64..256 dims) and V parts
 //               (64..128 keys x DV dims) as 5-D boxes, one request per
@@ -60,6 +60,8 @@
 //               memory once, at the end.  Epilogue: O / l as bf16 into the
 //               ring slots of the item's last V parts (swizzled like the
 //               output tensor map), TMA stores, then those slots are freed.
+//   warp 18     (MODS) the TMA stores of staged outputs, after which it frees their
+//               slots; the softmax warps go on with the next item meanwhile.
 // TMEM columns: S0/P0 [0,128), S1/P1 [128,256), O [256, 256 + DV).
 // The MMAs of one thread execute in issue order, so QK_{j+2} (issued after
 // PV_j) overwrites P_j only after PV_j has read it; no barrier is needed
@@ -150,7 +152,7 @@ struct TcBars {
   uint64_t full[kMaxSlots];
   uint64_t empty[kMaxSlots];
   uint64_t it_full[4];   // work-item queue entry written (by the producer)
-  uint64_t it_empty[4];  // entry read by the MMA issuer and the softmax warps
+  uint64_t it_empty[4];  // entry read by the MMA issuer and the softmax warps (MODS: each of them, and the storing warp)
   int items[4];          // work-item queue: item index, or -1 when none is left
   int kbeg[4], kend[4];  // MODS: the keys that some row of the item sees, [kbeg, kend)
   uint32_t tmem_base;
@@ -310,8 +312,8 @@ __device__ __forceinline__ void cap_scores(float (&s)[N], float cap_in, float ca
 // an infinity (its weight is zero, but zero times that is a NaN in the product): the warp forms the weights of the keys
 // that it does see, several at a time, with the row's own base m, and adds their values up, two columns per lane.
 // inv_l: 1 / row sum.  Done once all columns are NaN: the row sees one itself.
-//   A warp has up to 32 such rows (of 16384 keys 307 ms at head_dim 512, 158 at 128), and the others' bounded waits go on
-// meanwhile, so rows of more than kAgainKeys keys are left as they are.
+//   A warp has up to 32 such rows (of 16384 keys 307 ms at head_dim 512, 158 at 128; with all CTAs at it, up to two items
+// each, 449 and 152), and the others' bounded waits go on meanwhile, so rows of more than kAgainKeys keys are left as they are.
 constexpr int kAgainKeys = 1 << 15;
 
 template <int HD, int NC>

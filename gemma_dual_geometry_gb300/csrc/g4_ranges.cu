@@ -13,7 +13,7 @@
 // what came before and comes after.  A CTA of one tile keeps the ids in registers
 // between the two passes.
 //   Bound by latency: load, reduction, cluster barrier, scan, store: 8 rows of 32768
-// positions (3.7 MB) 5.8 us, one of 1000 3.0 us, one of 131072 12 us.  (CTAs that find what
+// positions (3.7 MB) 5.9 us, one of 1000 3.0 us, one of 131072 12 us.  (CTAs that find what
 // they need of the rest of the row by themselves, looking back for the beginning of their
 // run, took 18, 3.7 and 68 us.)
 #include <cooperative_groups.h>
@@ -26,9 +26,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-// (1024 threads of 4 positions: 6.4 us against 5.8 at 8 rows of 32768; 256 of 16: 6.2)
+// (1024 threads of 4 positions: 6.4 us against 5.9 at 8 rows of 32768; 256 of 16: 6.2)
 constexpr int kRangesThreads = 512;
-constexpr int kRangesMaxTiles = 512;             // tiles per CTA: 2^24 positions over 8 CTAs
+constexpr int kRangesMaxTiles = 512;             // tiles per CTA: 2^24 positions over 8 CTAs, where no cluster of 16 is to be had
 constexpr int kNone = 0x7fffffff;
 
 // One tile's ids of this thread (kPer consecutive positions), and what is a cut.
