@@ -53,22 +53,22 @@ DECODE_EVENT_STEPS = (0, 32, 64, 96, 127)
 # own size.  Each figure carries the kernel's source files and the first 16
 # hex digits of their SHA-256 at the capture: once the sources differ, the
 # counters describe another kernel and the figure is not reported.
-PREFILL_SOURCES = ("g4_prefill_tc.cuh", "g4_device.cuh", "g4_internal.h")
+PREFILL_SOURCES = ("g4_prefill_tc.cuh", "g4_tiles.h", "g4_device.cuh", "g4_internal.h")
 DECODE_SOURCES = ("g4_attn_simt.cuh", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
 WIN_SOURCES = ("g4_decode_win.cu", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
 GEMM_SOURCES = ("g4_gemm_tc.cu", "g4_device.cuh", "g4_internal.h", "g4_normrope.cuh")
 PROFILED_TRAFFIC = {
     # key: (bytes per launch, sources, digest, where it comes from)
-    "prefill_full": (521583616, PREFILL_SOURCES, "b1c7012b5f790912",
+    "prefill_full": (520771584, PREFILL_SOURCES, "482bc6bca9990ef8",
                      "ncu launch list, 42-layer stack at batch 2, layer-5 launches, x 4 sequences"),
-    "decode_full": (134683648, DECODE_SOURCES, "9fdceb0610310b2d",
+    "decode_full": (134682624, DECODE_SOURCES, "8db1fa060a09a021",
                     "ncu launch list, 42-layer stack at batch 2, full-layer decode steps, x 4 sequences"),
-    "decode_sliding": (8710144, WIN_SOURCES, "b2ca64d9b97a6cb4",
+    "decode_sliding": (8710144, WIN_SOURCES, "88a91ce2b8b16a4a",
                        "ncu launch list, 42-layer stack at batch 2, sliding-layer decode steps, x 4 sequences"),
-    "qkv_sliding": (299278336, GEMM_SOURCES, "542a27ab55a5fddd", "ncu launch list, qkv_proj_bf16, sliding layer"),
-    "qkv_full": (513194752, GEMM_SOURCES, "542a27ab55a5fddd", "ncu launch list, qkv_proj_bf16, full layer"),
-    "out_sliding": (378548992, GEMM_SOURCES, "542a27ab55a5fddd", "ncu launch list, out_proj_bf16, sliding layer"),
-    "out_full": (584822528, GEMM_SOURCES, "542a27ab55a5fddd", "ncu launch list, out_proj_bf16, full layer"),
+    "qkv_sliding": (299650048, GEMM_SOURCES, "ec6673447d21cdcf", "ncu launch list, qkv_proj_bf16, sliding layer"),
+    "qkv_full": (513181696, GEMM_SOURCES, "ec6673447d21cdcf", "ncu launch list, qkv_proj_bf16, full layer"),
+    "out_sliding": (378641152, GEMM_SOURCES, "ec6673447d21cdcf", "ncu launch list, out_proj_bf16, sliding layer"),
+    "out_full": (585236224, GEMM_SOURCES, "ec6673447d21cdcf", "ncu launch list, out_proj_bf16, full layer"),
 }
 
 
